@@ -409,6 +409,83 @@ kda_status_t kda_out_norm_gate_proj_noalloc(const void *o, const void *gate_logi
                                             int32_t D_model, float eps, void *y, kda_dtype_t dtype,
                                             void *stream);
 
+/*
+ * kda_qk_norm_fwd - the norm of queries and keys for each head, with the
+ * rotation by position in the same pass (the layer takes q and k normalised;
+ * this makes them so from the raw projections).  Per row x of D channels:
+ *   r = 1 / sqrt(sum x^2 + eps)    (KDA_NORM_L2)
+ *   r = 1 / sqrt(mean x^2 + eps)   (KDA_NORM_RMS)
+ *   y = r x w                      (w: the weight of queries or keys, or 1)
+ * and, with rot_dim = R > 0, the first R channels of y turned in pairs (a, b)
+ * to (a cos t - b sin t, a sin t + b cos t), t = position * inv_freq[j]: pair j
+ * is channels (j, j + R/2), or (2j, 2j + 1) with interleaved != 0.  The angle
+ * is evaluated in fp64 (exact for positions within +-2^31).
+ *   q, k          token (b, s) at b * stride_b + s * stride_s elements, its H
+ *                 heads of D channels contiguous there: views of the rows of a
+ *                 fused projection need no copy.  Strides 0 .. 2^40.
+ *   q_weight, k_weight  (D) fp32, or NULL
+ *   positions     (B, S) int64, read if rot_dim > 0;  inv_freq (rot_dim / 2) fp32
+ *   q_out, k_out  (B, S, H_q, D), (B, S, H_k, D) dtype, contiguous, out
+ * Sums are fp32.  D <= 256, at most 2^31 - 1 tokens.  A row of zeros with eps
+ * = 0 gives NaN, as the formula does.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype, D, number of tokens or heads).
+ */
+typedef enum kda_norm { KDA_NORM_L2 = 0, KDA_NORM_RMS = 1 } kda_norm_t;
+
+typedef struct kda_qk_norm_args {
+    int64_t B, S;
+    int32_t H_q, H_k, D;
+    kda_dtype_t dtype;
+    const void *q;
+    const void *k;
+    int64_t q_stride_b, q_stride_s;
+    int64_t k_stride_b, k_stride_s;
+    kda_norm_t norm;
+    float eps;
+    const float *q_weight;
+    const float *k_weight;
+    const int64_t *positions;
+    const float *inv_freq;
+    int32_t rot_dim;
+    int32_t interleaved;
+    void *q_out;
+    void *k_out;
+    void *stream;
+} kda_qk_norm_args;
+
+kda_status_t kda_qk_norm_fwd(const kda_qk_norm_args *args);
+
+/*
+ * kda_qk_norm_bwd - its gradients, recomputing the norms from q and k:
+ *   fwd           the forward's arguments (q_out and k_out are not read)
+ *   dq_out, dk_out  (B, S, H_q, D), (B, S, H_k, D) grad_dtype, contiguous:
+ *                 dL/d(q_out), dL/d(k_out); grad_dtype is fp32 (as the
+ *                 recurrence's backward passes give it) or dtype
+ *   dq, dk        dtype, contiguous, out
+ *   dq_weight, dk_weight  (D) fp32 out, or NULL to skip: sums over all tokens
+ *                 and heads, added in a fixed order (the same bits every run)
+ *   workspace     256-byte aligned; needed if a weight's gradient is asked for
+ *                 (its size depends on the current device's SM count)
+ * Without tokens the weights' gradients are zero.
+ * Errors: as kda_qk_norm_fwd; WORKSPACE.
+ */
+typedef struct kda_qk_norm_bwd_args {
+    kda_qk_norm_args fwd;
+    kda_dtype_t grad_dtype;
+    const void *dq_out;
+    const void *dk_out;
+    void *dq;
+    void *dk;
+    float *dq_weight;
+    float *dk_weight;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_qk_norm_bwd_args;
+
+kda_status_t kda_qk_norm_bwd_workspace_size(const kda_qk_norm_bwd_args *args, size_t *bytes);
+
+kda_status_t kda_qk_norm_bwd(const kda_qk_norm_bwd_args *args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(_HERE, os.path.basename(os.environ.get("KDA_LIBRARY", "l
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE, KDA_ERR_CUDA, KDA_ERR_TIMEOUT = range(6)
 KDA_F32, KDA_BF16 = 0, 1
 ENGINE_AUTO, ENGINE_SIMT, ENGINE_TC = 0, 1, 2
+NORM_L2, NORM_RMS = 0, 1
 
 _p = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -76,6 +77,30 @@ class DecodeArgs(ctypes.Structure):
     ]
 
 
+class QkNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", _i64), ("S", _i64),
+        ("H_q", _i32), ("H_k", _i32), ("D", _i32),
+        ("dtype", ctypes.c_int),
+        ("q", _p), ("k", _p),
+        ("q_stride_b", _i64), ("q_stride_s", _i64), ("k_stride_b", _i64), ("k_stride_s", _i64),
+        ("norm", ctypes.c_int),
+        ("eps", _f32),
+        ("q_weight", _p), ("k_weight", _p), ("positions", _p), ("inv_freq", _p),
+        ("rot_dim", _i32), ("interleaved", _i32),
+        ("q_out", _p), ("k_out", _p), ("stream", _p),
+    ]
+
+
+class QkNormBwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("fwd", QkNormArgs),
+        ("grad_dtype", ctypes.c_int),
+        ("dq_out", _p), ("dk_out", _p), ("dq", _p), ("dk", _p), ("dq_weight", _p), ("dk_weight", _p),
+        ("workspace", _p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 # name -> (restype, argtypes); every symbol declared in include/kda.h
 SIGNATURES = {
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -98,6 +123,9 @@ SIGNATURES = {
     "kda_dplr_recurrent_fwd": (ctypes.c_int, [ctypes.POINTER(DplrArgs)]),
     "kda_dplr_chunk_workspace_size": (ctypes.c_int, [ctypes.POINTER(DplrArgs), ctypes.POINTER(ctypes.c_size_t)]),
     "kda_dplr_chunk_fwd": (ctypes.c_int, [ctypes.POINTER(DplrArgs), ctypes.c_void_p, ctypes.c_size_t]),
+    "kda_qk_norm_fwd": (ctypes.c_int, [ctypes.POINTER(QkNormArgs)]),
+    "kda_qk_norm_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(QkNormBwdArgs), ctypes.POINTER(ctypes.c_size_t)]),
+    "kda_qk_norm_bwd": (ctypes.c_int, [ctypes.POINTER(QkNormBwdArgs)]),
     "kda_norm_gate": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _f32, _p, ctypes.c_int, _p]),
     "kda_out_proj": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _p, ctypes.c_int, _p]),
     "kda_out_norm_gate_proj_workspace_size": (ctypes.c_int, [_i64, _i32, _i32, ctypes.c_int,

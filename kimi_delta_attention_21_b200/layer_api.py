@@ -1,0 +1,158 @@
+"""Torch-facing binding of the operators around the gated delta rule: argument marshalling only.
+
+The norm of queries and keys with the rotation by position and its gradients.
+Every step runs inside libkda's CUDA kernels, on the current stream of the
+tensors' device (which need not be the current device).
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import QkNormArgs, QkNormBwdArgs, check
+from .api import _DT, _ptr
+
+NORMS = {"l2": _lib.NORM_L2, "rms": _lib.NORM_RMS}
+
+
+def _code(t, name):
+    try:
+        return _DT[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype} (float32 or bfloat16)") from None
+
+
+def _cuda(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t
+
+
+def _need(t, name, device, dtype, shape, contiguous=True):
+    """Checks an optional tensor (None passes) and returns it."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _call(name, device, *args):
+    """Calls an entry point with `device` current, and raises on a status other than KDA_OK."""
+    fn = getattr(_lib.load(), name)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st:
+        check(name, st)
+
+
+def _workspace(entry, device, args, given):
+    """The workspace of a call: the given tensor, or one allocated for the size the query answers."""
+    n = ctypes.c_size_t(0)
+    _call(entry + "_workspace_size", device, ctypes.byref(args), ctypes.byref(n))
+    if not n.value:
+        return None
+    ws = given if given is not None else torch.empty(n.value, dtype=torch.uint8, device=device)
+    _need(ws, "workspace", device, torch.uint8, ws.shape)
+    args.workspace = ws.data_ptr()
+    args.workspace_bytes = ws.numel()
+    return ws
+
+
+def _stream_of(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# ---------------------------------------------------------------- norms of queries and keys
+def _token_strides(t, name):
+    """(B, S, H, D) of a (B, S, H, D) or (S, H, D) tensor and its token strides; heads and channels contiguous."""
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must have shape (B, S, H, D) or (S, H, D) (got {tuple(t.shape)})")
+    H, D = t.shape[-2:]
+    if (D > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != D):
+        raise ValueError(f"{name}: the heads and channels of a token must be contiguous")
+    B, S = (1, t.shape[0]) if t.dim() == 3 else t.shape[:2]
+    return B, S, H, D, (t.stride(0) if t.dim() == 4 and B > 1 else 0), (t.stride(-3) if S > 1 else 0)
+
+
+def _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleaved):
+    dev, dt = _cuda(q, "q").device, q.dtype
+    code = _code(q, "q")
+    B, S, Hq, D, qb, qs = _token_strides(q, "q")
+    _need(k, "k", dev, dt, (*q.shape[:-2], k.shape[-2], D), contiguous=False)
+    Hk, kb, ks = (_token_strides(k, "k")[i] for i in (2, 4, 5))
+    _need(q_weight, "q_weight", dev, torch.float32, (D,))
+    _need(k_weight, "k_weight", dev, torch.float32, (D,))
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    rot = 0
+    if inv_freq is not None:
+        _need(positions, "positions", dev, torch.int64, q.shape[:-2])
+        _need(inv_freq, "inv_freq", dev, torch.float32, (inv_freq.numel(),))
+        rot = 2 * inv_freq.numel()
+    try:
+        kind = NORMS[norm]
+    except KeyError:
+        raise ValueError(f"norm must be one of {sorted(NORMS)} (got {norm!r})") from None
+    return QkNormArgs(B, S, Hq, Hk, D, code, q.data_ptr(), k.data_ptr(), qb, qs, kb, ks, kind, eps, _ptr(q_weight),
+                      _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot, bool(interleaved), None, None,
+                      _stream_of(dev))
+
+
+def qk_norm(q, k, *, norm="l2", eps=1e-6, q_weight=None, k_weight=None, positions=None, inv_freq=None,
+            interleaved=False, out_q=None, out_k=None):
+    """Per-head norm of queries and keys, and the rotation by position, in one pass (kda_qk_norm_fwd).
+
+    q (B,S,H_q,D) and k (B,S,H_k,D), or without B; the heads of a token are
+    contiguous, tokens may be strided (slices of a fused projection's rows).
+    ``norm``: "l2" (x / sqrt(sum x^2 + eps)) or "rms" (mean instead of sum);
+    ``q_weight`` / ``k_weight`` (D,) fp32 or None.  With ``inv_freq`` (R/2,)
+    fp32 and ``positions`` (B,S) int64 the first R channels are rotated by
+    position * inv_freq, in pairs (j, j + R/2) or, ``interleaved``, (2j, 2j + 1).
+    Returns contiguous (q_out, k_out) in the inputs' dtype."""
+    a = _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleaved)
+    dev = q.device
+    if out_q is None:
+        out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _need(out_q, "out_q", dev, q.dtype, q.shape)
+    if out_k is None:
+        out_k = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    else:
+        _need(out_k, "out_k", dev, q.dtype, k.shape)
+    a.q_out, a.k_out = out_q.data_ptr(), out_k.data_ptr()
+    _call("kda_qk_norm_fwd", dev, ctypes.byref(a))
+    return out_q, out_k
+
+
+def qk_norm_bwd(q, k, dq_out, dk_out, *, norm="l2", eps=1e-6, q_weight=None, k_weight=None, positions=None,
+                inv_freq=None, interleaved=False, workspace=None):
+    """Gradients of ``qk_norm`` (kda_qk_norm_bwd): the forward's arguments, and dq_out, dk_out = dL/d(outputs), both
+    fp32 or both in the inputs' dtype.  Returns a dict of dq, dk (inputs' dtype, contiguous) and dq_weight, dk_weight
+    (fp32, None without that weight)."""
+    f = _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleaved)
+    dev = q.device
+    gt = _cuda(dq_out, "dq_out").dtype
+    if gt not in (torch.float32, q.dtype):
+        raise TypeError(f"dq_out must be float32 or {q.dtype} (got {gt})")
+    _need(dq_out, "dq_out", dev, gt, q.shape)
+    _need(dk_out, "dk_out", dev, gt, k.shape)
+    out = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev), "dk": torch.empty(k.shape, dtype=q.dtype, device=dev),
+           "dq_weight": None if q_weight is None else torch.empty_like(q_weight),
+           "dk_weight": None if k_weight is None else torch.empty_like(k_weight)}
+    a = QkNormBwdArgs(f, _DT[gt], _ptr(dq_out), _ptr(dk_out), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dq_weight"]),
+                      _ptr(out["dk_weight"]), None, 0)
+    ws = _workspace("kda_qk_norm_bwd", dev, a, workspace)  # noqa: F841 (alive until the call has been queued)
+    _call("kda_qk_norm_bwd", dev, ctypes.byref(a))
+    return out

@@ -1,0 +1,84 @@
+"""Host side of the operators around the gated delta rule: their structs match
+the header, and bad calls are refused before anything is launched (fake device
+addresses, never dereferenced)."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+from kimi_delta_attention_21_b200 import _lib as L
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "kda.h")
+G = 1 << 30
+P = [(1 << 40) + i * G for i in range(24)]  # one GiB apart
+
+STRUCTS = {"kda_qk_norm_args": L.QkNormArgs, "kda_qk_norm_bwd_args": L.QkNormBwdArgs}
+
+
+def test_struct_layouts_match_the_header(tmp_path):
+    lines = ['#include <stdio.h>', '#include <stddef.h>', f'#include "{HEADER}"', "int main(void){"]
+    for c, S in STRUCTS.items():
+        lines.append(f'printf("{c} sizeof %zu\\n", sizeof({c}));')
+        lines += [f'printf("{c} {f} %zu\\n", offsetof({c}, {f}));' for f, _ in S._fields_]
+    prog, exe = tmp_path / "layout.c", tmp_path / "layout"
+    prog.write_text("\n".join(lines + ["return 0;}"]))
+    subprocess.check_call(["gcc", "-std=c11", "-o", str(exe), str(prog)])
+    for line in subprocess.check_output([str(exe)], text=True).splitlines():
+        c, f, n = line.split()
+        S = STRUCTS[c]
+        assert int(n) == (ctypes.sizeof(S) if f == "sizeof" else getattr(S, f).offset), (c, f)
+
+
+def refused(fn, args, status, *more):
+    lib = L.load()
+    n0 = lib.kda_launch_count()
+    assert getattr(lib, fn)(ctypes.byref(args), *more) == status, lib.kda_last_error().decode()
+    assert lib.kda_last_error().decode() != ""
+    assert lib.kda_launch_count() == n0
+
+
+def qk(**kw):
+    a = dict(B=2, S=8, H_q=4, H_k=2, D=64, dtype=L.KDA_BF16, q=P[0], k=P[1], q_stride_b=2048, q_stride_s=256,
+             k_stride_b=1024, k_stride_s=128, norm=L.NORM_RMS, eps=1e-6, positions=P[4], inv_freq=P[5], rot_dim=64,
+             q_out=P[2], k_out=P[3])
+    a.update(kw)
+    return L.QkNormArgs(**a)
+
+
+@pytest.mark.parametrize("mut,status", [
+    (dict(dtype=5), L.KDA_ERR_UNSUPPORTED), (dict(B=-1), L.KDA_ERR_INVALID_ARG), (dict(H_k=0), L.KDA_ERR_INVALID_ARG),
+    (dict(D=257), L.KDA_ERR_UNSUPPORTED), (dict(rot_dim=63), L.KDA_ERR_INVALID_ARG),
+    (dict(rot_dim=66), L.KDA_ERR_INVALID_ARG), (dict(norm=2), L.KDA_ERR_INVALID_ARG),
+    (dict(eps=float("nan")), L.KDA_ERR_INVALID_ARG), (dict(q=None), L.KDA_ERR_INVALID_ARG),
+    (dict(k=P[1] + 1), L.KDA_ERR_INVALID_ARG), (dict(positions=None), L.KDA_ERR_INVALID_ARG),
+    (dict(inv_freq=None), L.KDA_ERR_INVALID_ARG), (dict(q_out=None), L.KDA_ERR_INVALID_ARG),
+    (dict(q_out=P[1] + 64), L.KDA_ERR_INVALID_ARG), (dict(k_out=P[2] + 128), L.KDA_ERR_INVALID_ARG),
+    (dict(q_stride_s=-1), L.KDA_ERR_INVALID_ARG), (dict(k_stride_b=1 << 41), L.KDA_ERR_INVALID_ARG),
+    (dict(B=1 << 20, S=1 << 20), L.KDA_ERR_UNSUPPORTED), (dict(H_q=1 << 20), L.KDA_ERR_UNSUPPORTED),
+    (dict(q_weight=P[6] + 2), L.KDA_ERR_INVALID_ARG),
+])
+def test_qk_norm_refusals(mut, status):
+    refused("kda_qk_norm_fwd", qk(**mut), status)
+
+
+def test_qk_norm_bwd_refusals():
+    def args(fwd=None, **kw):
+        a = dict(fwd=fwd or qk(), grad_dtype=L.KDA_F32, dq_out=P[7], dk_out=P[8], dq=P[9], dk=P[10], dq_weight=P[11],
+                 workspace=P[12], workspace_bytes=1 << 28)
+        a.update(kw)
+        return L.QkNormBwdArgs(**a)
+
+    bad, unsup = L.KDA_ERR_INVALID_ARG, L.KDA_ERR_UNSUPPORTED
+    refused("kda_qk_norm_bwd", args(grad_dtype=3), unsup)
+    refused("kda_qk_norm_bwd", args(fwd=qk(dtype=L.KDA_F32), grad_dtype=L.KDA_BF16), unsup)
+    refused("kda_qk_norm_bwd", args(workspace=None), L.KDA_ERR_WORKSPACE)
+    refused("kda_qk_norm_bwd", args(workspace_bytes=64), L.KDA_ERR_WORKSPACE)
+    refused("kda_qk_norm_bwd", args(dq_out=None), bad)
+    refused("kda_qk_norm_bwd", args(dq=P[0]), bad)              # over an input
+    refused("kda_qk_norm_bwd", args(dk=P[9] + 64), bad)         # over another output
+    refused("kda_qk_norm_bwd", args(workspace=P[11]), bad)      # over a weight's gradient
+    n = ctypes.c_size_t(7)
+    a = args(dq_weight=None)
+    assert L.load().kda_qk_norm_bwd_workspace_size(ctypes.byref(a), ctypes.byref(n)) == L.KDA_OK and n.value == 0
