@@ -486,6 +486,49 @@ kda_status_t kda_qk_norm_bwd_workspace_size(const kda_qk_norm_bwd_args *args, si
 
 kda_status_t kda_qk_norm_bwd(const kda_qk_norm_bwd_args *args);
 
+/*
+ * kda_gdn_decode_step - the recurrent form of the gated delta rule (one scalar
+ * decay per token and head, as kda_gdn_chunk_fwd): T new tokens of each of B
+ * sequences, token by token, exact fp32, the states advanced IN PLACE.  T = 1
+ * is a decode step; more tokens are drafted ones or short prompts.  The state
+ * is read and written once per call, whatever T is.
+ *   q, k          (B, T, H, D_k)  dtype;   v (B, T, H, D_v)  dtype
+ *   z             (B, T, H)  dtype decay logits, alpha = exp(g_min * sigmoid(z)),
+ *                 or log_decay (B, T, H) fp32 (clamped to [g_min, 0]) instead
+ *   beta          (B, T, H)  dtype
+ *   state         (num_slots, H, D_k, D_v) fp32, read and written
+ *   slots         (B) int32: the state of each sequence, or NULL for 0 .. B - 1.
+ *                 A negative slot is a padded row: nothing of it is read or
+ *                 written, its rows of o stay as they were.  A slot >= num_slots,
+ *                 or one that an earlier sequence of the call has, is treated the
+ *                 same way and sets *dev_status to KDA_ERR_INVALID_ARG.
+ *   gate_logits   (B, T, H, D_v)  dtype or NULL (as in kda_chunk_fwd), eps
+ *   o             (B, T, H, D_v)  dtype, out
+ *   dev_status    device int32 that the caller zeroes, or NULL
+ * Errors: INVALID_ARG, UNSUPPORTED (D_k or D_v > 128, B*H > 2^31 - 1).
+ */
+typedef struct kda_gdn_decode_args {
+    int64_t B, num_slots;
+    int32_t T, H, D_k, D_v;
+    kda_dtype_t dtype;
+    const void *q;
+    const void *k;
+    const void *v;
+    const void *z;
+    const float *log_decay;
+    float g_min;
+    const void *beta;
+    float *state;
+    const int32_t *slots;
+    const void *gate_logits;
+    float eps;
+    void *o;
+    int32_t *dev_status;
+    void *stream;
+} kda_gdn_decode_args;
+
+kda_status_t kda_gdn_decode_step(const kda_gdn_decode_args *args);
+
 #ifdef __cplusplus
 }
 #endif

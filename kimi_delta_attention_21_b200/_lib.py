@@ -101,6 +101,19 @@ class QkNormBwdArgs(ctypes.Structure):
     ]
 
 
+class GdnDecodeArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", _i64), ("num_slots", _i64),
+        ("T", _i32), ("H", _i32), ("D_k", _i32), ("D_v", _i32),
+        ("dtype", ctypes.c_int),
+        ("q", _p), ("k", _p), ("v", _p), ("z", _p), ("log_decay", _p),
+        ("g_min", _f32),
+        ("beta", _p), ("state", _p), ("slots", _p), ("gate_logits", _p),
+        ("eps", _f32),
+        ("o", _p), ("dev_status", _p), ("stream", _p),
+    ]
+
+
 # name -> (restype, argtypes); every symbol declared in include/kda.h
 SIGNATURES = {
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -126,6 +139,7 @@ SIGNATURES = {
     "kda_qk_norm_fwd": (ctypes.c_int, [ctypes.POINTER(QkNormArgs)]),
     "kda_qk_norm_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(QkNormBwdArgs), ctypes.POINTER(ctypes.c_size_t)]),
     "kda_qk_norm_bwd": (ctypes.c_int, [ctypes.POINTER(QkNormBwdArgs)]),
+    "kda_gdn_decode_step": (ctypes.c_int, [ctypes.POINTER(GdnDecodeArgs)]),
     "kda_norm_gate": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _f32, _p, ctypes.c_int, _p]),
     "kda_out_proj": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _p, ctypes.c_int, _p]),
     "kda_out_norm_gate_proj_workspace_size": (ctypes.c_int, [_i64, _i32, _i32, ctypes.c_int,

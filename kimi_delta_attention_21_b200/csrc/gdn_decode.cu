@@ -1,0 +1,226 @@
+// The gated delta rule token by token (one scalar decay per token and head), from a pool of states
+// advanced in place:
+//   S' = alpha S,  p = S'^T k,  r = beta (v - p),  S = S' + k r^T,  o~ = S^T q = S'^T q + (q . k) r
+// for T new tokens of each sequence (T = 1: a decode step; T > 1: drafted tokens, or a short prompt).
+//
+// The state is the whole cost: 2 * D_k * D_v * 4 bytes per (sequence, head) and call, whatever T is.  It
+// is read once into registers, stays there over the T tokens, and is written once.  A CTA of 8 warps per
+// (sequence, head): lane l of warp w owns the key rows w, w + 8, ... and four value columns, so that a
+// warp reads whole rows; the sums over key rows are partial sums of 8 warps joined in shared memory, one
+// barrier each (the buffers alternate, so the next token's sums need no second one).
+#include "host_check.cuh"
+#include "kda_internal.cuh"
+#include "sm100_ptx.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int GD_NW = 8, GD_RPW = 16, GD_MAXD = 128;
+
+struct GdArgs {
+    int64_t slots_n;
+    int T, H, Dk, Dv;
+    const void *q, *k, *v, *z, *beta, *gate;
+    const float *log_decay;
+    float g_min, eps;
+    float *state;
+    const int32_t *slots;
+    void *o;
+    int32_t *status;
+    size_t state_bytes;
+    unsigned int *bounds;
+};
+
+// FULL: D_k = D_v = 128 with a 16-byte aligned state; lane l owns columns 4l .. 4l + 3.  Otherwise the
+// columns l, l + 32, l + 64, l + 96 within D_v and the rows within D_k.
+template <typename T, bool FULL>
+__global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constant__ GdArgs p) {
+    sm100::pdl_trigger();
+    sm100::pdl_wait();
+    __shared__ float s_q[2][GD_MAXD], s_k[2][GD_MAXD];
+    __shared__ __align__(16) float s_red[2][2][GD_NW][GD_MAXD];
+    const int Dk = FULL ? GD_MAXD : p.Dk, Dv = FULL ? GD_MAXD : p.Dv;
+    const int tid = threadIdx.x, w = tid >> 5, l = tid & 31;
+    const int64_t b = blockIdx.x / p.H;
+    const int h = (int)(blockIdx.x - b * p.H);
+    const int64_t slot = p.slots ? p.slots[b] : b;
+    if (slot < 0) return;  // a padded row of the batch
+    if (slot >= p.slots_n) {
+        if (tid == 0 && p.status) *p.status = KDA_ERR_INVALID_ARG;
+        return;
+    }
+    float *S = p.state + (slot * p.H + h) * (int64_t)Dk * Dv;
+    auto col = [&](int j) { return FULL ? 4 * l + j : l + 32 * j; };
+    float s[GD_RPW][4];
+#pragma unroll
+    for (int i = 0; i < GD_RPW; ++i) {
+        const int c = w + GD_NW * i;
+        if (FULL) {
+            const float4 t = __ldcs(reinterpret_cast<const float4 *>(S + c * GD_MAXD + 4 * l));
+            s[i][0] = t.x; s[i][1] = t.y; s[i][2] = t.z; s[i][3] = t.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = (c < Dk && col(j) < Dv) ? S[c * Dv + col(j)] : 0.f;
+        }
+    }
+    if (p.slots) {  // a slot that an earlier sequence of the batch has: two CTAs would race on its state
+        bool twice = false;
+        for (int64_t e = tid; e < b; e += 256) twice |= p.slots[e] == (int32_t)slot;
+        if (__syncthreads_or(twice)) {
+            if (tid == 0 && p.status) *p.status = KDA_ERR_INVALID_ARG;
+            return;
+        }
+    }
+    const int64_t tok0 = b * p.T * p.H + h;  // (token, head) index of token 0; p.H further for each token
+    auto fetch = [&](int t) {                // this thread's element of token t's q (threads < 128) or k
+        const int c = tid & 127;
+        const T *src = (const T *)(tid < 128 ? p.q : p.k);
+        return c < Dk ? load_elem(src, (tok0 + (int64_t)t * p.H) * Dk + c) : 0.f;
+    };
+    float pre = fetch(0);
+    for (int t = 0; t < p.T; ++t) {
+        const int64_t th = tok0 + (int64_t)t * p.H;
+        const int buf = t & 1;
+        (tid < 128 ? s_q : s_k)[buf][tid & 127] = pre;
+        float v[4], gt[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool in = FULL || col(j) < Dv;
+            v[j] = in ? load_elem((const T *)p.v, th * Dv + col(j)) : 0.f;
+            gt[j] = (in && p.gate) ? load_elem((const T *)p.gate, th * Dv + col(j)) : 0.f;
+        }
+        const float bt = load_elem((const T *)p.beta, th);
+        const float g = p.log_decay ? clamp_log_decay(p.log_decay[th], p.g_min)
+                                    : log_alpha_of(load_elem((const T *)p.z, th), p.g_min);
+        const float a = expf(g);
+        if (t + 1 < p.T) pre = fetch(t + 1);
+        __syncthreads();  // q and k of token t
+        float qk = 0.f, pp[4] = {0.f, 0.f, 0.f, 0.f}, qs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) qk = fmaf(s_q[buf][l + 32 * j], s_k[buf][l + 32 * j], qk);
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) qk += __shfl_xor_sync(0xffffffffu, qk, m);
+#pragma unroll
+        for (int i = 0; i < GD_RPW; ++i) {
+            const int c = w + GD_NW * i;
+            const float kc = s_k[buf][c], qc = s_q[buf][c];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] *= a;
+                pp[j] = fmaf(kc, s[i][j], pp[j]);
+                qs[j] = fmaf(qc, s[i][j], qs[j]);
+            }
+        }
+        *reinterpret_cast<float4 *>(&s_red[buf][0][w][4 * l]) = make_float4(pp[0], pp[1], pp[2], pp[3]);
+        *reinterpret_cast<float4 *>(&s_red[buf][1][w][4 * l]) = make_float4(qs[0], qs[1], qs[2], qs[3]);
+        __syncthreads();  // the partial sums
+        float r[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < GD_NW; ++u) {
+            const float4 x = *reinterpret_cast<const float4 *>(&s_red[buf][0][u][4 * l]);
+            const float4 y = *reinterpret_cast<const float4 *>(&s_red[buf][1][u][4 * l]);
+            r[0] += x.x; r[1] += x.y; r[2] += x.z; r[3] += x.w;
+            o[0] += y.x; o[1] += y.y; o[2] += y.z; o[3] += y.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            r[j] = bt * (v[j] - r[j]);
+            o[j] = fmaf(qk, r[j], o[j]);
+        }
+#pragma unroll
+        for (int i = 0; i < GD_RPW; ++i) {
+            const float kc = s_k[buf][w + GD_NW * i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = fmaf(kc, r[j], s[i][j]);
+        }
+        if (w == (t & 7)) {
+            if (p.gate) {
+                float ss = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) ss = (FULL || col(j) < Dv) ? fmaf(o[j], o[j], ss) : ss;
+#pragma unroll
+                for (int m = 16; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+                const float inv = 1.0f / sqrtf(ss / (float)Dv + p.eps);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] *= inv * sigmoid_precise(gt[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (FULL || col(j) < Dv) store_elem((T *)p.o, th * Dv + col(j), o[j]);
+        }
+    }
+    if (!in_bounds(S, (size_t)Dk * Dv * 4, p.state, p.state_bytes, p.bounds)) return;
+#pragma unroll
+    for (int i = 0; i < GD_RPW; ++i) {
+        const int c = w + GD_NW * i;
+        if (FULL) {
+            __stcs(reinterpret_cast<float4 *>(S + c * GD_MAXD + 4 * l), make_float4(s[i][0], s[i][1], s[i][2], s[i][3]));
+        } else if (c < Dk) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (col(j) < Dv) S[c * Dv + col(j)] = s[i][j];
+        }
+    }
+}
+
+template <typename T>
+cudaError_t gd_launch(const kda_gdn_decode_args &a, const GdArgs &p, cudaStream_t st) {
+    const dim3 grid((unsigned)(a.B * a.H));
+    if (a.D_k == GD_MAXD && a.D_v == GD_MAXD && aligned_to(a.state, 16))
+        return launch_pdl(gdn_decode_kernel<T, true>, grid, dim3(256), 0, st, p);
+    return launch_pdl(gdn_decode_kernel<T, false>, grid, dim3(256), 0, st, p);
+}
+
+}  // namespace
+
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" kda_status_t kda_gdn_decode_step(const kda_gdn_decode_args *a) {
+    clear_error();
+    if (!a) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
+    KDA_TRY(check_dtype(a->dtype));
+    KDA_TRY(check_gmin(a->g_min));
+    if (a->B < 0 || a->T < 0 || a->H < 1 || a->D_k < 1 || a->D_v < 1 || a->num_slots < 0)
+        return fail(KDA_ERR_INVALID_ARG, "bad sizes B=%lld T=%d H=%d D_k=%d D_v=%d num_slots=%lld", (long long)a->B, a->T,
+                    a->H, a->D_k, a->D_v, (long long)a->num_slots);
+    if (a->D_k > GD_MAXD || a->D_v > GD_MAXD) return fail(KDA_ERR_UNSUPPORTED, "D_k and D_v must be <= 128");
+    if (a->B > 0x7fffffffLL / a->H) return fail(KDA_ERR_UNSUPPORTED, "B*H exceeds 2^31 - 1");
+    if (a->num_slots > ((int64_t)1 << 40) / a->H) return fail(KDA_ERR_UNSUPPORTED, "num_slots too large");
+    if (a->B == 0 || a->T == 0) return KDA_OK;
+    if (!a->slots && a->num_slots < a->B)
+        return fail(KDA_ERR_INVALID_ARG, "without slots the pool needs a state for each of the %lld sequences (has %lld)",
+                    (long long)a->B, (long long)a->num_slots);
+    if (a->gate_logits && !(isfinite(a->eps) && a->eps >= 0.0f))
+        return fail(KDA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    const size_t es = esize(a->dtype), n = (size_t)a->B * a->T * a->H;
+    KDA_REQ_PTR(a->q, "q", es);
+    KDA_REQ_PTR(a->k, "k", es);
+    KDA_REQ_PTR(a->v, "v", es);
+    KDA_REQ_PTR(a->beta, "beta", es);
+    KDA_REQ_PTR(a->o, "o", es);
+    if (!a->log_decay) KDA_REQ_PTR(a->z, "z (or log_decay)", es);
+    KDA_OPT_PTR(a->log_decay, "log_decay", 4);
+    KDA_OPT_PTR(a->gate_logits, "gate_logits", es);
+    KDA_OPT_PTR(a->slots, "slots", 4);
+    KDA_OPT_PTR(a->dev_status, "dev_status", 4);
+    if (a->num_slots > 0) KDA_REQ_PTR(a->state, "state", 4);
+    const size_t ns = (size_t)a->num_slots * a->H * a->D_k * a->D_v * 4, nv = n * a->D_v * es;
+    const Buf ins[] = {{a->q, n * a->D_k * es, "q"}, {a->k, n * a->D_k * es, "k"}, {a->v, nv, "v"},
+                       {a->log_decay ? nullptr : a->z, n * es, "z"}, {a->log_decay, n * 4, "log_decay"},
+                       {a->beta, n * es, "beta"}, {a->gate_logits, nv, "gate_logits"},
+                       {a->slots, (size_t)a->B * 4, "slots"}, {a->dev_status, 4, "dev_status"}};
+    const int nin = (int)(sizeof(ins) / sizeof(ins[0]));
+    KDA_TRY(check_no_overlap(Buf{a->state, ns, "state"}, ins, nin));
+    KDA_TRY(check_no_overlap(Buf{a->o, nv, "o"}, ins, nin));
+    if (overlap(a->o, nv, a->state, ns)) return fail(KDA_ERR_INVALID_ARG, "o overlaps state");
+    const GdArgs p = {a->num_slots, a->T,     a->H,     a->D_k,       a->D_v, a->q,      a->k,
+                      a->v,         a->z,     a->beta,  a->gate_logits, a->log_decay, a->g_min, a->eps,
+                      a->state,     a->slots, a->o,     a->dev_status, ns,     device_bounds_counter()};
+    cudaStream_t st = (cudaStream_t)a->stream;
+    const cudaError_t e = a->dtype == KDA_F32 ? gd_launch<float>(*a, p, st) : gd_launch<__nv_bfloat16>(*a, p, st);
+    if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "gdn_decode_kernel: %s", cudaGetErrorString(e));
+    return check_launch("gdn_decode_kernel");
+}

@@ -1,6 +1,7 @@
 """Torch-facing binding of the operators around the gated delta rule: argument marshalling only.
 
-The norm of queries and keys with the rotation by position and its gradients.
+The norm of queries and keys with the rotation by position and its gradients;
+the gated delta rule token by token.
 Every step runs inside libkda's CUDA kernels, on the current stream of the
 tensors' device (which need not be the current device).
 """
@@ -11,7 +12,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import QkNormArgs, QkNormBwdArgs, check
+from ._lib import GdnDecodeArgs, QkNormArgs, QkNormBwdArgs, check
 from .api import _DT, _ptr
 
 NORMS = {"l2": _lib.NORM_L2, "rms": _lib.NORM_RMS}
@@ -155,4 +156,46 @@ def qk_norm_bwd(q, k, dq_out, dk_out, *, norm="l2", eps=1e-6, q_weight=None, k_w
                       _ptr(out["dk_weight"]), None, 0)
     ws = _workspace("kda_qk_norm_bwd", dev, a, workspace)  # noqa: F841 (alive until the call has been queued)
     _call("kda_qk_norm_bwd", dev, ctypes.byref(a))
+    return out
+
+
+# ---------------------------------------------------------------- the gated delta rule
+def gdn_decode_step(q, k, v, beta, state, *, z=None, log_decay=None, g_min=-5.0, gate_logits=None, eps=1e-6,
+                    slots=None, out=None, dev_status=None):
+    """The gated delta rule (one scalar decay per token and head) token by token (kda_gdn_decode_step).
+
+    One token for B sequences: q, k (B,H,D_k); v, gate_logits (B,H,D_v); beta and
+    z or log_decay (B,H).  T tokens each: the same with (B,T,H,...).  ``state``
+    (num_slots,H,D_k,D_v) fp32 is advanced IN PLACE; ``slots`` (B,) int32 picks
+    each sequence's state (None: the first B).  A negative slot is a padded row,
+    whose output rows stay as they were (zeros when ``out`` is not given); a slot
+    outside the pool, or given twice, is skipped like it and sets ``dev_status``
+    (a zeroed int32 tensor).  Returns o in the input dtype."""
+    dev, dt = _cuda(q, "q").device, q.dtype
+    code = _code(q, "q")
+    if q.dim() not in (3, 4):
+        raise ValueError(f"q must have shape (B, H, D_k) or (B, T, H, D_k) (got {tuple(q.shape)})")
+    lead = q.shape[:-1]
+    B, T, H = (lead[0], 1, lead[1]) if q.dim() == 3 else lead
+    Dk, Dv = q.shape[-1], v.shape[-1]
+    _need(q, "q", dev, dt, q.shape)
+    _need(k, "k", dev, dt, q.shape)
+    _need(v, "v", dev, dt, (*lead, Dv))
+    if beta.dim() == len(lead) + 1 and beta.shape[-1] == 1:
+        beta = beta.view(lead)
+    _need(beta, "beta", dev, dt, lead)
+    _need(z, "z", dev, dt, lead)
+    _need(log_decay, "log_decay", dev, torch.float32, lead)
+    _need(gate_logits, "gate_logits", dev, dt, (*lead, Dv))
+    _need(slots, "slots", dev, torch.int32, (B,))
+    _need(state, "state", dev, torch.float32, (state.shape[0], H, Dk, Dv))
+    _need(dev_status, "dev_status", dev, torch.int32, dev_status.shape if dev_status is not None else ())
+    if out is None:
+        out = (torch.empty if slots is None else torch.zeros)((*lead, Dv), dtype=dt, device=dev)
+    else:
+        _need(out, "out", dev, dt, (*lead, Dv))
+    a = GdnDecodeArgs(B, state.shape[0], T, H, Dk, Dv, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(z),
+                      _ptr(log_decay), g_min, beta.data_ptr(), state.data_ptr(), _ptr(slots), _ptr(gate_logits), eps,
+                      out.data_ptr(), _ptr(dev_status), _stream_of(dev))
+    _call("kda_gdn_decode_step", dev, ctypes.byref(a))
     return out

@@ -14,7 +14,8 @@ HEADER = os.path.join(ROOT, "include", "kda.h")
 G = 1 << 30
 P = [(1 << 40) + i * G for i in range(24)]  # one GiB apart
 
-STRUCTS = {"kda_qk_norm_args": L.QkNormArgs, "kda_qk_norm_bwd_args": L.QkNormBwdArgs}
+STRUCTS = {"kda_qk_norm_args": L.QkNormArgs, "kda_qk_norm_bwd_args": L.QkNormBwdArgs,
+           "kda_gdn_decode_args": L.GdnDecodeArgs}
 
 
 def test_struct_layouts_match_the_header(tmp_path):
@@ -82,3 +83,20 @@ def test_qk_norm_bwd_refusals():
     n = ctypes.c_size_t(7)
     a = args(dq_weight=None)
     assert L.load().kda_qk_norm_bwd_workspace_size(ctypes.byref(a), ctypes.byref(n)) == L.KDA_OK and n.value == 0
+
+
+@pytest.mark.parametrize("mut,status", [
+    (dict(dtype=2), L.KDA_ERR_UNSUPPORTED), (dict(g_min=0.0), L.KDA_ERR_INVALID_ARG), (dict(T=-1), L.KDA_ERR_INVALID_ARG),
+    (dict(D_v=129), L.KDA_ERR_UNSUPPORTED), (dict(B=1 << 31), L.KDA_ERR_UNSUPPORTED),
+    (dict(num_slots=-1), L.KDA_ERR_INVALID_ARG), (dict(num_slots=3), L.KDA_ERR_INVALID_ARG),  # 4 sequences, no slots
+    (dict(num_slots=1 << 41), L.KDA_ERR_UNSUPPORTED), (dict(k=None), L.KDA_ERR_INVALID_ARG),
+    (dict(z=None), L.KDA_ERR_INVALID_ARG), (dict(state=None), L.KDA_ERR_INVALID_ARG),
+    (dict(state=P[5] + 2), L.KDA_ERR_INVALID_ARG), (dict(slots=P[7] + 1), L.KDA_ERR_INVALID_ARG),
+    (dict(o=P[2] + 64), L.KDA_ERR_INVALID_ARG), (dict(o=P[5] + 64), L.KDA_ERR_INVALID_ARG),
+    (dict(state=P[0]), L.KDA_ERR_INVALID_ARG), (dict(gate_logits=P[8], eps=-1.0), L.KDA_ERR_INVALID_ARG),
+])
+def test_gdn_decode_refusals(mut, status):
+    a = dict(B=4, num_slots=4, T=2, H=3, D_k=32, D_v=32, dtype=L.KDA_BF16, q=P[0], k=P[1], v=P[2], z=P[3], g_min=-5.0,
+             beta=P[4], state=P[5], o=P[6], eps=1e-6)
+    a.update(mut)
+    refused("kda_gdn_decode_step", L.GdnDecodeArgs(**a), status)
