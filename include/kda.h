@@ -529,6 +529,45 @@ typedef struct kda_gdn_decode_args {
 
 kda_status_t kda_gdn_decode_step(const kda_gdn_decode_args *args);
 
+/*
+ * The output path in 8 bits: e4m3 values with one fp32 scale per block of 128
+ * channels (activations: blocks of one row, weights: of 128 rows; edge blocks
+ * are smaller).  For a block with largest magnitude amax
+ *   scale = max(amax / 448, 2^-126)  (1 for a block of zeros)
+ *   value = e4m3 nearest to x / scale (ties to even)
+ * and x stands for value * scale.  A NaN element stays NaN and does not enter
+ * amax; an infinite one makes its block's scale infinite and its values 0 or NaN.
+ *
+ * kda_quant_fp8 - quantises a matrix:
+ *   x (rows, cols) dtype;  x8 (rows, cols) e4m3 out;  block_rows 1 or 128;
+ *   scales (ceil(rows / block_rows), ceil(cols / 128)) fp32 out
+ */
+kda_status_t kda_quant_fp8(const void *x, kda_dtype_t dtype, int64_t rows, int64_t cols, int32_t block_rows,
+                           void *x8, float *scales, void *stream);
+
+/*
+ * kda_norm_gate_fp8 - kda_norm_gate with its result quantised as it is produced
+ * (never rounded to dtype in between):
+ *   o, gate_logits (N, H, D_v) dtype;  x8 (N, H * D_v) e4m3 out
+ *   scales (N, ceil(H * D_v / 128)) fp32 out (with D_v = 128: one per head)
+ * H and D_v <= 8192.
+ */
+kda_status_t kda_norm_gate_fp8(const void *o, const void *gate_logits, int64_t N, int32_t H, int32_t D_v, float eps,
+                               kda_dtype_t dtype, void *x8, float *scales, void *stream);
+
+/*
+ * kda_out_proj_fp8 - kda_out_proj from quantised operands:
+ *   y[n, m] = sum_kb x_scale[n, kb] W_scale[m / 128, kb] sum_{i in block kb} x8[n, i] W8[m, i]
+ *   x8 (N, K) e4m3, x_scale (N, ceil(K / 128)) fp32
+ *   W8 (D_model, K) e4m3, W_scale (ceil(D_model / 128), ceil(K / 128)) fp32
+ *   y (N, D_model) out_dtype
+ * Blocks of the sum are exact products accumulated in fp32, and are scaled and
+ * added in fp32.  K % 16 == 0, 16-byte rows of y and 16-byte aligned pointers
+ * run on the tcgen05 tensor cores; anything else on an exact-fp32 SIMT kernel.
+ */
+kda_status_t kda_out_proj_fp8(const void *x8, const float *x_scale, const void *W8, const float *W_scale, int64_t N,
+                              int32_t K, int32_t D_model, void *y, kda_dtype_t out_dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

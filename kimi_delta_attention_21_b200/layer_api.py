@@ -1,7 +1,7 @@
 """Torch-facing binding of the operators around the gated delta rule: argument marshalling only.
 
 The norm of queries and keys with the rotation by position and its gradients;
-the gated delta rule token by token.
+the gated delta rule token by token; the output path in e4m3.
 Every step runs inside libkda's CUDA kernels, on the current stream of the
 tensors' device (which need not be the current device).
 """
@@ -168,9 +168,9 @@ def gdn_decode_step(q, k, v, beta, state, *, z=None, log_decay=None, g_min=-5.0,
     z or log_decay (B,H).  T tokens each: the same with (B,T,H,...).  ``state``
     (num_slots,H,D_k,D_v) fp32 is advanced IN PLACE; ``slots`` (B,) int32 picks
     each sequence's state (None: the first B).  A negative slot is a padded row,
-    whose output rows stay as they were (zeros when ``out`` is not given); a slot
-    outside the pool, or given twice, is skipped like it and sets ``dev_status``
-    (a zeroed int32 tensor).  Returns o in the input dtype."""
+    whose rows of ``out`` stay as they were (unspecified when ``out`` is not given);
+    a slot outside the pool, or given twice, is skipped like it and sets
+    ``dev_status`` (a zeroed int32 tensor).  Returns o in the input dtype."""
     dev, dt = _cuda(q, "q").device, q.dtype
     code = _code(q, "q")
     if q.dim() not in (3, 4):
@@ -191,11 +191,72 @@ def gdn_decode_step(q, k, v, beta, state, *, z=None, log_decay=None, g_min=-5.0,
     _need(state, "state", dev, torch.float32, (state.shape[0], H, Dk, Dv))
     _need(dev_status, "dev_status", dev, torch.int32, dev_status.shape if dev_status is not None else ())
     if out is None:
-        out = (torch.empty if slots is None else torch.zeros)((*lead, Dv), dtype=dt, device=dev)
+        out = torch.empty((*lead, Dv), dtype=dt, device=dev)
     else:
         _need(out, "out", dev, dt, (*lead, Dv))
     a = GdnDecodeArgs(B, state.shape[0], T, H, Dk, Dv, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(z),
                       _ptr(log_decay), g_min, beta.data_ptr(), state.data_ptr(), _ptr(slots), _ptr(gate_logits), eps,
                       out.data_ptr(), _ptr(dev_status), _stream_of(dev))
     _call("kda_gdn_decode_step", dev, ctypes.byref(a))
+    return out
+
+
+# ---------------------------------------------------------------- the output path in e4m3
+def quant_fp8(x, block_rows=1):
+    """e4m3 values of a matrix x (..., K), float32 or bfloat16, and the fp32 scale of each block of 128 channels
+    (kda_quant_fp8): block_rows = 1 for activations, 128 for weights (D_model, K).  Returns (x8, scales) with scales
+    (..., ceil(K / 128)) or (ceil(D_model / 128), ceil(K / 128))."""
+    dev = _cuda(x, "x").device
+    code = _code(x, "x")
+    _need(x, "x", dev, x.dtype, x.shape)
+    if block_rows != 1 and x.dim() != 2:
+        raise ValueError("blocks of several rows need a matrix")
+    K = x.shape[-1]
+    kb = -(-K // 128)
+    rows = x.numel() // K if K else 0
+    x8 = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+    shape = (*x.shape[:-1], kb) if block_rows == 1 else (-(-rows // block_rows) if block_rows > 0 else 0, kb)
+    scales = torch.empty(shape, dtype=torch.float32, device=dev)
+    _call("kda_quant_fp8", dev, x.data_ptr(), code, rows, K, block_rows, x8.data_ptr(), scales.data_ptr(), _stream_of(dev))
+    return x8, scales
+
+
+def norm_gate_fp8(o, gate_logits, eps=1e-6):
+    """Per-head RMSNorm over D_v, sigmoid gate and quantisation to e4m3 in one pass (kda_norm_gate_fp8); o, gate_logits
+    (..., H, D_v).  Returns (x8 (..., H * D_v), scales (..., ceil(H * D_v / 128))) for ``out_proj_fp8``."""
+    dev = _cuda(o, "o").device
+    code = _code(o, "o")
+    _need(o, "o", dev, o.dtype, o.shape)
+    _need(gate_logits, "gate_logits", dev, o.dtype, o.shape)
+    H, Dv = o.shape[-2:]
+    lead, K = o.shape[:-2], H * Dv
+    x8 = torch.empty((*lead, K), dtype=torch.float8_e4m3fn, device=dev)
+    scales = torch.empty((*lead, -(-K // 128)), dtype=torch.float32, device=dev)
+    N = x8.numel() // K if K else 0
+    _call("kda_norm_gate_fp8", dev, o.data_ptr(), gate_logits.data_ptr(), N, H, Dv, eps, code, x8.data_ptr(),
+          scales.data_ptr(), _stream_of(dev))
+    return x8, scales
+
+
+def out_proj_fp8(x8, x_scale, W8, W_scale, out_dtype=torch.bfloat16, out=None):
+    """y = x W_o^T from e4m3 operands with a scale per block of 128 (kda_out_proj_fp8): x8 (..., K) and x_scale
+    (..., ceil(K / 128)); W8 (D_model, K) and W_scale (ceil(D_model / 128), ceil(K / 128)), as ``norm_gate_fp8`` and
+    ``quant_fp8(W_o, 128)`` give them.  Returns y (..., D_model) in ``out_dtype``."""
+    dev = _cuda(x8, "x8").device
+    Dm, K = W8.shape
+    kb = -(-K // 128)
+    lead = x8.shape[:-1]
+    _need(x8, "x8", dev, torch.float8_e4m3fn, (*lead, K))
+    _need(x_scale, "x_scale", dev, torch.float32, (*lead, kb))
+    _need(W8, "W8", dev, torch.float8_e4m3fn, (Dm, K))
+    _need(W_scale, "W_scale", dev, torch.float32, (-(-Dm // 128), kb))
+    if out_dtype not in _DT:
+        raise TypeError(f"out_dtype must be float32 or bfloat16 (got {out_dtype})")
+    if out is None:
+        out = torch.empty((*lead, Dm), dtype=out_dtype, device=dev)
+    else:
+        _need(out, "out", dev, out_dtype, (*lead, Dm))
+    N = x8.numel() // K if K else 0
+    _call("kda_out_proj_fp8", dev, x8.data_ptr(), x_scale.data_ptr(), W8.data_ptr(), W_scale.data_ptr(), N, K, Dm,
+          out.data_ptr(), _DT[out_dtype], _stream_of(dev))
     return out

@@ -100,3 +100,47 @@ def test_gdn_decode_refusals(mut, status):
              beta=P[4], state=P[5], o=P[6], eps=1e-6)
     a.update(mut)
     refused("kda_gdn_decode_step", L.GdnDecodeArgs(**a), status)
+
+
+def call_refused(fn, status, *args):
+    lib = L.load()
+    n0 = lib.kda_launch_count()
+    assert getattr(lib, fn)(*args) == status, lib.kda_last_error().decode()
+    assert lib.kda_launch_count() == n0
+
+
+def test_fp8_refusals():
+    bad, unsup, big = L.KDA_ERR_INVALID_ARG, L.KDA_ERR_UNSUPPORTED, 1 << 30
+    q = lambda status, x=P[0], dt=1, r=4, c=256, br=1, x8=P[1], sc=P[2]: call_refused(
+        "kda_quant_fp8", status, x, dt, r, c, br, x8, sc, None)
+    q(unsup, dt=3)
+    q(bad, r=-1)
+    q(bad, c=0)
+    q(bad, br=2)
+    q(unsup, r=1 << 40, c=1 << 20)
+    q(bad, x=None)
+    q(bad, x=P[0] + 1)
+    q(bad, x8=P[0] + 64)
+    q(bad, sc=P[1] + 64)
+    n = lambda status, o=P[0], g=P[1], N=4, H=2, Dv=128, eps=1e-6, dt=1, x8=P[2], sc=P[3]: call_refused(
+        "kda_norm_gate_fp8", status, o, g, N, H, Dv, eps, dt, x8, sc, None)
+    n(unsup, dt=9)
+    n(bad, H=0)
+    n(bad, eps=-1.0)
+    n(unsup, H=8193)
+    n(unsup, N=1 << 31)
+    n(bad, g=None)
+    n(bad, x8=P[1])
+    n(bad, sc=P[2])
+    p = lambda status, x=P[0], xs=P[1], w=P[2], ws=P[3], N=4, K=256, M=64, y=P[4], dt=1: call_refused(
+        "kda_out_proj_fp8", status, x, xs, w, ws, N, K, M, y, dt, None)
+    p(unsup, dt=2)
+    p(bad, K=0)
+    p(bad, N=-1)
+    p(unsup, N=1 << 31)
+    p(unsup, N=big, M=big)
+    p(bad, xs=None)
+    p(bad, ws=P[3] + 2)
+    p(bad, y=P[0])
+    p(bad, y=P[4] + 1)
+    p(L.KDA_OK, N=0)
