@@ -530,6 +530,21 @@ typedef struct kda_gdn_decode_args {
 kda_status_t kda_gdn_decode_step(const kda_gdn_decode_args *args);
 
 /*
+ * kda_gdn_chunk_bwd - gradients of the gated delta rule (kda_gdn_chunk_fwd's
+ * core output o~): kda_chunk_bwd with one scalar decay per token and head.
+ * Arguments, outputs and conventions are kda_recurrent_bwd's except
+ *   z, log_decay, dz  (B, S, H)
+ * fp32 accuracy throughout (tensor-core products of split operands, see
+ * csrc/mma_tf32.cuh); any g_min.  Outputs are fully written.  The workspace holds
+ * one record per (b, h, chunk of 64 tokens): 4 (256 + 12288 + 64 (Dk + 2 Dv) + 2 Dk Dv)
+ * bytes with D_k and D_v rounded up to multiples of 16 (273 KiB at 128).
+ * Errors: as kda_chunk_bwd; UNSUPPORTED if B*H*max(chunks, 16) exceeds 2^31 - 1.
+ */
+kda_status_t kda_gdn_chunk_bwd_workspace_size(const kda_recurrent_bwd_args *args, size_t *bytes);
+
+kda_status_t kda_gdn_chunk_bwd(const kda_recurrent_bwd_args *args);
+
+/*
  * The output path in 8 bits: e4m3 values with one fp32 scale per block of 128
  * channels (activations: blocks of one row, weights: of 128 rows; edge blocks
  * are smaller).  For a block with largest magnitude amax

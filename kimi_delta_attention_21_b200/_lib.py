@@ -140,6 +140,8 @@ SIGNATURES = {
     "kda_qk_norm_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(QkNormBwdArgs), ctypes.POINTER(ctypes.c_size_t)]),
     "kda_qk_norm_bwd": (ctypes.c_int, [ctypes.POINTER(QkNormBwdArgs)]),
     "kda_gdn_decode_step": (ctypes.c_int, [ctypes.POINTER(GdnDecodeArgs)]),
+    "kda_gdn_chunk_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(RecBwdArgs), ctypes.POINTER(ctypes.c_size_t)]),
+    "kda_gdn_chunk_bwd": (ctypes.c_int, [ctypes.POINTER(RecBwdArgs)]),
     "kda_quant_fp8": (ctypes.c_int, [_p, ctypes.c_int, _i64, _i64, _i32, _p, _p, _p]),
     "kda_norm_gate_fp8": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _f32, ctypes.c_int, _p, _p, _p]),
     "kda_out_proj_fp8": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, _p, ctypes.c_int, _p]),

@@ -1,0 +1,841 @@
+// Gradients of the gated delta rule (one scalar decay per token and head), chunk form, fp32 accuracy.
+//
+// Inside a chunk of C = 64 tokens, with G_r the cumulative log-decay, E[r,i] = e^{G_r - G_i} (i <= r) and
+// e^{D_r} = e^{G_last - G_r}:
+//   P[r,i] = (k_r . k_i) E[r,i] (i < r),   A = Diag(beta) P,   T = (I + A)^{-1}
+//   Bk = Diag(beta e^G) K,  Bv = Diag(beta) V,  W = T Bk,  U = T Bv,  V' = U - W S
+//   M[r,i] = (q_r . k_i) E[r,i] (i <= r),   O = Diag(e^G) Q S + M V',
+//   S_next = gamma S + K^T Diag(e^D) V',  gamma = e^{G_last}
+// (S: the state entering the chunk), and in reverse, with dS_next the gradient of the state leaving it:
+//   dV' = M^T dO + Diag(e^D) K dS_next
+//   dS  = gamma dS_next + Q^T Diag(e^G) dO - W^T dV'
+//   dQg = dO S^T,  dKd = V' dS_next^T,  dM = dO V'^T (i <= r),  dW = -dV' S^T
+//   dT  = dV' Bv^T + dW Bk^T,  dBv = T^T dV',  dBk = T^T dW,  dA = -T^T dT T^T (i < r)
+//   dv = beta dBv,   dq = e^G dQg + (dM * E) K
+//   dk = beta e^G dBk + e^D dKd + (dP' + dP'^T) K + (dM * E)^T Q,   dP' = Diag(beta) dA * E
+//   dbeta = rowsum(dBv * V) + rowsum(dBk * e^G K) + rowsum(dA * P)
+// Because the decay is one number per token, its gradient needs no difference of large sums: log alpha_t is a
+// factor of every pair (r, i) with i < t <= r, of the rows r >= t of Q e^G and Bk, of the rows i < t of
+// K e^D, and of gamma:
+//   dlog alpha_t = sum_{r >= t > i} (dA * A + dM * M)[r,i] + sum_{r >= t} (dQg . Qg + dBk . Bk)_r
+//                  + sum_{i < t} (dKd . Kd)_i + gamma <dS_next, S>.
+// G is cumulated and differenced in fp64: in-chunk sums reach 64 |g_min|, where the fp32 difference of two
+// neighbours would be off by 1e-5.  No factor e^{-G} is ever formed, so any g_min works.
+//
+// Three launches: gb_prep (a CTA per chunk: P, M, T, W, U into a workspace record), gb_chain (a CTA per
+// (b, h, 16 value columns) and direction: the state forward, which leaves S and V' of every chunk, and at the
+// same time its gradient backward, which leaves dS_next and dV': the two do not depend on each other), and
+// gb_grad (a CTA per chunk: everything else).  All products run on the tensor cores to fp32 accuracy
+// (mma_tf32.cuh); bf16 inputs are exact operands there and cost a third less, which is why the scale factors
+// of K and Q rows are applied to the other operand or to the result.
+#include "host_check.cuh"
+#include "kda_internal.cuh"
+#include "mma_tf32.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int C = 64;       // tokens per chunk
+constexpr int LD = 136;     // pitch of [64 or 128][D] tiles in shared memory: 8 mod 32
+constexpr int LC = 72;      // pitch of [64][64] tiles
+constexpr int NT_P = 512;   // threads of the per-chunk kernels
+constexpr int NT_C = 256;   // threads of the chain kernel
+constexpr int VS = 16;      // value columns per chain CTA
+constexpr int LS = 20, LV = 24;  // chain pitches of [Dk][16] and [64][16] tiles (conflict-free reads by k)
+
+__host__ __device__ inline int pad16(int x) { return (x + 15) & ~15; }
+
+// One (b, h, chunk) record; offsets in floats, all blocks whole 64-byte rows.  D_k and D_v are padded to
+// multiples of 16; the padding holds zeros.
+struct Rec {
+    int64_t G;          // [64] double
+    int64_t eG, eD;     // [64] e^G, e^{G_last - G}
+    int64_t T, P, M;    // [64][64]
+    int64_t W;          // [64][Dkp]
+    int64_t V;          // [64][Dvp]: U, then V'
+    int64_t S, dS;      // [Dkp][Dvp]: the state entering the chunk, the gradient of the state leaving it
+    int64_t dV;         // [64][Dvp]: dV'
+    int64_t size;
+};
+
+__host__ __device__ inline Rec make_rec(int Dk, int Dv) {
+    const int64_t dk = pad16(Dk), dv = pad16(Dv);
+    Rec r;
+    r.G = 0;
+    r.eG = 2 * C;
+    r.eD = r.eG + C;
+    r.T = r.eD + C;
+    r.P = r.T + C * C;
+    r.M = r.P + C * C;
+    r.W = r.M + C * C;
+    r.V = r.W + C * dk;
+    r.S = r.V + C * dv;
+    r.dS = r.S + dk * dv;
+    r.dV = r.dS + dk * dv;
+    r.size = r.dV + C * dv;
+    return r;
+}
+
+struct GbArgs {
+    int64_t S;
+    int H, Dk, Dv, Nc, nslice;
+    const void *q, *k, *v, *z, *beta, *dO;
+    const float *log_decay;
+    float g_min;
+    const float *S0, *dST;
+    float *dq, *dk, *dv, *dbeta, *dz, *dS0;
+    float *ws;
+    size_t ws_bytes, ns_bytes;
+    unsigned int *bounds;
+};
+
+struct Unit {
+    int64_t b, t0, row0;  // row0: index of (token t0, head h) in a (B, S, H) tensor
+    int h, len;
+};
+
+__device__ __forceinline__ Unit unit_of(const GbArgs &p, int64_t bh, int n) {
+    Unit u;
+    u.b = bh / p.H;
+    u.h = (int)(bh - u.b * p.H);
+    u.t0 = (int64_t)n * C;
+    u.len = (int)min((int64_t)C, p.S - u.t0);
+    u.row0 = (u.b * p.S + u.t0) * p.H + u.h;
+    return u;
+}
+
+// Token rows (rs elements apart) as fp32 into [64][ld], zero past `len` rows and D columns up to Dp; eight
+// loads in flight per thread.
+template <typename T, int NT>
+__device__ __forceinline__ void load_rows(float *dst, int ld, const T *src, int64_t rs, int len, int D, int Dp) {
+    const int n = C * Dp;
+    for (int base = threadIdx.x; base < n; base += 8 * NT) {
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = base + u * NT, r = i / Dp, c = i - r * Dp;
+            v[u] = (i < n && r < len && c < D) ? load_elem(src, (int64_t)r * rs + c) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = base + u * NT, r = i / Dp, c = i - r * Dp;
+            if (i < n) dst[r * ld + c] = v[u];
+        }
+    }
+}
+
+// The same rows kept in their type, by cp.async where 16-byte pieces are possible.
+template <typename T>
+__device__ __forceinline__ void stage_rows(T *dst, const T *src, int64_t rs, int len, int D, int Dp, bool wide) {
+    constexpr int E = 16 / (int)sizeof(T);
+    if (wide) {  // D is a multiple of E, every row starts on 16 bytes
+        const int W = Dp / E, n = C * W;
+        for (int i = threadIdx.x; i < n; i += NT_C) {
+            const int r = i / W, c = (i - r * W) * E;
+            const bool in = r < len && c < D;
+            cp_async16_fill(reinterpret_cast<float *>(dst + r * LD + c),
+                            reinterpret_cast<const float *>(src + (in ? (int64_t)r * rs + c : 0)), in);
+        }
+        return;
+    }
+    for (int i = threadIdx.x; i < C * Dp; i += NT_C) {
+        const int r = i / Dp, c = i - r * Dp;
+        dst[r * LD + c] = (r < len && c < D) ? src[(int64_t)r * rs + c] : T(0.f);
+    }
+}
+
+// A record block of `rows` rows of `cols` floats (a multiple of 4, pitch `pitch`) into shared memory.
+template <int NT>
+__device__ __forceinline__ void stage_block(float *dst, int ld, const float *src, int pitch, int rows, int cols) {
+    const int W = cols / 4, n = rows * W;
+    for (int i = threadIdx.x; i < n; i += NT) {
+        const int r = i / W, c = (i - r * W) * 4;
+        cp_async16_fill(dst + r * ld + c, src + (int64_t)r * pitch + c);
+    }
+}
+
+// ---------------------------------------------------------------- per chunk: P, M, T, W, U
+constexpr size_t PREP_SMEM = sizeof(float) * (3 * C * LD + 3 * C * LC + 3 * C) + sizeof(double) * C;
+
+template <typename T>
+__global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant__ GbArgs p) {
+    constexpr bool EX = sizeof(T) == 2;
+    extern __shared__ __align__(16) uint8_t gb_sm[];
+    double *sG = reinterpret_cast<double *>(gb_sm);
+    float *sK = reinterpret_cast<float *>(sG + C), *sQ = sK + C * LD, *sV = sQ + C * LD;
+    float *sA = sV + C * LD, *sT = sA + C * LC, *sY = sT + C * LC, *sb = sY + C * LC, *seG = sb + C, *seD = seG + C;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t bh = blockIdx.x / p.Nc;
+    const int n = (int)(blockIdx.x - bh * p.Nc);
+    const Unit u = unit_of(p, bh, n);
+    const int Dkp = pad16(p.Dk), Dvp = pad16(p.Dv);
+    const Rec R = make_rec(p.Dk, p.Dv);
+    float *rec = p.ws + (int64_t)blockIdx.x * R.size;
+    if (!in_bounds(rec, (size_t)R.size * 4, p.ws, p.ws_bytes, p.bounds)) return;
+
+    load_rows<T, NT_P>(sK, LD, (const T *)p.k + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp);
+    load_rows<T, NT_P>(sQ, LD, (const T *)p.q + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp);
+    load_rows<T, NT_P>(sV, LD, (const T *)p.v + u.row0 * p.Dv, (int64_t)p.H * p.Dv, u.len, p.Dv, Dvp);
+    if (warp == 0) {  // the cumulative log-decay: two tokens per lane, a scan over the warp
+        double g[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 2 * lane + e;
+            float x = 0.f;
+            if (r < u.len) {
+                const int64_t i = u.row0 + (int64_t)r * p.H;
+                x = p.log_decay ? clamp_log_decay(p.log_decay[i], p.g_min)
+                                : log_alpha_of(load_elem((const T *)p.z, i), p.g_min);
+            }
+            g[e] = (double)x;
+            sb[r] = r < u.len ? load_elem((const T *)p.beta, u.row0 + (int64_t)r * p.H) : 0.f;
+        }
+        double s = g[0] + g[1];
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const double o = __shfl_up_sync(0xffffffffu, s, m);
+            if (lane >= m) s += o;
+        }
+        const double last = __shfl_sync(0xffffffffu, s, 31);
+        const double G1 = s, G0 = s - g[1];
+        sG[2 * lane] = G0;
+        sG[2 * lane + 1] = G1;
+        double *gG = reinterpret_cast<double *>(rec + R.G);
+        gG[2 * lane] = G0;
+        gG[2 * lane + 1] = G1;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 2 * lane + e;
+            const float a = expf((float)(e ? G1 : G0)), d = expf((float)(last - (e ? G1 : G0)));
+            seG[r] = a;
+            rec[R.eG + r] = a;
+            rec[R.eD + r] = d;
+        }
+    }
+    for (int i = tid; i < C * LC; i += NT_P) sT[i] = 0.f;
+    __syncthreads();
+    // P and M: warp (32 rows, 8 columns); tiles above the diagonal are zeros
+    {
+        const int r0 = 32 * (warp & 1), c0 = 8 * (warp >> 1);
+        float kk[2][1][4] = {}, qk[2][1][4] = {};
+        if (c0 < r0 + 32) {
+            tf32::tile<2, 1, false, false, EX, EX>(kk, sK + r0 * LD, LD, sK + c0 * LD, LD, 0, Dkp);
+            tf32::tile<2, 1, false, false, EX, EX>(qk, sQ + r0 * LD, LD, sK + c0 * LD, LD, 0, Dkp);
+        }
+        tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
+            r += r0;
+            c += c0;
+            const float x = c <= r ? expf((float)(sG[r] - sG[c])) : 0.f;
+            const float P = c < r ? kk[i][j][e] * x : 0.f;
+            rec[R.P + r * C + c] = P;
+            rec[R.M + r * C + c] = c <= r ? qk[i][j][e] * x : 0.f;
+            sA[r * LC + c] = sb[r] * P;
+        });
+    }
+    __syncthreads();
+    // T = (I + A)^{-1}: the four diagonal blocks of 16 by forward substitution (a thread per column) ...
+    if (warp < 4 && lane < 16) {
+        const float *a = sA + 16 * warp * (LC + 1);
+        float x[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            float s = r == lane ? 1.f : 0.f;
+#pragma unroll
+            for (int m = 0; m < r; ++m) s = fmaf(-a[r * LC + m], x[m], s);
+            x[r] = s;
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sT[(16 * warp + r) * LC + 16 * warp + lane] = x[r];
+    }
+    __syncthreads();
+    // ... then T21 = -T22 (A21 T11), blocks of 16 and of 32
+    {
+        const int b0 = 32 * (tid >> 8), r = (tid & 255) >> 4, c = tid & 15;
+        float s = 0.f;
+#pragma unroll
+        for (int m = 0; m < 16; ++m) s = fmaf(sA[(b0 + 16 + r) * LC + b0 + m], sT[(b0 + m) * LC + b0 + c], s);
+        sY[(b0 + r) * LC + c] = s;
+        __syncthreads();
+        s = 0.f;
+#pragma unroll
+        for (int m = 0; m < 16; ++m) s = fmaf(-sT[(b0 + 16 + r) * LC + b0 + 16 + m], sY[(b0 + m) * LC + c], s);
+        sT[(b0 + 16 + r) * LC + b0 + c] = s;
+    }
+    __syncthreads();
+    {
+        float s[2] = {0.f, 0.f};
+        const int c = tid & 31, r = tid >> 5;
+#pragma unroll 8
+        for (int m = 0; m < 32; ++m) {
+            const float t = sT[m * LC + c];
+            s[0] = fmaf(sA[(32 + r) * LC + m], t, s[0]);
+            s[1] = fmaf(sA[(48 + r) * LC + m], t, s[1]);
+        }
+        sY[r * LC + c] = s[0];
+        sY[(16 + r) * LC + c] = s[1];
+        __syncthreads();
+        s[0] = s[1] = 0.f;
+#pragma unroll 8
+        for (int m = 0; m < 32; ++m) {
+            const float y = sY[m * LC + c];
+            s[0] = fmaf(-sT[(32 + r) * LC + 32 + m], y, s[0]);
+            s[1] = fmaf(-sT[(48 + r) * LC + 32 + m], y, s[1]);
+        }
+        sT[(32 + r) * LC + c] = s[0];
+        sT[(48 + r) * LC + c] = s[1];
+    }
+    __syncthreads();
+    // T out; T Diag(beta e^G) over A, T Diag(beta) over the scratch: the scales of Bk's and Bv's rows
+    for (int i = tid; i < C * C; i += NT_P) {
+        const int r = i >> 6, c = i & 63;
+        const float t = sT[r * LC + c], tb = t * sb[c];
+        rec[R.T + i] = t;
+        sA[r * LC + c] = tb * seG[c];
+        sY[r * LC + c] = tb;
+    }
+    __syncthreads();
+    const int r0 = 32 * (warp & 1), c0 = 16 * (warp >> 1);
+    if (c0 < Dkp) {
+        float acc[2][2][4] = {};
+        tf32::tile<2, 2, false, true, false, EX>(acc, sA + r0 * LC, LC, sK + c0, LD, 0, r0 + 32);
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) { rec[R.W + (r0 + r) * Dkp + c0 + c] = acc[i][j][e]; });
+    }
+    if (c0 < Dvp) {
+        float acc[2][2][4] = {};
+        tf32::tile<2, 2, false, true, false, EX>(acc, sY + r0 * LC, LC, sV + c0, LD, 0, r0 + 32);
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) { rec[R.V + (r0 + r) * Dvp + c0 + c] = acc[i][j][e]; });
+    }
+}
+
+// ---------------------------------------------------------------- the state and its gradient through the chunks
+template <typename T> constexpr size_t chain_smem() {
+    // backward (the larger): M, W, K, Q, dO, dV', dS, e^G and e^D
+    return sizeof(float) * (C * LC + C * LD + 2 * C * LV + 128 * LS + 2 * C) + 2 * sizeof(T) * C * LD;
+}
+
+// Forward: the state stays in the MMA accumulators of the warps (16 key rows each), with a copy in shared
+// memory as the next product's operand.  W and U of the next chunk arrive while K is used, K while W is.
+template <typename T>
+__device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j0, float *sm, bool wide) {
+    constexpr bool EX = sizeof(T) == 2;
+    float *sW = sm, *sU = sW + C * LD, *sVp = sU + C * VS, *sS = sVp + C * LV, *se = sS + 128 * LS;
+    T *sK = reinterpret_cast<T *>(se + 2 * C);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int Dkp = pad16(p.Dk), Dvp = pad16(p.Dv);
+    const Rec R = make_rec(p.Dk, p.Dv);
+    const int64_t b = bh / p.H;
+    const int h = (int)(bh - b * p.H);
+    float *rec0 = p.ws + bh * p.Nc * R.size;
+    auto stage_w = [&](int n) {
+        const float *rec = rec0 + (int64_t)n * R.size;
+        stage_block<NT_C>(sW, LD, rec + R.W, Dkp, C, Dkp);
+        stage_block<NT_C>(sU, VS, rec + R.V + j0, Dvp, C, VS);
+        cp_async_commit_group();
+    };
+    auto stage_k = [&](int n) {
+        const Unit u = unit_of(p, bh, n);
+        stage_block<NT_C>(se, 2 * C, rec0 + (int64_t)n * R.size + R.eG, 2 * C, 1, 2 * C);
+        stage_rows<T>(sK, (const T *)p.k + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, wide);
+        cp_async_commit_group();
+    };
+    (void)b;
+    (void)h;
+    const int m0 = 16 * warp;  // this warp's key rows
+    float S[1][2][4] = {};
+    tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
+        if (m0 + r < p.Dk && j0 + c < p.Dv && p.S0) S[i][j][e] = p.S0[(bh * p.Dk + m0 + r) * p.Dv + j0 + c];
+        if (m0 < Dkp) sS[(m0 + r) * LS + c] = S[i][j][e];
+    });
+    stage_w(0);
+    for (int n = 0; n < p.Nc; ++n) {
+        float *rec = rec0 + (int64_t)n * R.size;
+        cp_async_wait<0>();  // W and U of chunk n
+        __syncthreads();
+        stage_k(n);
+        if (m0 < Dkp)  // the state entering the chunk
+            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
+                if (!(e & 1))
+                    *reinterpret_cast<float2 *>(rec + R.S + (int64_t)(m0 + r) * Dvp + j0 + c) =
+                        make_float2(S[i][j][e], S[i][j][e + 1]);
+            });
+        float v[1][1][4] = {};
+        const int r0 = 16 * (warp & 3), c0 = 8 * (warp >> 2);
+        tf32::tile<1, 1, false, true, false, false, true>(v, sW + r0 * LD, LD, sS + c0, LS, 0, Dkp);
+        tf32::each<1, 1>([&](int i, int j, int e, int r, int c) { v[i][j][e] = sU[(r0 + r) * VS + c0 + c] - v[i][j][e]; });
+        cp_async_wait<0>();  // K of chunk n
+        tf32::each<1, 1>([&](int i, int j, int e, int r, int c) {
+            if (!(e & 1))
+                *reinterpret_cast<float2 *>(rec + R.V + (int64_t)(r0 + r) * Dvp + j0 + c0 + c) =
+                    make_float2(v[i][j][e], v[i][j][e + 1]);
+        });
+        __syncthreads();  // K and e^D are there for everyone
+        tf32::each<1, 1>([&](int i, int j, int e, int r, int c) {
+            sVp[(r0 + r) * LV + c0 + c] = se[C + r0 + r] * v[i][j][e];  // e^D V'
+        });
+        __syncthreads();
+        if (n + 1 < p.Nc) stage_w(n + 1);
+        if (m0 < Dkp) {  // S <- gamma S + K^T (e^D V')
+            const float gamma = se[C - 1];
+            tf32::each<1, 2>([&](int i, int j, int e, int, int) { S[i][j][e] *= gamma; });
+            tf32::tile<1, 2, true, true, EX, false>(S, sK + m0, LD, sVp, LV, 0, C);
+            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { sS[(m0 + r) * LS + c] = S[i][j][e]; });
+        }
+    }
+}
+
+// Backward: the same for dS, from the last chunk to the first.  M, K (first half of a step) and Q, W
+// (second half) are refilled with the previous chunk's as soon as their half is done.
+template <typename T>
+__device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int j0, float *sm, bool wide) {
+    constexpr bool EX = sizeof(T) == 2;
+    constexpr int PER = C * VS / NT_C;
+    float *sM = sm, *sW = sM + C * LC, *sdO = sW + C * LD, *sdV = sdO + C * LV, *sS = sdV + C * LV, *se = sS + 128 * LS;
+    T *sK = reinterpret_cast<T *>(se + 2 * C), *sQ = sK + C * LD;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int Dkp = pad16(p.Dk), Dvp = pad16(p.Dv);
+    const Rec R = make_rec(p.Dk, p.Dv);
+    float *rec0 = p.ws + bh * p.Nc * R.size;
+    auto stage_a = [&](int n) {
+        const Unit u = unit_of(p, bh, n);
+        stage_block<NT_C>(sM, LC, rec0 + (int64_t)n * R.size + R.M, C, C, C);
+        stage_rows<T>(sK, (const T *)p.k + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, wide);
+        cp_async_commit_group();
+    };
+    auto stage_b = [&](int n) {
+        const Unit u = unit_of(p, bh, n);
+        stage_block<NT_C>(sW, LD, rec0 + (int64_t)n * R.size + R.W, Dkp, C, Dkp);
+        stage_rows<T>(sQ, (const T *)p.q + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, wide);
+        cp_async_commit_group();
+    };
+    float pre[PER], pe = 0.f;  // this thread's elements of dO's columns, and its e^G or e^D
+    auto fetch = [&](int n) {
+        const Unit u = unit_of(p, bh, n);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int r = (tid + i * NT_C) / VS, c = (tid + i * NT_C) % VS;
+            pre[i] = (r < u.len && j0 + c < p.Dv)
+                         ? load_elem((const T *)p.dO, (u.row0 + (int64_t)r * p.H) * p.Dv + j0 + c)
+                         : 0.f;
+        }
+        if (tid < 2 * C) pe = rec0[(int64_t)n * R.size + R.eG + tid];
+    };
+    const int m0 = 16 * warp;
+    float dS[1][2][4] = {};
+    tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
+        if (m0 + r < p.Dk && j0 + c < p.Dv && p.dST) dS[i][j][e] = p.dST[(bh * p.Dk + m0 + r) * p.Dv + j0 + c];
+    });
+    stage_a(p.Nc - 1);
+    fetch(p.Nc - 1);
+    for (int n = p.Nc - 1; n >= 0; --n) {
+        float *rec = rec0 + (int64_t)n * R.size;
+        __syncthreads();  // everyone has left the previous step: its Q, W, dO, dV' and dS are read
+        stage_b(n);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) sdO[(tid + i * NT_C) / VS * LV + (tid + i * NT_C) % VS] = pre[i];
+        if (tid < 2 * C) se[tid] = pe;
+        if (m0 < Dkp)  // the gradient of the state leaving the chunk
+            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
+                sS[(m0 + r) * LS + c] = dS[i][j][e];
+                if (!(e & 1))
+                    *reinterpret_cast<float2 *>(rec + R.dS + (int64_t)(m0 + r) * Dvp + j0 + c) =
+                        make_float2(dS[i][j][e], dS[i][j][e + 1]);
+            });
+        cp_async_wait<1>();  // M and K of chunk n
+        __syncthreads();
+        // dV' = M^T dO + e^D (K dS_next): a warp per 16 rows and 8 columns
+        const int r0 = 16 * (warp & 3), c0 = 8 * (warp >> 2);
+        float v[1][1][4] = {}, x[1][1][4] = {};
+        tf32::tile<1, 1, true, true, false, EX, true>(v, sM + r0, LC, sdO + c0, LV, r0, C);
+        tf32::tile<1, 1, false, true, EX, false, true>(x, sK + r0 * LD, LD, sS + c0, LS, 0, Dkp);
+        tf32::each<1, 1>([&](int i, int j, int e, int r, int c) {
+            v[i][j][e] = fmaf(se[C + r0 + r], x[i][j][e], v[i][j][e]);
+            sdV[(r0 + r) * LV + c0 + c] = -v[i][j][e];
+        });
+        tf32::each<1, 1>([&](int i, int j, int e, int r, int c) {
+            if (!(e & 1))
+                *reinterpret_cast<float2 *>(rec + R.dV + (int64_t)(r0 + r) * Dvp + j0 + c0 + c) =
+                    make_float2(v[i][j][e], v[i][j][e + 1]);
+        });
+        __syncthreads();  // M, K and dO are read
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int r = (tid + i * NT_C) / VS, c = (tid + i * NT_C) % VS;
+            sdO[r * LV + c] = se[r] * pre[i];  // e^G dO
+        }
+        if (n > 0) {
+            stage_a(n - 1);
+            cp_async_wait<1>();  // Q and W of chunk n
+        } else {
+            cp_async_wait<0>();
+        }
+        __syncthreads();
+        if (n > 0) fetch(n - 1);
+        if (m0 < Dkp) {  // dS <- gamma dS_next + Q^T (e^G dO) - W^T dV'
+            const float gamma = se[C - 1];
+            tf32::each<1, 2>([&](int i, int j, int e, int, int) { dS[i][j][e] *= gamma; });
+            tf32::tile<1, 2, true, true, EX, false>(dS, sQ + m0, LD, sdO, LV, 0, C);
+            tf32::tile<1, 2, true, true, false, false>(dS, sW + m0, LD, sdV, LV, 0, C);
+        }
+    }
+    if (p.dS0 && in_bounds(p.dS0 + bh * p.Dk * p.Dv, (size_t)p.Dk * p.Dv * 4, p.dS0, p.ns_bytes, p.bounds))
+        tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
+            if (m0 + r < p.Dk && j0 + c < p.Dv) p.dS0[(bh * p.Dk + m0 + r) * p.Dv + j0 + c] = dS[i][j][e];
+        });
+}
+
+template <typename T>
+__global__ void __launch_bounds__(NT_C, sizeof(T) == 2 ? 2 : 1) gb_chain_kernel(const __grid_constant__ GbArgs p, int wide) {
+    extern __shared__ __align__(16) uint8_t gb_sm[];
+    const int64_t job = blockIdx.x >> 1, bh = job / p.nslice;
+    const int j0 = (int)(job - bh * p.nslice) * VS;
+    const Rec R = make_rec(p.Dk, p.Dv);
+    if (!in_bounds(p.ws + bh * p.Nc * R.size, (size_t)p.Nc * R.size * 4, p.ws, p.ws_bytes, p.bounds)) return;
+    float *sm = reinterpret_cast<float *>(gb_sm);
+    if (blockIdx.x & 1) chain_forward<T>(p, bh, j0, sm, wide);
+    else chain_backward<T>(p, bh, j0, sm, wide);
+}
+
+// ---------------------------------------------------------------- per chunk: the gradients
+constexpr size_t GRAD_SMEM = sizeof(float) * (128 * LD + 4 * C * LD + C * LC + 3 * C + 32) + sizeof(double) * C;
+
+template <typename T>
+__global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant__ GbArgs p) {
+    constexpr bool EX = sizeof(T) == 2;
+    extern __shared__ __align__(16) uint8_t gb_sm[];
+    double *sG = reinterpret_cast<double *>(gb_sm);
+    float *bS = reinterpret_cast<float *>(sG + C);        // S, then dS_next [128][LD]; then V and K [64][LD]
+    float *bO = bS + 128 * LD;                             // dO [64][LD]; then T [64][LC]; then row sums
+    float *bdV = bO + C * LD;                              // dV' [64][LD]; then T^T dT [64][LC]; then pair sums
+    float *bdW = bdV + C * LD;                             // dW [64][LD]; then dP' [64][LC]
+    float *bV = bdW + C * LD;                              // V' [64][LD]; then dT [64][LC]; then Q [64][LD]
+    float *sM = bV + C * LD;                               // dM * E [64][LC]
+    float *seG = sM + C * LC, *seD = seG + C, *sb = seD + C, *sred = sb + C;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const int64_t bh = blockIdx.x / p.Nc;
+    const int n = (int)(blockIdx.x - bh * p.Nc);
+    const Unit u = unit_of(p, bh, n);
+    const int Dk = p.Dk, Dv = p.Dv, Dkp = pad16(Dk), Dvp = pad16(Dv), len = u.len;
+    const Rec R = make_rec(Dk, Dv);
+    const float *rec = p.ws + (int64_t)blockIdx.x * R.size;
+    if (!in_bounds(rec, (size_t)R.size * 4, p.ws, p.ws_bytes, p.bounds)) return;
+    const int64_t rk = (int64_t)p.H * Dk, rv = (int64_t)p.H * Dv;
+    const T *gq = (const T *)p.q + u.row0 * Dk, *gk = (const T *)p.k + u.row0 * Dk;
+
+    stage_block<NT_P>(bS, LD, rec + R.S, Dvp, Dkp, Dvp);
+    stage_block<NT_P>(bdV, LD, rec + R.dV, Dvp, C, Dvp);
+    stage_block<NT_P>(bV, LD, rec + R.V, Dvp, C, Dvp);
+    cp_async_commit_group();
+    load_rows<T, NT_P>(bO, LD, (const T *)p.dO + u.row0 * Dv, rv, len, Dv, Dvp);
+    if (tid < C) {
+        sG[tid] = reinterpret_cast<const double *>(rec + R.G)[tid];
+        seG[tid] = rec[R.eG + tid];
+        seD[tid] = rec[R.eD + tid];
+        sb[tid] = tid < len ? load_elem((const T *)p.beta, u.row0 + (int64_t)tid * p.H) : 0.f;
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+
+    // every warp: 32 rows from r0; 16 columns from c0 of [64][D] results, 8 from c1 of [64][64] ones
+    const int r0 = 32 * (warp & 1), c0 = 16 * (warp >> 1), c1 = 8 * (warp >> 1);
+    const bool inK = c0 < Dkp, inV = c0 < Dvp, tri = c1 < r0 + 32;  // tri: the tile reaches below the diagonal
+    float dq[2][2][4] = {}, dk[2][2][4] = {}, X[2][1][4] = {};
+    float late[2][2] = {}, early[2][2] = {}, db[2][2] = {};  // row sums of this lane's rows 16 i + g + 8 half
+
+    // dQg = dO S^T (dq = e^G dQg) and dW = -dV' S^T
+    if (inK) {
+        tf32::tile<2, 2, false, false, EX, false>(dq, bO + r0 * LD, LD, bS + c0 * LD, LD, 0, Dvp);
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
+            dq[i][j][e] *= seG[r0 + r];
+            const float qv = (r0 + r < len && c0 + c < Dk) ? load_elem(gq, (r0 + r) * rk + c0 + c) : 0.f;
+            late[i][e >> 1] = fmaf(dq[i][j][e], qv, late[i][e >> 1]);
+        });
+        float w[2][2][4] = {};
+        tf32::tile<2, 2, false, false, false, false>(w, bdV + r0 * LD, LD, bS + c0 * LD, LD, 0, Dvp);
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) { bdW[(r0 + r) * LD + c0 + c] = -w[i][j][e]; });
+    }
+    {  // dM = dO V'^T (i <= r)
+        float m[2][1][4] = {};
+        if (tri) tf32::tile<2, 1, false, false, EX, false>(m, bO + r0 * LD, LD, bV + c1 * LD, LD, 0, Dvp);
+        tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
+            r += r0;
+            c += c1;
+            const float d = c <= r ? m[i][j][e] : 0.f;
+            sM[r * LC + c] = c <= r ? d * expf((float)(sG[r] - sG[c])) : 0.f;
+            if (c < r) X[i][j][e] = d * rec[R.M + r * C + c];
+        });
+    }
+    __syncthreads();
+    // dS_next over S, with <dS_next, S> on the way
+    float dot = 0.f;
+    {
+        const int W = Dvp / 4, m = Dkp * W;
+        for (int base = tid; base < m; base += 4 * NT_P) {
+            float4 d[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = base + e * NT_P;
+                d[e] = i < m ? *reinterpret_cast<const float4 *>(rec + R.dS + 4 * (int64_t)i) : make_float4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = base + e * NT_P;
+                if (i < m) {
+                    float4 *s = reinterpret_cast<float4 *>(bS + (i / W) * LD + (i % W) * 4);
+                    const float4 o = *s;
+                    dot = fmaf(o.x, d[e].x, fmaf(o.y, d[e].y, fmaf(o.z, d[e].z, fmaf(o.w, d[e].w, dot))));
+                    *s = d[e];
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (inK) {  // dKd = V' dS_next^T (dk = e^D dKd)
+        tf32::tile<2, 2, false, false, false, false>(dk, bV + r0 * LD, LD, bS + c0 * LD, LD, 0, Dvp);
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
+            dk[i][j][e] *= seD[r0 + r];
+            const float kv = (r0 + r < len && c0 + c < Dk) ? load_elem(gk, (r0 + r) * rk + c0 + c) : 0.f;
+            early[i][e >> 1] = fmaf(dk[i][j][e], kv, early[i][e >> 1]);
+        });
+    }
+    __syncthreads();
+    float *sV = bS, *sK = bS + C * LD, *sT = bO, *sdT = bV;
+    stage_block<NT_P>(sT, LC, rec + R.T, C, C, C);
+    cp_async_commit_group();
+    load_rows<T, NT_P>(sV, LD, (const T *)p.v + u.row0 * Dv, rv, len, Dv, Dvp);
+    load_rows<T, NT_P>(sK, LD, gk, rk, len, Dk, Dkp);
+    cp_async_wait<0>();
+    __syncthreads();
+    {  // dT = dV' Bv^T + dW Bk^T, on and below the diagonal (T has nothing above it)
+        float a[2][1][4] = {}, b[2][1][4] = {};
+        if (tri) {
+            tf32::tile<2, 1, false, false, false, EX>(a, bdV + r0 * LD, LD, sV + c1 * LD, LD, 0, Dvp);
+            tf32::tile<2, 1, false, false, false, EX>(b, bdW + r0 * LD, LD, sK + c1 * LD, LD, 0, Dkp);
+        }
+        tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
+            r += r0;
+            c += c1;
+            sdT[r * LC + c] = c <= r ? sb[c] * fmaf(seG[c], b[i][j][e], a[i][j][e]) : 0.f;
+        });
+    }
+    __syncthreads();
+    if (inV) {  // dBv = T^T dV'
+        float a[2][2][4] = {};
+        tf32::tile<2, 2, true, true, false, false>(a, sT + r0, LC, bdV + c0, LD, r0, C);
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
+            r += r0;
+            c += c0;
+            db[i][e >> 1] = fmaf(a[i][j][e], sV[r * LD + c], db[i][e >> 1]);
+            if (r < len && c < Dv) p.dv[(u.row0 + (int64_t)r * p.H) * Dv + c] = sb[r] * a[i][j][e];
+        });
+    }
+    if (inK) {  // dBk = T^T dW
+        float a[2][2][4] = {};
+        tf32::tile<2, 2, true, true, false, false>(a, sT + r0, LC, bdW + c0, LD, r0, C);
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
+            r += r0;
+            const float x = a[i][j][e] * seG[r], xk = x * sK[r * LD + c0 + c];
+            db[i][e >> 1] += xk;
+            late[i][e >> 1] = fmaf(sb[r], xk, late[i][e >> 1]);
+            dk[i][j][e] = fmaf(sb[r], x, dk[i][j][e]);
+        });
+    }
+    float y[2][1][4] = {};  // T^T dT
+    tf32::tile<2, 1, true, true, false, false>(y, sT + r0, LC, sdT + c1, LC, r0, C);
+    __syncthreads();
+    tf32::each<2, 1>([&](int i, int j, int e, int r, int c) { bdV[(r0 + r) * LC + c1 + c] = y[i][j][e]; });
+    float *sQ = bV;
+    load_rows<T, NT_P>(sQ, LD, gq, rk, len, Dk, Dkp);
+    __syncthreads();
+    {  // dA = -(T^T dT) T^T (i < r);  dP' = beta dA E
+        float a[2][1][4] = {};
+        if (tri) tf32::tile<2, 1, false, false, false, false>(a, bdV + r0 * LC, LC, sT + c1 * LC, LC, 0, c1 + 8);
+        tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
+            r += r0;
+            c += c1;
+            float d = 0.f;
+            if (c < r) {
+                const float P = rec[R.P + r * C + c];
+                db[i][e >> 1] = fmaf(-a[i][j][e], P, db[i][e >> 1]);
+                d = -a[i][j][e] * sb[r];
+                X[i][j][e] = fmaf(d, P, X[i][j][e]);
+                d *= expf((float)(sG[r] - sG[c]));
+            }
+            bdW[r * LC + c] = d;
+        });
+    }
+    __syncthreads();
+    if (inK) {
+        tf32::tile<2, 2, false, true, false, EX>(dq, sM + r0 * LC, LC, sK + c0, LD, 0, r0 + 32);
+        tf32::tile<2, 2, false, true, false, EX>(dk, bdW + r0 * LC, LC, sK + c0, LD, 0, r0 + 32);
+        tf32::tile<2, 2, true, true, false, EX>(dk, bdW + r0, LC, sK + c0, LD, r0, C);
+        tf32::tile<2, 2, true, true, false, EX>(dk, sM + r0, LC, sQ + c0, LD, r0, C);
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
+            r += r0;
+            c += c0;
+            if (r < len && c < Dk) {
+                const int64_t at = (u.row0 + (int64_t)r * p.H) * Dk + c;
+                p.dq[at] = dq[i][j][e];
+                p.dk[at] = dk[i][j][e];
+            }
+        });
+    }
+    // the sums over rows and pairs.  T^T dT is read: the pair sums go there; T is read: the row sums go there
+    float *sX = bdV, *part = bO;  // part: [late, early, db][8 column groups][64]
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            float s[3] = {late[i][hh], early[i][hh], db[i][hh]};
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                s[k] += __shfl_xor_sync(0xffffffffu, s[k], 1);
+                s[k] += __shfl_xor_sync(0xffffffffu, s[k], 2);
+                if (t4 == 0) part[(k * 8 + (warp >> 1)) * C + r0 + 16 * i + 8 * hh + g] = s[k];
+            }
+        }
+    tf32::each<2, 1>([&](int i, int j, int e, int r, int c) { sX[(r0 + r) * LC + c1 + c] = X[i][j][e]; });
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+    if (lane == 0) sred[warp] = dot;
+    __syncthreads();
+    // sX[r][t] <- sum over i <= t of row r (a warp per four rows, two columns per lane)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float *row = sX + (4 * warp + i) * LC + 2 * lane;
+        const float a = row[0], b = row[1];
+        float s = a + b;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const float o = __shfl_up_sync(0xffffffffu, s, m);
+            if (lane >= m) s += o;
+        }
+        row[0] = s - b;
+        row[1] = s;
+    }
+    float *sums = part + 24 * C;  // late, early, db [64] each
+    if (tid < 3 * C) {
+        const int k = tid / C, r = tid % C;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) s += part[(k * 8 + w) * C + r];
+        sums[tid] = s;
+    }
+    __syncthreads();
+    if (tid < C) {
+        const int t = tid;
+        float s = 0.f, before = 0.f, pairs = 0.f, d = 0.f;
+        for (int r = t; r < C; ++r) {
+            s += sums[r];
+            pairs += t > 0 ? sX[r * LC + t - 1] : 0.f;
+        }
+        for (int i = 0; i < t; ++i) before += sums[C + i];
+#pragma unroll
+        for (int w = 0; w < 16; ++w) d += sred[w];
+        const float dg = s + pairs + before + seG[C - 1] * d;
+        if (t < len) {
+            const int64_t at = u.row0 + (int64_t)t * p.H;
+            p.dbeta[at] = sums[2 * C + t];
+            if (p.log_decay) {  // a clamped input has no gradient
+                const float x = p.log_decay[at];
+                p.dz[at] = (x >= p.g_min && x <= 0.f) ? dg : 0.f;
+            } else {  // d sigmoid(z)/dz = e / (1 + e)^2, e = e^{-|z|}: no cancellation where sigmoid is near 1
+                const float e = expf(-fabsf(load_elem((const T *)p.z, at)));
+                p.dz[at] = dg * p.g_min * e / ((1.f + e) * (1.f + e));
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+size_t gdn_bwd_workspace(int64_t B, int64_t S, int H, int Dk, int Dv) {
+    return (size_t)B * H * ((S + C - 1) / C) * (size_t)make_rec(Dk, Dv).size * sizeof(float);
+}
+
+template <typename T>
+kda_status_t gb_launch(const GbArgs &p, int64_t nbh, cudaStream_t st) {
+    const int64_t units = nbh * p.Nc, jobs = 2 * nbh * p.nslice;
+    cudaFuncSetAttribute(gb_prep_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PREP_SMEM);
+    cudaFuncSetAttribute(gb_chain_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain_smem<T>());
+    cudaFuncSetAttribute(gb_grad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GRAD_SMEM);
+    // 16-byte pieces of the token rows of q and k
+    const int wide = p.Dk * (int)sizeof(T) % 16 == 0 && aligned_to(p.q, 16) && aligned_to(p.k, 16);
+    gb_prep_kernel<T><<<(unsigned)units, NT_P, PREP_SMEM, st>>>(p);
+    KDA_TRY(check_launch("gb_prep_kernel"));
+    gb_chain_kernel<T><<<(unsigned)jobs, NT_C, chain_smem<T>(), st>>>(p, wide);
+    KDA_TRY(check_launch("gb_chain_kernel"));
+    gb_grad_kernel<T><<<(unsigned)units, NT_P, GRAD_SMEM, st>>>(p);
+    return check_launch("gb_grad_kernel");
+}
+
+kda_status_t gb_validate(const kda_recurrent_bwd_args *a) {
+    if (!a) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
+    KDA_TRY(check_dtype(a->dtype));
+    KDA_TRY(check_gmin(a->g_min));
+    if (a->B < 0 || a->S < 0 || a->H < 1 || a->D_k < 1 || a->D_v < 1)
+        return fail(KDA_ERR_INVALID_ARG, "bad sizes B=%lld S=%lld H=%d D_k=%d D_v=%d", (long long)a->B, (long long)a->S,
+                    a->H, a->D_k, a->D_v);
+    if (a->D_k > 128 || a->D_v > 128)
+        return fail(KDA_ERR_UNSUPPORTED, "D_k and D_v must be <= 128 (got %d, %d)", a->D_k, a->D_v);
+    // one CTA per (b, h, chunk), and two per (b, h, 16 value columns)
+    const int64_t nc = a->S / C + (a->S % C != 0), most = nc > 16 ? nc : 16;
+    if (a->B > 0 && (a->B > 0x7fffffffLL / a->H || a->B * a->H > 0x7fffffffLL / most))
+        return fail(KDA_ERR_UNSUPPORTED, "gdn backward: B*H*max(chunks, 16) exceeds 2^31 - 1");
+    return KDA_OK;
+}
+
+}  // namespace
+
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+kda_status_t kda_gdn_chunk_bwd_workspace_size(const kda_recurrent_bwd_args *a, size_t *bytes) {
+    clear_error();
+    if (!bytes) return fail(KDA_ERR_INVALID_ARG, "bytes is NULL");
+    KDA_TRY(gb_validate(a));
+    *bytes = gdn_bwd_workspace(a->B, a->S, a->H, a->D_k, a->D_v);
+    return KDA_OK;
+}
+
+kda_status_t kda_gdn_chunk_bwd(const kda_recurrent_bwd_args *a) {
+    clear_error();
+    KDA_TRY(gb_validate(a));
+    if (a->B == 0) return KDA_OK;
+    const size_t need = gdn_bwd_workspace(a->B, a->S, a->H, a->D_k, a->D_v);
+    KDA_TRY(bwd_check_buffers(a, need, true));
+    cudaStream_t st = (cudaStream_t)a->stream;
+    const int64_t nbh = a->B * a->H;
+    GbArgs p;
+    p.S = a->S;
+    p.H = a->H;
+    p.Dk = a->D_k;
+    p.Dv = a->D_v;
+    p.Nc = (int)((a->S + C - 1) / C);
+    p.nslice = pad16(a->D_v) / VS;
+    p.q = a->q; p.k = a->k; p.v = a->v; p.z = a->z; p.beta = a->beta; p.dO = a->d_o;
+    p.log_decay = a->log_decay;
+    p.g_min = a->g_min;
+    p.S0 = a->initial_state;
+    p.dST = a->d_final_state;
+    p.dq = a->dq; p.dk = a->dk; p.dv = a->dv; p.dbeta = a->dbeta; p.dz = a->dz; p.dS0 = a->d_initial_state;
+    p.ws = reinterpret_cast<float *>(a->workspace);
+    p.ws_bytes = need;
+    p.ns_bytes = (size_t)nbh * a->D_k * a->D_v * 4;
+    p.bounds = device_bounds_counter();
+    if (a->S == 0) {  // no token: the state's gradient passes through
+        if (a->d_initial_state) {
+            const cudaError_t e = a->d_final_state
+                                      ? cudaMemcpyAsync(a->d_initial_state, a->d_final_state, p.ns_bytes,
+                                                        cudaMemcpyDeviceToDevice, st)
+                                      : cudaMemsetAsync(a->d_initial_state, 0, p.ns_bytes, st);
+            if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "gdn backward: %s", cudaGetErrorString(e));
+        }
+        return KDA_OK;
+    }
+    return a->dtype == KDA_F32 ? gb_launch<float>(p, nbh, st) : gb_launch<__nv_bfloat16>(p, nbh, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,125 @@
+// Products of shared-memory tiles to fp32 accuracy on the tensor cores, for the per-chunk algebra of the
+// gated delta rule's gradients: warp-level mma.m16n8k8 with tf32 operands.
+//
+// A tf32 operand has 11 significant bits.  An fp32 value x is split into hi = x rounded to tf32 and
+// lo = x - hi (exact), and a product becomes hi hi' + hi lo' + lo hi': what is left out is below 2^-21 of
+// the product.  An operand that tf32 holds exactly (bf16 values) has no lo, and its products are one (both
+// exact) or two instructions.  Accumulation is fp32.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+namespace tf32 {
+
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// x = hi + lo, hi rounded to the nearest tf32 (the carry of the added half step goes into the exponent)
+__device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+
+__device__ __forceinline__ void load2(const float *p, float &x, float &y) {
+    const float2 t = *reinterpret_cast<const float2 *>(p);
+    x = t.x;
+    y = t.y;
+}
+__device__ __forceinline__ void load2(const __nv_bfloat16 *p, float &x, float &y) {
+    const uint32_t t = *reinterpret_cast<const uint32_t *>(p);
+    x = __uint_as_float(t << 16);
+    y = __uint_as_float(t & 0xffff0000u);
+}
+
+// acc += A B^T over k0 <= k < k1 (multiples of 8), for a warp's MT x 16 rows and NT x 8 columns:
+// acc[i][j] holds (16i + g, 8j + 2t), (.., + 1), (16i + g + 8, ..), (.., + 1) with g = lane / 4, t = lane % 4.
+//   A(m, k) = A[m * lda + k], or A[k * lda + m] with AT;  B(n, k) = B[n * ldb + k], or B[k * ldb + n] with BT.
+// AEX / BEX: tf32 holds the operand exactly.  The order of k within an instruction is free, as long as A and
+// B share it: where an operand is contiguous in k, a lane takes neighbouring k (one 8-byte load).
+// Pitches of 8 mod 32 floats make the reads free of bank conflicts (mixed orientations: two-way).
+// CROSS: the lo terms go to accumulators of their own (shorter dependent chains where a warp has few tiles).
+template <int MT, int NT, bool AT, bool BT, bool AEX, bool BEX, bool CROSS = false, typename TA, typename TB>
+__device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int lda, const TB *B, int ldb, int k0,
+                                     int k1) {
+    constexpr bool PAIR = !(AT && BT);
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float cross[CROSS ? MT : 1][CROSS ? NT : 1][4] = {};
+#pragma unroll 2
+    for (int k = k0; k < k1; k += 8) {
+        const int ka = PAIR ? k + 2 * t : k + t, kb = PAIR ? ka + 1 : ka + 4;
+        uint32_t ah[MT][4], al[MT][4], bh[NT][2], bl[NT][2];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            float x[4];
+            if (AT) {
+                const TA *p = A + ka * lda + 16 * i + g, *q = A + kb * lda + 16 * i + g;
+                x[0] = load_elem(p, 0);
+                x[1] = load_elem(p, 8);
+                x[2] = load_elem(q, 0);
+                x[3] = load_elem(q, 8);
+            } else if (PAIR) {
+                load2(A + (16 * i + g) * lda + ka, x[0], x[2]);
+                load2(A + (16 * i + g + 8) * lda + ka, x[1], x[3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (AEX) ah[i][e] = __float_as_uint(x[e]);
+                else split(x[e], ah[i][e], al[i][e]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            float x[2];
+            if (BT) {
+                x[0] = load_elem(B, ka * ldb + 8 * j + g);
+                x[1] = load_elem(B, kb * ldb + 8 * j + g);
+            } else {
+                load2(B + (8 * j + g) * ldb + ka, x[0], x[1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (BEX) bh[j][e] = __float_as_uint(x[e]);
+                else split(x[e], bh[j][e], bl[j][e]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                if (!BEX) mma(CROSS ? cross[CROSS ? i : 0][CROSS ? j : 0] : acc[i][j], ah[i], bl[j]);
+                if (!AEX) mma(CROSS ? cross[CROSS ? i : 0][CROSS ? j : 0] : acc[i][j], al[i], bh[j]);
+            }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma(acc[i][j], ah[i], bh[j]);
+    }
+    if (CROSS && !(AEX && BEX)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] += cross[CROSS ? i : 0][CROSS ? j : 0][e];
+    }
+}
+
+// Calls f(i, j, e, row, column) for every element of a warp's tile.
+template <int MT, int NT, typename F>
+__device__ __forceinline__ void each(F &&f) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f(i, j, e, 16 * i + g + (e >> 1) * 8, 8 * j + 2 * t + (e & 1));
+}
+
+}  // namespace tf32
+}  // namespace kda

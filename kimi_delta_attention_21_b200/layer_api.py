@@ -1,7 +1,7 @@
 """Torch-facing binding of the operators around the gated delta rule: argument marshalling only.
 
 The norm of queries and keys with the rotation by position and its gradients;
-the gated delta rule token by token; the output path in e4m3.
+the gated delta rule token by token and its gradients; the output path in e4m3.
 Every step runs inside libkda's CUDA kernels, on the current stream of the
 tensors' device (which need not be the current device).
 """
@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import GdnDecodeArgs, QkNormArgs, QkNormBwdArgs, check
+from ._lib import GdnDecodeArgs, QkNormArgs, QkNormBwdArgs, RecBwdArgs, check
 from .api import _DT, _ptr
 
 NORMS = {"l2": _lib.NORM_L2, "rms": _lib.NORM_RMS}
@@ -198,6 +198,41 @@ def gdn_decode_step(q, k, v, beta, state, *, z=None, log_decay=None, g_min=-5.0,
                       _ptr(log_decay), g_min, beta.data_ptr(), state.data_ptr(), _ptr(slots), _ptr(gate_logits), eps,
                       out.data_ptr(), _ptr(dev_status), _stream_of(dev))
     _call("kda_gdn_decode_step", dev, ctypes.byref(a))
+    return out
+
+
+def gdn_chunk_bwd(q, k, v, beta, d_o, *, z=None, log_decay=None, g_min=-5.0, initial_state=None, d_final_state=None,
+                  want_d_initial_state=True, workspace=None):
+    """Gradients of the gated delta rule (kda_gdn_chunk_bwd), the core output o~ of ``gdn_chunk_fwd``: given d_o = dL/do~
+    (B,S,H,D_v) and d_final_state = dL/dS_T (B,H,D_k,D_v) or None, a dict of fp32 tensors dq, dk (B,S,H,D_k), dv
+    (B,S,H,D_v), dbeta and dz (or dlog_decay) (B,S,H), d_initial_state (or None).  z / log_decay: (B,S,H)."""
+    dev, dt = _cuda(q, "q").device, q.dtype
+    code = _code(q, "q")
+    B, S, H, Dk = q.shape
+    Dv = v.shape[-1]
+    _need(q, "q", dev, dt, q.shape)
+    _need(k, "k", dev, dt, q.shape)
+    _need(v, "v", dev, dt, (B, S, H, Dv))
+    if beta.dim() == 4 and beta.shape[-1] == 1:
+        beta = beta.view(B, S, H)
+    _need(beta, "beta", dev, dt, (B, S, H))
+    _need(d_o, "d_o", dev, dt, (B, S, H, Dv))
+    _need(z, "z", dev, dt, (B, S, H))
+    _need(log_decay, "log_decay", dev, torch.float32, (B, S, H))
+    _need(initial_state, "initial_state", dev, torch.float32, (B, H, Dk, Dv))
+    _need(d_final_state, "d_final_state", dev, torch.float32, (B, H, Dk, Dv))
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = {"dq": torch.empty(q.shape, **f32), "dk": torch.empty(q.shape, **f32), "dv": torch.empty(v.shape, **f32),
+           "dbeta": torch.empty((B, S, H), **f32), "dz": torch.empty((B, S, H), **f32),
+           "d_initial_state": torch.empty((B, H, Dk, Dv), **f32) if want_d_initial_state else None}
+    a = RecBwdArgs(B, S, H, Dk, Dv, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(z), _ptr(log_decay), g_min,
+                   beta.data_ptr(), _ptr(initial_state), d_o.data_ptr(), _ptr(d_final_state), out["dq"].data_ptr(),
+                   out["dk"].data_ptr(), out["dv"].data_ptr(), out["dbeta"].data_ptr(), out["dz"].data_ptr(),
+                   _ptr(out["d_initial_state"]), None, 0, _stream_of(dev))
+    ws = _workspace("kda_gdn_chunk_bwd", dev, a, workspace)  # noqa: F841 (alive until the call has been queued)
+    _call("kda_gdn_chunk_bwd", dev, ctypes.byref(a))
+    if log_decay is not None:
+        out["dlog_decay"] = out.pop("dz")
     return out
 
 

@@ -144,3 +144,32 @@ def test_fp8_refusals():
     p(bad, y=P[0])
     p(bad, y=P[4] + 1)
     p(L.KDA_OK, N=0)
+
+
+def gdn_bwd(**kw):
+    a = dict(B=1, S=130, H=2, D_k=32, D_v=48, dtype=L.KDA_BF16, q=P[0], k=P[1], v=P[2], z=P[3], g_min=-5.0, beta=P[4],
+             d_o=P[5], dq=P[6], dk=P[7], dv=P[8], dbeta=P[9], dz=P[10], workspace=P[11], workspace_bytes=1 << 29)
+    a.update(kw)
+    return L.RecBwdArgs(**a)
+
+
+@pytest.mark.parametrize("mut,status", [
+    (dict(dtype=4), L.KDA_ERR_UNSUPPORTED), (dict(g_min=0.5), L.KDA_ERR_INVALID_ARG), (dict(S=-1), L.KDA_ERR_INVALID_ARG),
+    (dict(D_k=129), L.KDA_ERR_UNSUPPORTED), (dict(S=64 << 28, H=16), L.KDA_ERR_UNSUPPORTED),
+    (dict(B=1 << 28, S=1, H=1), L.KDA_ERR_UNSUPPORTED), (dict(d_o=None), L.KDA_ERR_INVALID_ARG),
+    (dict(z=None), L.KDA_ERR_INVALID_ARG), (dict(dz=None), L.KDA_ERR_INVALID_ARG),
+    (dict(workspace_bytes=1000), L.KDA_ERR_WORKSPACE), (dict(workspace=None), L.KDA_ERR_WORKSPACE),
+    (dict(workspace=P[11] + 16), L.KDA_ERR_INVALID_ARG), (dict(dq=P[0]), L.KDA_ERR_INVALID_ARG),
+    (dict(dz=P[9] + 16), L.KDA_ERR_INVALID_ARG), (dict(d_initial_state=P[11] + 1024), L.KDA_ERR_INVALID_ARG),
+])
+def test_gdn_bwd_refusals(mut, status):
+    refused("kda_gdn_chunk_bwd", gdn_bwd(**mut), status)
+
+
+@pytest.mark.parametrize("B,S,H,Dk,Dv", [(1, 4096, 16, 128, 128), (2, 100, 3, 18, 13), (0, 5, 1, 8, 8), (2, 0, 1, 8, 8)])
+def test_gdn_bwd_workspace_is_one_record_per_chunk(B, S, H, Dk, Dv):
+    n, r16 = ctypes.c_size_t(1), lambda x: -(-x // 16) * 16
+    a = gdn_bwd(B=B, S=S, H=H, D_k=Dk, D_v=Dv)
+    assert L.load().kda_gdn_chunk_bwd_workspace_size(ctypes.byref(a), ctypes.byref(n)) == L.KDA_OK
+    dk, dv = r16(Dk), r16(Dv)
+    assert n.value == B * H * -(-S // 64) * 4 * (256 + 12288 + 64 * (dk + 2 * dv) + 2 * dk * dv)
