@@ -97,6 +97,82 @@ __global__ void __launch_bounds__(256) quant_tiles_kernel(const T *__restrict__ 
 }
 
 // ---------------------------------------------------------------- norm, gate and quantisation
+// sigmoid by the fast exponential and quotient: off by (2 + 1.2 |x|) units in the last place of fp32
+__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+template <typename T> struct Q8Vec;
+template <> struct Q8Vec<float> {
+    static constexpr int N = 4;
+    __device__ static void unpack(const uint4 &u, float (&f)[4]) {
+        f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
+        f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+    }
+};
+template <> struct Q8Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ static void unpack(const uint4 &u, float (&f)[8]) {
+        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(v[i] << 16);
+            f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+        }
+    }
+};
+
+// D_v = 8 (fp32: 4) .. 128, a power of two: a block of 128 channels holds whole heads.  A group of 128 / VEC
+// lanes per block, 16 bytes of o and of the gate per lane; `hl` lanes share a head's norm.  Four blocks per group
+// are in flight together.  2 * es + 1 bytes per channel pass HBM; about 30 instructions per channel would take the
+// SMs as long, which is why the sigmoid is the fast one and the division by the scale a product with its inverse.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_gate_fp8_vec_kernel(const T *__restrict__ o, const T *__restrict__ gate,
+                                                                int64_t N, int K, int nb, int hl, float inv_dv,
+                                                                float eps, uint8_t *__restrict__ out,
+                                                                float *__restrict__ scales) {
+    sm100::pdl_trigger();
+    sm100::pdl_wait();
+    constexpr int VEC = Q8Vec<T>::N, G = 128 / VEC, PER = 256 / G, U = 4;
+    const int lane = threadIdx.x & (G - 1);
+    const int64_t units = N * nb, u0 = (int64_t)blockIdx.x * (PER * U) + threadIdx.x / G;
+    uint4 ov[U], gv[U];
+    int64_t at[U];
+    bool in[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t unit = u0 + u * PER, tok = unit / nb;
+        const int c = (int)(unit - tok * nb) * 128 + lane * VEC;
+        in[u] = unit < units && c < K;
+        at[u] = tok * K + c;
+        ov[u] = in[u] ? __ldcs(reinterpret_cast<const uint4 *>(o + at[u])) : make_uint4(0, 0, 0, 0);
+        gv[u] = in[u] ? __ldcs(reinterpret_cast<const uint4 *>(gate + at[u])) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float f[VEC], t[VEC];
+        Q8Vec<T>::unpack(ov[u], f);
+        Q8Vec<T>::unpack(gv[u], t);
+        float ss = 0.f, amax = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) ss = fmaf(f[e], f[e], ss);
+        for (int m = hl >> 1; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+        const float inv = rsqrtf(fmaf(ss, inv_dv, eps));
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            f[e] = in[u] ? f[e] * inv * sigmoid_fast(t[e]) : 0.f;  // (an absent row with eps = 0 would be NaN)
+            amax = fmaxf(amax, fabsf(f[e]));
+        }
+        const float s = q8_scale(group_max<G>(amax)), r = 1.0f / s;
+        uint32_t w[VEC / 4];
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) w[e / 4] = q8_pack4(f[e] * r, f[e + 1] * r, f[e + 2] * r, f[e + 3] * r);
+        if (in[u]) {
+            if (VEC == 8) *reinterpret_cast<uint2 *>(out + at[u]) = make_uint2(w[0], w[VEC / 4 - 1]);
+            else *reinterpret_cast<uint32_t *>(out + at[u]) = w[0];
+            if (lane == 0) scales[u0 + u * PER] = s;
+        }
+    }
+}
+
 // Any H and D_v: a CTA per token, first the heads' 1 / rms, then a warp per block of 128 channels.
 template <typename T>
 __global__ void __launch_bounds__(256) norm_gate_fp8_kernel(const T *__restrict__ o, const T *__restrict__ gate, int H,
@@ -123,17 +199,33 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_kernel(const T *__restrict_
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = 128 * u + l + 32 * j;
-            f[j] = c < K ? load_elem(o, base + c) * s_inv[c / Dv] * sigmoid_precise(load_elem(gate, base + c)) : 0.f;
+            f[j] = c < K ? load_elem(o, base + c) * s_inv[c / Dv] * sigmoid_fast(load_elem(gate, base + c)) : 0.f;
             amax = fmaxf(amax, fabsf(f[j]));
         }
-        const float s = q8_scale(group_max<32>(amax));
+        const float s = q8_scale(group_max<32>(amax)), r = 1.0f / s;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = 128 * u + l + 32 * j;
-            if (c < K) out[base + c] = q8_one(f[j] / s);
+            if (c < K) out[base + c] = q8_one(f[j] * r);
         }
         if (l == 0) scales[(int64_t)blockIdx.x * nb + u] = s;
     }
+}
+
+template <typename T>
+cudaError_t ng8_launch(const void *o, const void *gl, int64_t N, int H, int Dv, float eps, void *x8, float *scales,
+                       cudaStream_t st) {
+    constexpr int VEC = Q8Vec<T>::N;
+    const int K = H * Dv, nb = (K + 127) / 128;
+    // whole 16-byte vectors of one head per lane, whole heads per block, aligned rows
+    if (Dv >= VEC && Dv <= 128 && (Dv & (Dv - 1)) == 0 && aligned_to(o, 16) && aligned_to(gl, 16) && aligned_to(x8, VEC)) {
+        const int64_t ctas = (N * nb + 8 * VEC - 1) / (8 * VEC);  // 256 threads: 2 VEC groups of four blocks
+        if (ctas <= 0x7fffffffLL)
+            return launch_pdl(norm_gate_fp8_vec_kernel<T>, dim3((unsigned)ctas), dim3(256), 0, st, (const T *)o,
+                              (const T *)gl, N, K, nb, Dv / VEC, 1.0f / (float)Dv, eps, (uint8_t *)x8, scales);
+    }
+    return launch_pdl(norm_gate_fp8_kernel<T>, dim3((unsigned)N), dim3(256), (size_t)H * 4, st, (const T *)o,
+                      (const T *)gl, H, Dv, eps, (uint8_t *)x8, scales);
 }
 
 }  // namespace
@@ -196,13 +288,8 @@ kda_status_t kda_norm_gate_fp8(const void *o, const void *gl, int64_t N, int32_t
     KDA_TRY(check_no_overlap(Buf{scales, ns, "scales"}, ins, 2));
     if (overlap(x8, n, scales, ns)) return fail(KDA_ERR_INVALID_ARG, "outputs x8 and scales overlap");
     cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e;
-    if (dtype == KDA_F32)
-        e = launch_pdl(norm_gate_fp8_kernel<float>, dim3((unsigned)N), dim3(256), (size_t)H * 4, st, (const float *)o,
-                       (const float *)gl, H, Dv, eps, (uint8_t *)x8, scales);
-    else
-        e = launch_pdl(norm_gate_fp8_kernel<__nv_bfloat16>, dim3((unsigned)N), dim3(256), (size_t)H * 4, st,
-                       (const __nv_bfloat16 *)o, (const __nv_bfloat16 *)gl, H, Dv, eps, (uint8_t *)x8, scales);
+    const cudaError_t e = dtype == KDA_F32 ? ng8_launch<float>(o, gl, N, H, Dv, eps, x8, scales, st)
+                                           : ng8_launch<__nv_bfloat16>(o, gl, N, H, Dv, eps, x8, scales, st);
     if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "norm_gate_fp8: %s", cudaGetErrorString(e));
     return check_launch("norm_gate_fp8");
 }

@@ -377,9 +377,12 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
         if (n + 1 < p.Nc) stage_w(n + 1);
         if (m0 < Dkp) {  // S <- gamma S + K^T (e^D V')
             const float gamma = se[C - 1];
-            tf32::each<1, 2>([&](int i, int j, int e, int, int) { S[i][j][e] *= gamma; });
-            tf32::tile<1, 2, true, true, EX, false>(S, sK + m0, LD, sVp, LV, 0, C);
-            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { sS[(m0 + r) * LS + c] = S[i][j][e]; });
+            float add[1][2][4] = {};  // (its own accumulator: the tensor core truncates as it adds, S is rounded once)
+            tf32::tile<1, 2, true, true, EX, false>(add, sK + m0, LD, sVp, LV, 0, C);
+            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
+                S[i][j][e] = fmaf(gamma, S[i][j][e], add[i][j][e]);
+                sS[(m0 + r) * LS + c] = S[i][j][e];
+            });
         }
     }
 }
@@ -473,9 +476,12 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
         if (n > 0) fetch(n - 1);
         if (m0 < Dkp) {  // dS <- gamma dS_next + Q^T (e^G dO) - W^T dV'
             const float gamma = se[C - 1];
-            tf32::each<1, 2>([&](int i, int j, int e, int, int) { dS[i][j][e] *= gamma; });
-            tf32::tile<1, 2, true, true, EX, false>(dS, sQ + m0, LD, sdO, LV, 0, C);
-            tf32::tile<1, 2, true, true, false, false>(dS, sW + m0, LD, sdV, LV, 0, C);
+            float add[1][2][4] = {}, sub[1][2][4] = {};
+            tf32::tile<1, 2, true, true, EX, false>(add, sQ + m0, LD, sdO, LV, 0, C);
+            tf32::tile<1, 2, true, true, false, false>(sub, sW + m0, LD, sdV, LV, 0, C);
+            tf32::each<1, 2>([&](int i, int j, int e, int, int) {
+                dS[i][j][e] = fmaf(gamma, dS[i][j][e], add[i][j][e] + sub[i][j][e]);
+            });
         }
     }
     if (p.dS0 && in_bounds(p.dS0 + bh * p.Dk * p.Dv, (size_t)p.Dk * p.Dv * 4, p.dS0, p.ns_bytes, p.bounds))

@@ -7,11 +7,13 @@
 // over 128 x BN output tiles:
 //   warp 0       TMA producer: 128 x 128-byte tiles of x and BN x 128-byte tiles of W into a ring of
 //                shared-memory stages (128-byte swizzle);
-//   warp 1       MMA issuer: 4 tcgen05.mma (M = 128, N = BN, K = 32) per block into one of two TMEM
-//                accumulators, alternating by block;
-//   warps 2..9   two warps per TMEM lane quarter, half the columns each: read the block's accumulator,
-//                scale and add it to the tile's sums (BN / 2 registers per thread) while the tensor core
-//                works on the next block; after the last block, through shared memory to y by TMA.
+//   warp 1       MMA issuer: tcgen05.mma (M = 128, K = 32), 4 per block and column part, into 512 / BN TMEM
+//                accumulators in turn; a 256-column one is handed over in two parts, so that adding the
+//                first overlaps the products of the second;
+//   warps 4..11  two warps per TMEM lane quarter, half the columns each: read the block's accumulator,
+//                scale and add it to the tile's sums (BN / 2 registers per thread: the register split below)
+//                while the tensor core works on the next block; after the last block, through shared memory
+//                to y by TMA.
 // A block of a 128 x 256 tile takes the tensor core 512 cycles at the nominal rate; the 32768 additions take
 // the SM's 128 fp32 lanes 256, so the tensor core stays the bound.
 #include <cuda_fp8.h>
@@ -27,7 +29,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int PM = 128, PK = 128, PF_NT = 320;
+constexpr int PM = 128, PK = 128, PF_NT = 384;
 
 // kind::f8f6f4, e4m3 operands (format 0), fp32 accumulation, both K-major
 constexpr uint32_t idesc_e4m3(int M, int N) {
@@ -54,14 +56,22 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void 
 template <int BN> struct P8Cfg {
     static constexpr int STAGES = BN >= 256 ? 4 : (BN >= 128 ? 5 : 7);
     static constexpr uint32_t A_BYTES = PM * PK, B_BYTES = BN * PK, STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr uint32_t TMEM_COLS = 2 * BN;
+    static constexpr int BUFS = 512 / BN;            // TMEM accumulators
+    static constexpr int PARTS = BN >= 256 ? 2 : 1;  // column parts of an accumulator that are handed over separately
     static constexpr uint32_t OUT_BYTES = 8 * 32 * 128;  // each epilogue warp: 32 rows of 128 bytes
     // bytes of a row that an epilogue warp stores at a time: its BN / 2 columns, at most 128 bytes
     template <typename OT> static constexpr int row_bytes() {
         return BN / 2 * (int)sizeof(OT) < 128 ? BN / 2 * (int)sizeof(OT) : 128;
     }
-    static constexpr size_t SMEM = STAGES * STAGE_BYTES + OUT_BYTES + 1024 + 256;
+    static constexpr size_t SMEM = STAGES * STAGE_BYTES + OUT_BYTES + 1024 + 512;
 };
+
+// 32 columns of an accumulator, scaled and added
+template <int HC>
+__device__ __forceinline__ void add_scaled(float (&acc)[HC], int c, const uint32_t (&r)[32], float s) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(s, __uint_as_float(r[j]), acc[c + j]);
+}
 
 template <int BN, typename OT>
 __global__ void __launch_bounds__(PF_NT, 1)
@@ -72,14 +82,15 @@ proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     pdl_wait();
     using Cfg = P8Cfg<BN>;
     constexpr int ST = Cfg::STAGES, HC = BN / 2;  // columns per epilogue warp
+    constexpr int NB = Cfg::BUFS, NP = Cfg::PARTS, PN = BN / NP;
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smraw + ((1024u - (static_cast<uint32_t>(__cvta_generic_to_shared(smraw)) & 1023u)) & 1023u);
     uint8_t *sA = sm, *sB = sm + ST * Cfg::A_BYTES, *sY = sm + ST * Cfg::STAGE_BYTES;
     uint64_t *full = reinterpret_cast<uint64_t *>(sY + Cfg::OUT_BYTES);
     uint64_t *empty = full + ST;
-    uint64_t *acc_full = empty + ST;     // [2] MMA -> epilogue
-    uint64_t *acc_empty = acc_full + 2;  // [2] epilogue -> MMA
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    uint64_t *acc_full = empty + ST;           // [NB][NP] MMA -> epilogue
+    uint64_t *acc_empty = acc_full + NB * NP;  // [NB][NP] epilogue -> MMA
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + NB * NP);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles_m = (M + PM - 1) / PM, tiles_n = (N + BN - 1) / BN, tiles = tiles_m * tiles_n;
@@ -89,9 +100,9 @@ proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < NB * NP; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);  // one arrival per epilogue warp
+            mbar_init(&acc_empty[b], 8 / NP);  // one arrival per epilogue warp that reads it
         }
         fence_barrier_init();
         prefetch_tensormap(&tmA);
@@ -99,7 +110,7 @@ proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         prefetch_tensormap(&tmY);
     }
     if (warp == 0) {
-        tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
+        tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -116,48 +127,59 @@ proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         n0 = (rem / rows) * BN;
     };
 
-    if (warp == 0 && lane == 0) {
-        int it = 0;
-        for (int t = blockIdx.x; t < tiles && !timed_out; t += gridDim.x) {
-            int m0, n0;
-            tile_mn(t, m0, n0);
-            for (int kb = 0; kb < KB; ++kb, ++it) {
-                const int s = it % ST;
-                if (it >= ST && !mbar_wait(&empty[s], ((it / ST) - 1) & 1)) {
-                    timed_out = true;
-                    break;
+    if (warp < 4) {
+        // registers: 384 threads x 168 at launch = 128 x 72 + 256 x 216
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 0 && lane == 0) {
+            int it = 0;
+            for (int t = blockIdx.x; t < tiles && !timed_out; t += gridDim.x) {
+                int m0, n0;
+                tile_mn(t, m0, n0);
+                for (int kb = 0; kb < KB; ++kb, ++it) {
+                    const int s = it % ST;
+                    if (it >= ST && !mbar_wait(&empty[s], ((it / ST) - 1) & 1)) {
+                        timed_out = true;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
+                    tma_load_2d(sA + s * Cfg::A_BYTES, &tmA, &full[s], kb * PK, m0);
+                    tma_load_2d(sB + s * Cfg::B_BYTES, &tmB, &full[s], kb * PK, n0);
                 }
-                mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
-                tma_load_2d(sA + s * Cfg::A_BYTES, &tmA, &full[s], kb * PK, m0);
-                tma_load_2d(sB + s * Cfg::B_BYTES, &tmB, &full[s], kb * PK, n0);
             }
-        }
-        if (timed_out)  // let the copies already issued land before the CTA can exit
-            for (int j = (it > ST ? it - ST : 0); j < it; ++j) mbar_wait(&full[j % ST], (j / ST) & 1);
-    } else if (warp == 1 && lane == 0) {
-        constexpr uint32_t idesc = idesc_e4m3(PM, BN);
-        int it = 0;
-        for (int t = blockIdx.x; t < tiles && !timed_out; t += gridDim.x) {
-            for (int kb = 0; kb < KB; ++kb, ++it) {
-                const int s = it % ST, buf = it & 1;
-                // the accumulator was read (two blocks ago) and the operands are there
-                if ((it >= 2 && !mbar_wait(&acc_empty[buf], ((it >> 1) - 1) & 1)) ||
-                    !mbar_wait(&full[s], (it / ST) & 1)) {
-                    timed_out = true;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d = tmem + buf * BN;
-                const uint64_t ad = smem_desc(smem_u32(sA + s * Cfg::A_BYTES), 16, 1024, LAYOUT_SW128);
-                const uint64_t bd = smem_desc(smem_u32(sB + s * Cfg::B_BYTES), 16, 1024, LAYOUT_SW128);
+            if (timed_out)  // let the copies already issued land before the CTA can exit
+                for (int j = (it > ST ? it - ST : 0); j < it; ++j) mbar_wait(&full[j % ST], (j / ST) & 1);
+        } else if (warp == 1 && lane == 0) {
+            constexpr uint32_t idesc = idesc_e4m3(PM, PN);
+            int it = 0;
+            for (int t = blockIdx.x; t < tiles && !timed_out; t += gridDim.x) {
+                for (int kb = 0; kb < KB && !timed_out; ++kb, ++it) {
+                    const int s = it % ST, buf = it % NB;
+                    if (!mbar_wait(&full[s], (it / ST) & 1)) {
+                        timed_out = true;
+                        break;
+                    }
+                    const uint64_t ad = smem_desc(smem_u32(sA + s * Cfg::A_BYTES), 16, 1024, LAYOUT_SW128);
+                    const uint64_t bd = smem_desc(smem_u32(sB + s * Cfg::B_BYTES), 16, 1024, LAYOUT_SW128);
 #pragma unroll
-                for (int k = 0; k < PK / 32; ++k) mma_f8_ss(d, ad + (uint64_t)(k * 2), bd + (uint64_t)(k * 2), idesc, k != 0);
-                mma_commit(&empty[s]);
-                mma_commit(&acc_full[buf]);
+                    for (int h = 0; h < NP; ++h) {  // the accumulator's part was read (NB blocks ago)
+                        if (it >= NB && !mbar_wait(&acc_empty[buf * NP + h], ((it / NB) - 1) & 1)) {
+                            timed_out = true;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < PK / 32; ++k)
+                            mma_f8_ss(tmem + buf * BN + h * PN, ad + (uint64_t)(k * 2),
+                                      bd + (uint64_t)(k * 2 + h * PN * PK / 16), idesc, k != 0);
+                        mma_commit(&acc_full[buf * NP + h]);
+                    }
+                    mma_commit(&empty[s]);
+                }
             }
         }
-    } else if (warp >= 2) {
-        const int e = warp - 2, q = warp & 3, half = e >> 2;  // lane quarter (fixed by the warp), column half
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int e = warp - 4, q = warp & 3, half = e >> 2;  // lane quarter (fixed by the warp), column half
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         uint8_t *out = sY + e * 4096;
         int it = 0;
@@ -172,28 +194,43 @@ proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             for (int i = 0; i < HC; ++i) acc[i] = 0.f;
             float sx = xr[0], sw = wr[0];
             for (int kb = 0; kb < KB; ++kb, ++it) {
-                const int buf = it & 1;
+                const int buf = it % NB, bar = buf * NP + (NP == 2 ? half : 0);
                 const float s = sx * sw;
                 if (kb + 1 < KB) {  // the next block's scales, while this block is waited for
                     sx = xr[kb + 1];
                     sw = wr[kb + 1];
                 }
-                if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (it >> 1) & 1))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[bar], (it / NB) & 1))) {
                     timed_out = true;
                     break;
                 }
                 tc_fence_after();
+                const uint32_t ta = tmem + lane_base + buf * BN + half * HC;
+                // 32 columns at a time, the next 32 on their way while these are added
+                uint32_t r0[32], r1[32];
+                tmem_ld_32x32b_x32(ta, r0);
+                tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < HC; c += 32) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(tmem + lane_base + buf * BN + half * HC + c, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(s, __uint_as_float(r[j]), acc[c + j]);
+                for (int c = 0; c < HC; c += 64) {
+                    if (c + 32 < HC) tmem_ld_32x32b_x32(ta + c + 32, r1);
+                    add_scaled<HC>(acc, c, r0, s);
+                    if (c + 32 < HC) {
+                        tmem_wait_ld();
+                        if (c + 64 < HC) tmem_ld_32x32b_x32(ta + c + 64, r0);
+                        if (c + 64 >= HC) {  // the last load has landed: the accumulator can be written again
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&acc_empty[bar]);
+                        }
+                        add_scaled<HC>(acc, c + 32, r1, s);
+                        if (c + 64 < HC) tmem_wait_ld();
+                    }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                if (HC == 32) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_empty[bar]);
+                }
             }
             if (timed_out) break;
             // the warp's 32 rows, up to 128 bytes of columns at a time, in the swizzle of the store's map: the
@@ -233,7 +270,7 @@ proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, Cfg::TMEM_COLS);
+    if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------- any K, any alignment

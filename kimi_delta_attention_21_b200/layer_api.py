@@ -13,9 +13,17 @@ import torch
 
 from . import _lib
 from ._lib import GdnDecodeArgs, QkNormArgs, QkNormBwdArgs, RecBwdArgs, check
-from .api import _DT, _ptr
+from .api import _DT
 
 NORMS = {"l2": _lib.NORM_L2, "rms": _lib.NORM_RMS}
+
+
+# These calls can take a few microseconds on the GPU, so the marshalling keeps its own share small: tensors by
+# empty_like (the cheapest allocation call), raw addresses, and the raw stream without a Stream object around it.
+_CONTIGUOUS = torch.contiguous_format
+_empty_like = torch.empty_like
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _code(t, name):
@@ -32,7 +40,7 @@ def _cuda(t, name):
 
 
 def _need(t, name, device, dtype, shape, contiguous=True):
-    """Checks an optional tensor (None passes) and returns it."""
+    """Checks an optional tensor (None passes) and returns its address."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor) or t.device != device:
@@ -43,13 +51,17 @@ def _need(t, name, device, dtype, shape, contiguous=True):
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
+    return t.data_ptr()
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _call(name, device, *args):
     """Calls an entry point with `device` current, and raises on a status other than KDA_OK."""
     fn = getattr(_lib.load(), name)
-    if torch.cuda.current_device() == device.index:
+    if _current_device() == device.index:
         st = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -65,50 +77,52 @@ def _workspace(entry, device, args, given):
     if not n.value:
         return None
     ws = given if given is not None else torch.empty(n.value, dtype=torch.uint8, device=device)
-    _need(ws, "workspace", device, torch.uint8, ws.shape)
-    args.workspace = ws.data_ptr()
+    args.workspace = _need(ws, "workspace", device, torch.uint8, ws.shape)
     args.workspace_bytes = ws.numel()
     return ws
-
-
-def _stream_of(device):
-    return torch.cuda.current_stream(device).cuda_stream
 
 
 # ---------------------------------------------------------------- norms of queries and keys
 def _token_strides(t, name):
     """(B, S, H, D) of a (B, S, H, D) or (S, H, D) tensor and its token strides; heads and channels contiguous."""
-    if t.dim() not in (3, 4):
-        raise ValueError(f"{name} must have shape (B, S, H, D) or (S, H, D) (got {tuple(t.shape)})")
-    H, D = t.shape[-2:]
-    if (D > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != D):
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 4:
+        (B, S, H, D), (b, s, h, d) = shape, stride
+    elif len(shape) == 3:
+        (S, H, D), (s, h, d), B, b = shape, stride, 1, 0
+    else:
+        raise ValueError(f"{name} must have shape (B, S, H, D) or (S, H, D) (got {tuple(shape)})")
+    if (d != 1 and D > 1) or (h != D and H > 1):
         raise ValueError(f"{name}: the heads and channels of a token must be contiguous")
-    B, S = (1, t.shape[0]) if t.dim() == 3 else t.shape[:2]
-    return B, S, H, D, (t.stride(0) if t.dim() == 4 and B > 1 else 0), (t.stride(-3) if S > 1 else 0)
+    return B, S, H, D, (b if B > 1 else 0), (s if S > 1 else 0)
 
 
 def _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleaved):
     dev, dt = _cuda(q, "q").device, q.dtype
     code = _code(q, "q")
     B, S, Hq, D, qb, qs = _token_strides(q, "q")
-    _need(k, "k", dev, dt, (*q.shape[:-2], k.shape[-2], D), contiguous=False)
-    Hk, kb, ks = (_token_strides(k, "k")[i] for i in (2, 4, 5))
-    _need(q_weight, "q_weight", dev, torch.float32, (D,))
-    _need(k_weight, "k_weight", dev, torch.float32, (D,))
+    if not isinstance(k, torch.Tensor) or k.device != dev:
+        raise ValueError(f"k must be a tensor on {dev}")
+    if k.dtype != dt:
+        raise TypeError(f"k must be {dt} (got {k.dtype})")
+    kB, kS, Hk, kD, kb, ks = _token_strides(k, "k")
+    if kB != B or kS != S or kD != D or k.dim() != q.dim():
+        raise ValueError(f"k's shape {tuple(k.shape)} does not go with q's {tuple(q.shape)}")
+    qw = None if q_weight is None else _need(q_weight, "q_weight", dev, torch.float32, (D,))
+    kw = None if k_weight is None else _need(k_weight, "k_weight", dev, torch.float32, (D,))
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
-    rot = 0
+    rot, pos, inv = 0, None, None
     if inv_freq is not None:
-        _need(positions, "positions", dev, torch.int64, q.shape[:-2])
-        _need(inv_freq, "inv_freq", dev, torch.float32, (inv_freq.numel(),))
-        rot = 2 * inv_freq.numel()
-    try:
-        kind = NORMS[norm]
-    except KeyError:
-        raise ValueError(f"norm must be one of {sorted(NORMS)} (got {norm!r})") from None
-    return QkNormArgs(B, S, Hq, Hk, D, code, q.data_ptr(), k.data_ptr(), qb, qs, kb, ks, kind, eps, _ptr(q_weight),
-                      _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot, bool(interleaved), None, None,
-                      _stream_of(dev))
+        n = inv_freq.numel()
+        pos = _need(positions, "positions", dev, torch.int64, (B, S) if q.dim() == 4 else (S,))
+        inv = _need(inv_freq, "inv_freq", dev, torch.float32, (n,))
+        rot = 2 * n
+    kind = NORMS.get(norm)
+    if kind is None:
+        raise ValueError(f"norm must be one of {sorted(NORMS)} (got {norm!r})")
+    return QkNormArgs(B, S, Hq, Hk, D, code, q.data_ptr(), k.data_ptr(), qb, qs, kb, ks, kind, eps, qw, kw, pos, inv, rot,
+                      bool(interleaved), None, None, _raw_stream(dev.index))
 
 
 def qk_norm(q, k, *, norm="l2", eps=1e-6, q_weight=None, k_weight=None, positions=None, inv_freq=None,
@@ -125,14 +139,11 @@ def qk_norm(q, k, *, norm="l2", eps=1e-6, q_weight=None, k_weight=None, position
     a = _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleaved)
     dev = q.device
     if out_q is None:
-        out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    else:
-        _need(out_q, "out_q", dev, q.dtype, q.shape)
+        out_q = _empty_like(q, memory_format=_CONTIGUOUS)
     if out_k is None:
-        out_k = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    else:
-        _need(out_k, "out_k", dev, q.dtype, k.shape)
-    a.q_out, a.k_out = out_q.data_ptr(), out_k.data_ptr()
+        out_k = _empty_like(k, memory_format=_CONTIGUOUS)
+    a.q_out = _need(out_q, "out_q", dev, q.dtype, q.shape)
+    a.k_out = _need(out_k, "out_k", dev, q.dtype, k.shape)
     _call("kda_qk_norm_fwd", dev, ctypes.byref(a))
     return out_q, out_k
 
@@ -147,13 +158,11 @@ def qk_norm_bwd(q, k, dq_out, dk_out, *, norm="l2", eps=1e-6, q_weight=None, k_w
     gt = _cuda(dq_out, "dq_out").dtype
     if gt not in (torch.float32, q.dtype):
         raise TypeError(f"dq_out must be float32 or {q.dtype} (got {gt})")
-    _need(dq_out, "dq_out", dev, gt, q.shape)
-    _need(dk_out, "dk_out", dev, gt, k.shape)
-    out = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev), "dk": torch.empty(k.shape, dtype=q.dtype, device=dev),
-           "dq_weight": None if q_weight is None else torch.empty_like(q_weight),
-           "dk_weight": None if k_weight is None else torch.empty_like(k_weight)}
-    a = QkNormBwdArgs(f, _DT[gt], _ptr(dq_out), _ptr(dk_out), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dq_weight"]),
-                      _ptr(out["dk_weight"]), None, 0)
+    out = {"dq": _empty_like(q, memory_format=_CONTIGUOUS), "dk": _empty_like(k, memory_format=_CONTIGUOUS),
+           "dq_weight": None if q_weight is None else _empty_like(q_weight),
+           "dk_weight": None if k_weight is None else _empty_like(k_weight)}
+    a = QkNormBwdArgs(f, _DT[gt], _need(dq_out, "dq_out", dev, gt, q.shape), _need(dk_out, "dk_out", dev, gt, k.shape),
+                      out["dq"].data_ptr(), out["dk"].data_ptr(), _addr(out["dq_weight"]), _addr(out["dk_weight"]), None, 0)
     ws = _workspace("kda_qk_norm_bwd", dev, a, workspace)  # noqa: F841 (alive until the call has been queued)
     _call("kda_qk_norm_bwd", dev, ctypes.byref(a))
     return out
@@ -175,28 +184,25 @@ def gdn_decode_step(q, k, v, beta, state, *, z=None, log_decay=None, g_min=-5.0,
     code = _code(q, "q")
     if q.dim() not in (3, 4):
         raise ValueError(f"q must have shape (B, H, D_k) or (B, T, H, D_k) (got {tuple(q.shape)})")
-    lead = q.shape[:-1]
+    lead, Dk, Dv = q.shape[:-1], q.shape[-1], v.shape[-1]
     B, T, H = (lead[0], 1, lead[1]) if q.dim() == 3 else lead
-    Dk, Dv = q.shape[-1], v.shape[-1]
-    _need(q, "q", dev, dt, q.shape)
-    _need(k, "k", dev, dt, q.shape)
-    _need(v, "v", dev, dt, (*lead, Dv))
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    vec = (*lead, Dv)
     if beta.dim() == len(lead) + 1 and beta.shape[-1] == 1:
         beta = beta.view(lead)
-    _need(beta, "beta", dev, dt, lead)
-    _need(z, "z", dev, dt, lead)
-    _need(log_decay, "log_decay", dev, torch.float32, lead)
-    _need(gate_logits, "gate_logits", dev, dt, (*lead, Dv))
-    _need(slots, "slots", dev, torch.int32, (B,))
-    _need(state, "state", dev, torch.float32, (state.shape[0], H, Dk, Dv))
-    _need(dev_status, "dev_status", dev, torch.int32, dev_status.shape if dev_status is not None else ())
     if out is None:
-        out = torch.empty((*lead, Dv), dtype=dt, device=dev)
-    else:
-        _need(out, "out", dev, dt, (*lead, Dv))
-    a = GdnDecodeArgs(B, state.shape[0], T, H, Dk, Dv, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(z),
-                      _ptr(log_decay), g_min, beta.data_ptr(), state.data_ptr(), _ptr(slots), _ptr(gate_logits), eps,
-                      out.data_ptr(), _ptr(dev_status), _stream_of(dev))
+        out = _empty_like(v)
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must have shape (num_slots, H, D_k, D_v)")
+    n = state.shape[0]
+    a = GdnDecodeArgs(B, n, T, H, Dk, Dv, code, q.data_ptr(), _need(k, "k", dev, dt, q.shape), _need(v, "v", dev, dt, vec),
+                      _need(z, "z", dev, dt, lead), _need(log_decay, "log_decay", dev, torch.float32, lead), g_min,
+                      _need(beta, "beta", dev, dt, lead), _need(state, "state", dev, torch.float32, (n, H, Dk, Dv)),
+                      _need(slots, "slots", dev, torch.int32, (B,)), _need(gate_logits, "gate_logits", dev, dt, vec), eps,
+                      _need(out, "out", dev, dt, vec),
+                      None if dev_status is None else _need(dev_status, "dev_status", dev, torch.int32, dev_status.shape),
+                      _raw_stream(dev.index))
     _call("kda_gdn_decode_step", dev, ctypes.byref(a))
     return out
 
@@ -210,25 +216,20 @@ def gdn_chunk_bwd(q, k, v, beta, d_o, *, z=None, log_decay=None, g_min=-5.0, ini
     code = _code(q, "q")
     B, S, H, Dk = q.shape
     Dv = v.shape[-1]
-    _need(q, "q", dev, dt, q.shape)
-    _need(k, "k", dev, dt, q.shape)
-    _need(v, "v", dev, dt, (B, S, H, Dv))
     if beta.dim() == 4 and beta.shape[-1] == 1:
         beta = beta.view(B, S, H)
-    _need(beta, "beta", dev, dt, (B, S, H))
-    _need(d_o, "d_o", dev, dt, (B, S, H, Dv))
-    _need(z, "z", dev, dt, (B, S, H))
-    _need(log_decay, "log_decay", dev, torch.float32, (B, S, H))
-    _need(initial_state, "initial_state", dev, torch.float32, (B, H, Dk, Dv))
-    _need(d_final_state, "d_final_state", dev, torch.float32, (B, H, Dk, Dv))
-    f32 = dict(dtype=torch.float32, device=dev)
-    out = {"dq": torch.empty(q.shape, **f32), "dk": torch.empty(q.shape, **f32), "dv": torch.empty(v.shape, **f32),
-           "dbeta": torch.empty((B, S, H), **f32), "dz": torch.empty((B, S, H), **f32),
-           "d_initial_state": torch.empty((B, H, Dk, Dv), **f32) if want_d_initial_state else None}
-    a = RecBwdArgs(B, S, H, Dk, Dv, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(z), _ptr(log_decay), g_min,
-                   beta.data_ptr(), _ptr(initial_state), d_o.data_ptr(), _ptr(d_final_state), out["dq"].data_ptr(),
-                   out["dk"].data_ptr(), out["dv"].data_ptr(), out["dbeta"].data_ptr(), out["dz"].data_ptr(),
-                   _ptr(out["d_initial_state"]), None, 0, _stream_of(dev))
+    tok, val, st, f32 = (B, S, H), (B, S, H, Dv), (B, H, Dk, Dv), torch.float32
+    addr = {n: _need(t, n, dev, dt, shape) for n, t, shape in (("q", q, q.shape), ("k", k, q.shape), ("v", v, val),
+                                                              ("z", z, tok), ("beta", beta, tok), ("d_o", d_o, val))}
+    out = {"dq": _empty_like(q, dtype=f32), "dk": _empty_like(k, dtype=f32), "dv": _empty_like(v, dtype=f32),
+           "dbeta": _empty_like(beta, dtype=f32), "dz": _empty_like(beta, dtype=f32),
+           "d_initial_state": torch.empty(st, dtype=f32, device=dev) if want_d_initial_state else None}
+    a = RecBwdArgs(B, S, H, Dk, Dv, code, addr["q"], addr["k"], addr["v"], addr["z"],
+                   _need(log_decay, "log_decay", dev, f32, tok), g_min, addr["beta"],
+                   _need(initial_state, "initial_state", dev, f32, st), addr["d_o"],
+                   _need(d_final_state, "d_final_state", dev, f32, st), out["dq"].data_ptr(), out["dk"].data_ptr(),
+                   out["dv"].data_ptr(), out["dbeta"].data_ptr(), out["dz"].data_ptr(), _addr(out["d_initial_state"]),
+                   None, 0, _raw_stream(dev.index))
     ws = _workspace("kda_gdn_chunk_bwd", dev, a, workspace)  # noqa: F841 (alive until the call has been queued)
     _call("kda_gdn_chunk_bwd", dev, ctypes.byref(a))
     if log_decay is not None:
@@ -252,7 +253,7 @@ def quant_fp8(x, block_rows=1):
     x8 = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
     shape = (*x.shape[:-1], kb) if block_rows == 1 else (-(-rows // block_rows) if block_rows > 0 else 0, kb)
     scales = torch.empty(shape, dtype=torch.float32, device=dev)
-    _call("kda_quant_fp8", dev, x.data_ptr(), code, rows, K, block_rows, x8.data_ptr(), scales.data_ptr(), _stream_of(dev))
+    _call("kda_quant_fp8", dev, x.data_ptr(), code, rows, K, block_rows, x8.data_ptr(), scales.data_ptr(), _raw_stream(dev.index))
     return x8, scales
 
 
@@ -261,15 +262,14 @@ def norm_gate_fp8(o, gate_logits, eps=1e-6):
     (..., H, D_v).  Returns (x8 (..., H * D_v), scales (..., ceil(H * D_v / 128))) for ``out_proj_fp8``."""
     dev = _cuda(o, "o").device
     code = _code(o, "o")
-    _need(o, "o", dev, o.dtype, o.shape)
-    _need(gate_logits, "gate_logits", dev, o.dtype, o.shape)
+    po, pg = _need(o, "o", dev, o.dtype, o.shape), _need(gate_logits, "gate_logits", dev, o.dtype, o.shape)
     H, Dv = o.shape[-2:]
     lead, K = o.shape[:-2], H * Dv
-    x8 = torch.empty((*lead, K), dtype=torch.float8_e4m3fn, device=dev)
-    scales = torch.empty((*lead, -(-K // 128)), dtype=torch.float32, device=dev)
-    N = x8.numel() // K if K else 0
-    _call("kda_norm_gate_fp8", dev, o.data_ptr(), gate_logits.data_ptr(), N, H, Dv, eps, code, x8.data_ptr(),
-          scales.data_ptr(), _stream_of(dev))
+    x8 = o.new_empty((*lead, K), dtype=torch.float8_e4m3fn)
+    scales = o.new_empty((*lead, -(-K // 128)), dtype=torch.float32)
+    N = o.numel() // K if K else 0
+    _call("kda_norm_gate_fp8", dev, po, pg, N, H, Dv, eps, code, x8.data_ptr(), scales.data_ptr(),
+          _raw_stream(dev.index))
     return x8, scales
 
 
@@ -281,17 +281,16 @@ def out_proj_fp8(x8, x_scale, W8, W_scale, out_dtype=torch.bfloat16, out=None):
     Dm, K = W8.shape
     kb = -(-K // 128)
     lead = x8.shape[:-1]
-    _need(x8, "x8", dev, torch.float8_e4m3fn, (*lead, K))
-    _need(x_scale, "x_scale", dev, torch.float32, (*lead, kb))
-    _need(W8, "W8", dev, torch.float8_e4m3fn, (Dm, K))
-    _need(W_scale, "W_scale", dev, torch.float32, (-(-Dm // 128), kb))
-    if out_dtype not in _DT:
+    px = _need(x8, "x8", dev, torch.float8_e4m3fn, (*lead, K))
+    ps = _need(x_scale, "x_scale", dev, torch.float32, (*lead, kb))
+    pw = _need(W8, "W8", dev, torch.float8_e4m3fn, (Dm, K))
+    pv = _need(W_scale, "W_scale", dev, torch.float32, (-(-Dm // 128), kb))
+    code = _DT.get(out_dtype)
+    if code is None:
         raise TypeError(f"out_dtype must be float32 or bfloat16 (got {out_dtype})")
     if out is None:
-        out = torch.empty((*lead, Dm), dtype=out_dtype, device=dev)
-    else:
-        _need(out, "out", dev, out_dtype, (*lead, Dm))
+        out = x_scale.new_empty((*lead, Dm), dtype=out_dtype)
+    py = _need(out, "out", dev, out_dtype, (*lead, Dm))
     N = x8.numel() // K if K else 0
-    _call("kda_out_proj_fp8", dev, x8.data_ptr(), x_scale.data_ptr(), W8.data_ptr(), W_scale.data_ptr(), N, K, Dm,
-          out.data_ptr(), _DT[out_dtype], _stream_of(dev))
+    _call("kda_out_proj_fp8", dev, px, ps, pw, pv, N, K, Dm, py, code, _raw_stream(dev.index))
     return out
