@@ -7,9 +7,8 @@
 // over 128 x BN output tiles:
 //   warp 0       TMA producer: 128 x 128-byte tiles of x and BN x 128-byte tiles of W into a ring of
 //                shared-memory stages (128-byte swizzle);
-//   warp 1       MMA issuer: tcgen05.mma (M = 128, K = 32), 4 per block and column part, into 512 / BN TMEM
-//                accumulators in turn; a 256-column one is handed over in two parts, so that adding the
-//                first overlaps the products of the second;
+//   warp 1       MMA issuer: 4 tcgen05.mma (M = 128, N = BN, K = 32) per block, into 512 / BN TMEM
+//                accumulators in turn;
 //   warps 4..11  two warps per TMEM lane quarter, half the columns each: read the block's accumulator,
 //                scale and add it to the tile's sums (BN / 2 registers per thread: the register split below)
 //                while the tensor core works on the next block; after the last block, through shared memory
@@ -57,7 +56,6 @@ template <int BN> struct P8Cfg {
     static constexpr int STAGES = BN >= 256 ? 4 : (BN >= 128 ? 5 : 7);
     static constexpr uint32_t A_BYTES = PM * PK, B_BYTES = BN * PK, STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int BUFS = 512 / BN;            // TMEM accumulators
-    static constexpr int PARTS = BN >= 256 ? 2 : 1;  // column parts of an accumulator that are handed over separately
     static constexpr uint32_t OUT_BYTES = 8 * 32 * 128;  // each epilogue warp: 32 rows of 128 bytes
     // bytes of a row that an epilogue warp stores at a time: its BN / 2 columns, at most 128 bytes
     template <typename OT> static constexpr int row_bytes() {
@@ -66,11 +64,17 @@ template <int BN> struct P8Cfg {
     static constexpr size_t SMEM = STAGES * STAGE_BYTES + OUT_BYTES + 1024 + 512;
 };
 
-// 32 columns of an accumulator, scaled and added
+// 32 columns of an accumulator, scaled and added: two per instruction, which leaves the other warps twice the issue
+// slots (with single fmas 16384 x 4096 x 4096 took 279 us, so 255 us)
 template <int HC>
 __device__ __forceinline__ void add_scaled(float (&acc)[HC], int c, const uint32_t (&r)[32], float s) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(s, __uint_as_float(r[j]), acc[c + j]);
+    for (int j = 0; j < 32; j += 2)
+        asm("{\n\t.reg .b64 a, b, d;\n\t"
+            "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 d, {%0, %1};\n\t"
+            "fma.rn.f32x2 d, a, b, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
+            : "+f"(acc[c + j]), "+f"(acc[c + j + 1])
+            : "r"(r[j]), "r"(r[j + 1]), "f"(s));
 }
 
 template <int BN, typename OT>
@@ -82,15 +86,15 @@ proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     pdl_wait();
     using Cfg = P8Cfg<BN>;
     constexpr int ST = Cfg::STAGES, HC = BN / 2;  // columns per epilogue warp
-    constexpr int NB = Cfg::BUFS, NP = Cfg::PARTS, PN = BN / NP;
+    constexpr int NB = Cfg::BUFS;
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smraw + ((1024u - (static_cast<uint32_t>(__cvta_generic_to_shared(smraw)) & 1023u)) & 1023u);
     uint8_t *sA = sm, *sB = sm + ST * Cfg::A_BYTES, *sY = sm + ST * Cfg::STAGE_BYTES;
     uint64_t *full = reinterpret_cast<uint64_t *>(sY + Cfg::OUT_BYTES);
     uint64_t *empty = full + ST;
-    uint64_t *acc_full = empty + ST;           // [NB][NP] MMA -> epilogue
-    uint64_t *acc_empty = acc_full + NB * NP;  // [NB][NP] epilogue -> MMA
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + NB * NP);
+    uint64_t *acc_full = empty + ST;      // [NB] MMA -> epilogue
+    uint64_t *acc_empty = acc_full + NB;  // [NB] epilogue -> MMA
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + NB);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles_m = (M + PM - 1) / PM, tiles_n = (N + BN - 1) / BN, tiles = tiles_m * tiles_n;
@@ -100,9 +104,9 @@ proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < NB * NP; ++b) {
+        for (int b = 0; b < NB; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8 / NP);  // one arrival per epilogue warp that reads it
+            mbar_init(&acc_empty[b], 8);  // one arrival per epilogue warp
         }
         fence_barrier_init();
         prefetch_tensormap(&tmA);
@@ -149,30 +153,24 @@ proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             if (timed_out)  // let the copies already issued land before the CTA can exit
                 for (int j = (it > ST ? it - ST : 0); j < it; ++j) mbar_wait(&full[j % ST], (j / ST) & 1);
         } else if (warp == 1 && lane == 0) {
-            constexpr uint32_t idesc = idesc_e4m3(PM, PN);
+            constexpr uint32_t idesc = idesc_e4m3(PM, BN);
             int it = 0;
             for (int t = blockIdx.x; t < tiles && !timed_out; t += gridDim.x) {
-                for (int kb = 0; kb < KB && !timed_out; ++kb, ++it) {
+                for (int kb = 0; kb < KB; ++kb, ++it) {
                     const int s = it % ST, buf = it % NB;
-                    if (!mbar_wait(&full[s], (it / ST) & 1)) {
+                    // the accumulator was read (NB blocks ago), and the operands are there
+                    if ((it >= NB && !mbar_wait(&acc_empty[buf], ((it / NB) - 1) & 1)) ||
+                        !mbar_wait(&full[s], (it / ST) & 1)) {
                         timed_out = true;
                         break;
                     }
+                    tc_fence_after();
                     const uint64_t ad = smem_desc(smem_u32(sA + s * Cfg::A_BYTES), 16, 1024, LAYOUT_SW128);
                     const uint64_t bd = smem_desc(smem_u32(sB + s * Cfg::B_BYTES), 16, 1024, LAYOUT_SW128);
 #pragma unroll
-                    for (int h = 0; h < NP; ++h) {  // the accumulator's part was read (NB blocks ago)
-                        if (it >= NB && !mbar_wait(&acc_empty[buf * NP + h], ((it / NB) - 1) & 1)) {
-                            timed_out = true;
-                            break;
-                        }
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = 0; k < PK / 32; ++k)
-                            mma_f8_ss(tmem + buf * BN + h * PN, ad + (uint64_t)(k * 2),
-                                      bd + (uint64_t)(k * 2 + h * PN * PK / 16), idesc, k != 0);
-                        mma_commit(&acc_full[buf * NP + h]);
-                    }
+                    for (int k = 0; k < PK / 32; ++k)
+                        mma_f8_ss(tmem + buf * BN, ad + (uint64_t)(k * 2), bd + (uint64_t)(k * 2), idesc, k != 0);
+                    mma_commit(&acc_full[buf]);
                     mma_commit(&empty[s]);
                 }
             }
@@ -192,45 +190,61 @@ proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             float acc[HC];
 #pragma unroll
             for (int i = 0; i < HC; ++i) acc[i] = 0.f;
-            float sx = xr[0], sw = wr[0];
-            for (int kb = 0; kb < KB; ++kb, ++it) {
-                const int buf = it % NB, bar = buf * NP + (NP == 2 ? half : 0);
-                const float s = sx * sw;
-                if (kb + 1 < KB) {  // the next block's scales, while this block is waited for
-                    sx = xr[kb + 1];
-                    sw = wr[kb + 1];
-                }
-                if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[bar], (it / NB) & 1))) {
-                    timed_out = true;
-                    break;
-                }
+            // 32 columns at a time: while they are added, the next 32 are on their way, those of the next block too
+            constexpr int NC = HC / 32;
+            static_assert(NC == 1 || NC % 2 == 0, "two register buffers in turn");
+            uint32_t r0[32], r1[32];
+            auto ready = [&](int i) {  // waits for block i's accumulator
+                if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[i % NB], (i / NB) & 1))) timed_out = true;
                 tc_fence_after();
-                const uint32_t ta = tmem + lane_base + buf * BN + half * HC;
-                // 32 columns at a time, the next 32 on their way while these are added
-                uint32_t r0[32], r1[32];
-                tmem_ld_32x32b_x32(ta, r0);
-                tmem_wait_ld();
+            };
+            auto load = [&](int i, int c, uint32_t(&r)[32]) {
+                tmem_ld_32x32b_x32(tmem + lane_base + (i % NB) * BN + half * HC + 32 * c, r);
+            };
+            auto release = [&](int i) {  // everything of block i's accumulator has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[i % NB]);
+            };
+            float s = xr[0] * wr[0];
+            ready(it);
+            if (timed_out) break;
+            load(it, 0, r0);
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                const bool more = kb + 1 < KB;
+                const float sx = more ? xr[kb + 1] : 0.f, sw = more ? wr[kb + 1] : 0.f;
+                if (NC == 1) {
+                    tmem_wait_ld();
+                    release(it);
 #pragma unroll
-                for (int c = 0; c < HC; c += 64) {
-                    if (c + 32 < HC) tmem_ld_32x32b_x32(ta + c + 32, r1);
-                    add_scaled<HC>(acc, c, r0, s);
-                    if (c + 32 < HC) {
-                        tmem_wait_ld();
-                        if (c + 64 < HC) tmem_ld_32x32b_x32(ta + c + 64, r0);
-                        if (c + 64 >= HC) {  // the last load has landed: the accumulator can be written again
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&acc_empty[bar]);
-                        }
-                        add_scaled<HC>(acc, c + 32, r1, s);
-                        if (c + 64 < HC) tmem_wait_ld();
+                    for (int j = 0; j < 32; ++j) r1[j] = r0[j];
+                    if (more) {
+                        ready(it + 1);
+                        if (timed_out) break;
+                        load(it + 1, 0, r0);
                     }
+                    add_scaled<HC>(acc, 0, r1, s);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < NC; c += 2) {
+                        tmem_wait_ld();
+                        load(it, c + 1, r1);
+                        add_scaled<HC>(acc, 32 * c, r0, s);
+                        tmem_wait_ld();
+                        if (c + 2 < NC) {
+                            load(it, c + 2, r0);
+                        } else {
+                            release(it);
+                            if (more) {
+                                ready(it + 1);
+                                if (!timed_out) load(it + 1, 0, r0);
+                            }
+                        }
+                        add_scaled<HC>(acc, 32 * (c + 1), r1, s);
+                    }
+                    if (timed_out) break;
                 }
-                if (HC == 32) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&acc_empty[bar]);
-                }
+                s = sx * sw;
             }
             if (timed_out) break;
             // the warp's 32 rows, up to 128 bytes of columns at a time, in the swizzle of the store's map: the
