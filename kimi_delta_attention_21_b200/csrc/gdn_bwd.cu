@@ -23,7 +23,7 @@
 // neighbours would be off by 1e-5.  No factor e^{-G} is ever formed, so any g_min works.
 //
 // Three launches: gb_prep (a CTA per chunk: P, M, T, W, U into a workspace record), gb_chain (a CTA per
-// (b, h, 16 value columns) and direction: the state forward, which leaves S and V' of every chunk, and at the
+// (b, h, 32 value columns) and direction: the state forward, which leaves S and V' of every chunk, and at the
 // same time its gradient backward, which leaves dS_next and dV': the two do not depend on each other), and
 // gb_grad (a CTA per chunk: everything else).  All products run on the tensor cores to fp32 accuracy
 // (mma_tf32.cuh); bf16 inputs are exact operands there and cost a third less, which is why the scale factors
@@ -40,14 +40,16 @@ constexpr int C = 64;       // tokens per chunk
 constexpr int LD = 136;     // pitch of [64 or 128][D] tiles in shared memory: 8 mod 32
 constexpr int LC = 72;      // pitch of [64][64] tiles
 constexpr int NT_P = 512;   // threads of the per-chunk kernels
-constexpr int NT_C = 256;   // threads of the chain kernel
-constexpr int VS = 16;      // value columns per chain CTA
-constexpr int LS = 20, LV = 24;  // chain pitches of [Dk][16] and [64][16] tiles (conflict-free reads by k)
+constexpr int NT_C = 512;   // threads of the chain kernel
+constexpr int VS = 32;      // value columns per chain CTA
+// chain pitches (conflict-free reads by k): split [Dk][32] and [64][32] tiles, plain [64][32]
+constexpr int LS = 34, LV = 36, LO = 40;
 
 __host__ __device__ inline int pad16(int x) { return (x + 15) & ~15; }
+__host__ __device__ inline int pad32(int x) { return (x + 31) & ~31; }
 
-// One (b, h, chunk) record; offsets in floats, all blocks whole 64-byte rows.  D_k and D_v are padded to
-// multiples of 16; the padding holds zeros.
+// One (b, h, chunk) record; offsets in floats, all blocks whole 64-byte rows.  D_k is padded to a
+// multiple of 16, D_v to one of 32; the padding holds zeros.
 struct Rec {
     int64_t G;          // [64] double
     int64_t eG, eD;     // [64] e^G, e^{G_last - G}
@@ -60,7 +62,7 @@ struct Rec {
 };
 
 __host__ __device__ inline Rec make_rec(int Dk, int Dv) {
-    const int64_t dk = pad16(Dk), dv = pad16(Dv);
+    const int64_t dk = pad16(Dk), dv = pad32(Dv);
     Rec r;
     r.G = 0;
     r.eG = 2 * C;
@@ -80,6 +82,8 @@ __host__ __device__ inline Rec make_rec(int Dk, int Dv) {
 struct GbArgs {
     int64_t S;
     int H, Dk, Dv, Nc, nslice;
+    bool wide_k, wide_v;  // 16-byte vectors in the token rows of q and k, of v and dO
+    bool pair_k, pair_v;  // 8-byte pairs in the rows of dq and dk, of dv
     const void *q, *k, *v, *z, *beta, *dO;
     const float *log_decay;
     float g_min;
@@ -105,53 +109,97 @@ __device__ __forceinline__ Unit unit_of(const GbArgs &p, int64_t bh, int n) {
     return u;
 }
 
-// Token rows (rs elements apart) as fp32 into [64][ld], zero past `len` rows and D columns up to Dp; eight
-// loads in flight per thread.
+// Token rows (rs elements apart) as fp32 into [64][ld], zero past `len` rows and D columns up to Dp.  wide: D is a
+// multiple of a 16-byte vector and every row starts on 16 bytes; a thread's loads are all in flight together.
 template <typename T, int NT>
-__device__ __forceinline__ void load_rows(float *dst, int ld, const T *src, int64_t rs, int len, int D, int Dp) {
-    const int n = C * Dp;
-    for (int base = threadIdx.x; base < n; base += 8 * NT) {
-        float v[8];
+__device__ __forceinline__ void load_rows(float *dst, int ld, const T *src, int64_t rs, int len, int D, int Dp, bool wide) {
+    constexpr int E = 16 / (int)sizeof(T), VPR = 128 / E;  // vectors of a full row
+    if (wide) {
+        constexpr int U = C * VPR / NT;
+        uint4 v[U];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int i = base + u * NT, r = i / Dp, c = i - r * Dp;
-            v[u] = (i < n && r < len && c < D) ? load_elem(src, (int64_t)r * rs + c) : 0.f;
+        for (int u = 0; u < U; ++u) {
+            const int i = threadIdx.x + u * NT, r = i / VPR, c = i % VPR * E;
+            v[u] = (r < len && c < D) ? *reinterpret_cast<const uint4 *>(src + (int64_t)r * rs + c) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int i = base + u * NT, r = i / Dp, c = i - r * Dp;
-            if (i < n) dst[r * ld + c] = v[u];
+        for (int u = 0; u < U; ++u) {
+            const int i = threadIdx.x + u * NT, r = i / VPR, c = i % VPR * E;
+            if (c >= Dp) continue;
+            float4 *d = reinterpret_cast<float4 *>(dst + r * ld + c);
+            if (sizeof(T) == 4) {
+                *d = make_float4(__uint_as_float(v[u].x), __uint_as_float(v[u].y), __uint_as_float(v[u].z),
+                                 __uint_as_float(v[u].w));
+            } else {
+                d[0] = make_float4(__uint_as_float(v[u].x << 16), __uint_as_float(v[u].x & 0xffff0000u),
+                                   __uint_as_float(v[u].y << 16), __uint_as_float(v[u].y & 0xffff0000u));
+                d[1] = make_float4(__uint_as_float(v[u].z << 16), __uint_as_float(v[u].z & 0xffff0000u),
+                                   __uint_as_float(v[u].w << 16), __uint_as_float(v[u].w & 0xffff0000u));
+            }
         }
+        return;
     }
+    const int c = threadIdx.x & 127;
+    if (c >= Dp) return;
+#pragma unroll 8
+    for (int r = threadIdx.x >> 7; r < C; r += NT / 128)
+        dst[r * ld + c] = (r < len && c < D) ? load_elem(src, (int64_t)r * rs + c) : 0.f;
 }
 
 // The same rows kept in their type, by cp.async where 16-byte pieces are possible.
 template <typename T>
 __device__ __forceinline__ void stage_rows(T *dst, const T *src, int64_t rs, int len, int D, int Dp, bool wide) {
-    constexpr int E = 16 / (int)sizeof(T);
-    if (wide) {  // D is a multiple of E, every row starts on 16 bytes
-        const int W = Dp / E, n = C * W;
-        for (int i = threadIdx.x; i < n; i += NT_C) {
-            const int r = i / W, c = (i - r * W) * E;
+    if (wide) {
+        constexpr int E = 16 / (int)sizeof(T), VPR = 128 / E;
+#pragma unroll
+        for (int i = threadIdx.x; i < C * VPR; i += NT_C) {
+            const int r = i / VPR, c = i % VPR * E;
             const bool in = r < len && c < D;
-            cp_async16_fill(reinterpret_cast<float *>(dst + r * LD + c),
-                            reinterpret_cast<const float *>(src + (in ? (int64_t)r * rs + c : 0)), in);
+            if (c < Dp)
+                cp_async16_fill(reinterpret_cast<float *>(dst + r * LD + c),
+                                reinterpret_cast<const float *>(src + (in ? (int64_t)r * rs + c : 0)), in);
         }
         return;
     }
-    for (int i = threadIdx.x; i < C * Dp; i += NT_C) {
-        const int r = i / Dp, c = i - r * Dp;
-        dst[r * LD + c] = (r < len && c < D) ? src[(int64_t)r * rs + c] : T(0.f);
+    const int c = threadIdx.x & 127;
+    if (c < Dp)
+        for (int r = threadIdx.x >> 7; r < C; r += NT_C / 128)
+            dst[r * LD + c] = (r < len && c < D) ? src[(int64_t)r * rs + c] : T(0.f);
+}
+
+// A record block of `rows` rows of `cols` floats (a multiple of 4, at most 4 VPR; pitch `pitch`) into shared memory.
+template <int NT, int VPR>
+__device__ __forceinline__ void stage_block(float *dst, int ld, const float *src, int pitch, int rows, int cols) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < rows * VPR; i += NT) {
+        const int r = i / VPR, c = i % VPR * 4;
+        if (c < cols) cp_async16_fill(dst + r * ld + c, src + (int64_t)r * pitch + c);
     }
 }
 
-// A record block of `rows` rows of `cols` floats (a multiple of 4, pitch `pitch`) into shared memory.
-template <int NT>
-__device__ __forceinline__ void stage_block(float *dst, int ld, const float *src, int pitch, int rows, int cols) {
-    const int W = cols / 4, n = rows * W;
-    for (int i = threadIdx.x; i < n; i += NT) {
-        const int r = i / W, c = (i - r * W) * 4;
-        cp_async16_fill(dst + r * ld + c, src + (int64_t)r * pitch + c);
+// Neighbouring columns c (even) and c + 1 of a token row: zero outside.
+template <typename T>
+__device__ __forceinline__ float2 row_pair(const T *row, int c, int D, bool in, bool wide) {
+    float2 v = make_float2(0.f, 0.f);
+    if (in && c < D) {
+        if (wide) {
+            tf32::load2(row + c, v.x, v.y);
+        } else {
+            v.x = load_elem(row, c);
+            if (c + 1 < D) v.y = load_elem(row, c + 1);
+        }
+    }
+    return v;
+}
+
+// Columns c (even) and c + 1 of an output row.
+__device__ __forceinline__ void store_pair(float *row, int c, int D, bool in, bool pair, float x, float y) {
+    if (!in || c >= D) return;
+    if (pair) {
+        *reinterpret_cast<float2 *>(row + c) = make_float2(x, y);
+    } else {
+        row[c] = x;
+        if (c + 1 < D) row[c + 1] = y;
     }
 }
 
@@ -164,19 +212,19 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
     extern __shared__ __align__(16) uint8_t gb_sm[];
     double *sG = reinterpret_cast<double *>(gb_sm);
     float *sK = reinterpret_cast<float *>(sG + C), *sQ = sK + C * LD, *sV = sQ + C * LD;
-    float *sA = sV + C * LD, *sT = sA + C * LC, *sY = sT + C * LC, *sb = sY + C * LC, *seG = sb + C, *seD = seG + C;
+    float *sA = sV + C * LD, *sT = sA + C * LC, *sY = sT + C * LC, *sb = sY + C * LC, *seG = sb + C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t bh = blockIdx.x / p.Nc;
     const int n = (int)(blockIdx.x - bh * p.Nc);
     const Unit u = unit_of(p, bh, n);
-    const int Dkp = pad16(p.Dk), Dvp = pad16(p.Dv);
+    const int Dkp = pad16(p.Dk), Dvp = pad32(p.Dv);
     const Rec R = make_rec(p.Dk, p.Dv);
     float *rec = p.ws + (int64_t)blockIdx.x * R.size;
     if (!in_bounds(rec, (size_t)R.size * 4, p.ws, p.ws_bytes, p.bounds)) return;
 
-    load_rows<T, NT_P>(sK, LD, (const T *)p.k + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp);
-    load_rows<T, NT_P>(sQ, LD, (const T *)p.q + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp);
-    load_rows<T, NT_P>(sV, LD, (const T *)p.v + u.row0 * p.Dv, (int64_t)p.H * p.Dv, u.len, p.Dv, Dvp);
+    load_rows<T, NT_P>(sK, LD, (const T *)p.k + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, p.wide_k);
+    load_rows<T, NT_P>(sQ, LD, (const T *)p.q + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, p.wide_k);
+    load_rows<T, NT_P>(sV, LD, (const T *)p.v + u.row0 * p.Dv, (int64_t)p.H * p.Dv, u.len, p.Dv, Dvp, p.wide_v);
     if (warp == 0) {  // the cumulative log-decay: two tokens per lane, a scan over the warp
         double g[2];
 #pragma unroll
@@ -227,10 +275,13 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
             r += r0;
             c += c0;
             const float x = c <= r ? expf((float)(sG[r] - sG[c])) : 0.f;
-            const float P = c < r ? kk[i][j][e] * x : 0.f;
-            rec[R.P + r * C + c] = P;
-            rec[R.M + r * C + c] = c <= r ? qk[i][j][e] * x : 0.f;
-            sA[r * LC + c] = sb[r] * P;
+            kk[i][j][e] = c < r ? kk[i][j][e] * x : 0.f;
+            qk[i][j][e] = c <= r ? qk[i][j][e] * x : 0.f;
+            sA[r * LC + c] = sb[r] * kk[i][j][e];
+            if (e & 1) {
+                *reinterpret_cast<float2 *>(rec + R.P + r * C + c - 1) = make_float2(kk[i][j][e - 1], kk[i][j][e]);
+                *reinterpret_cast<float2 *>(rec + R.M + r * C + c - 1) = make_float2(qk[i][j][e - 1], qk[i][j][e]);
+            }
         });
     }
     __syncthreads();
@@ -299,53 +350,65 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
     if (c0 < Dkp) {
         float acc[2][2][4] = {};
         tf32::tile<2, 2, false, true, false, EX>(acc, sA + r0 * LC, LC, sK + c0, LD, 0, r0 + 32);
-        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) { rec[R.W + (r0 + r) * Dkp + c0 + c] = acc[i][j][e]; });
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
+            if (!(e & 1))
+                *reinterpret_cast<float2 *>(rec + R.W + (r0 + r) * Dkp + c0 + c) =
+                    make_float2(acc[i][j][e], acc[i][j][e + 1]);
+        });
     }
     if (c0 < Dvp) {
         float acc[2][2][4] = {};
         tf32::tile<2, 2, false, true, false, EX>(acc, sY + r0 * LC, LC, sV + c0, LD, 0, r0 + 32);
-        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) { rec[R.V + (r0 + r) * Dvp + c0 + c] = acc[i][j][e]; });
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
+            if (!(e & 1))
+                *reinterpret_cast<float2 *>(rec + R.V + (r0 + r) * Dvp + c0 + c) =
+                    make_float2(acc[i][j][e], acc[i][j][e + 1]);
+        });
     }
 }
 
 // ---------------------------------------------------------------- the state and its gradient through the chunks
 template <typename T> constexpr size_t chain_smem() {
-    // backward (the larger): M, W, K, Q, dO, dV', dS, e^G and e^D
-    return sizeof(float) * (C * LC + C * LD + 2 * C * LV + 128 * LS + 2 * C) + 2 * sizeof(T) * C * LD;
+    // backward (the larger): M, W, dO, dO split, dV' split, dS split, e^G and e^D, K, Q
+    return sizeof(float) * (C * LC + C * LD + C * LO + 2 * 2 * C * LV + 2 * 128 * LS + 2 * C) + 2 * sizeof(T) * C * LD;
 }
 
-// Forward: the state stays in the MMA accumulators of the warps (16 key rows each), with a copy in shared
-// memory as the next product's operand.  W and U of the next chunk arrive while K is used, K while W is.
+// 16 warps: [64][32] results as 4 x 2 tiles of 16 x 16, the sum over k shared by two groups of warps; [Dk][32] ones
+// as 8 x 2 tiles.  The operands that several warps read as B are kept split in shared memory.
+
+// Forward: the state stays in the accumulators of the warps that own it, with a split copy in shared memory as the
+// next product's operand.  W and U of the next chunk arrive while K is used, K while W is.
 template <typename T>
-__device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j0, float *sm, bool wide) {
+__device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j0, float *sm) {
     constexpr bool EX = sizeof(T) == 2;
-    float *sW = sm, *sU = sW + C * LD, *sVp = sU + C * VS, *sS = sVp + C * LV, *se = sS + 128 * LS;
-    T *sK = reinterpret_cast<T *>(se + 2 * C);
-    const int tid = threadIdx.x, warp = tid >> 5;
-    const int Dkp = pad16(p.Dk), Dvp = pad16(p.Dv);
+    float *sW = sm, *sU = sW + C * LD, *sY = sU + C * VS, *se = sY + C * LO;
+    float2 *sVp = reinterpret_cast<float2 *>(se + 2 * C), *sS = sVp + C * LV;
+    T *sK = reinterpret_cast<T *>(sS + 128 * LS);
+    const int warp = threadIdx.x >> 5;
+    const int Dkp = pad16(p.Dk), Dvp = pad32(p.Dv);
     const Rec R = make_rec(p.Dk, p.Dv);
-    const int64_t b = bh / p.H;
-    const int h = (int)(bh - b * p.H);
     float *rec0 = p.ws + bh * p.Nc * R.size;
     auto stage_w = [&](int n) {
         const float *rec = rec0 + (int64_t)n * R.size;
-        stage_block<NT_C>(sW, LD, rec + R.W, Dkp, C, Dkp);
-        stage_block<NT_C>(sU, VS, rec + R.V + j0, Dvp, C, VS);
+        stage_block<NT_C, 32>(sW, LD, rec + R.W, Dkp, C, Dkp);
+        stage_block<NT_C, 8>(sU, VS, rec + R.V + j0, Dvp, C, VS);
         cp_async_commit_group();
     };
     auto stage_k = [&](int n) {
         const Unit u = unit_of(p, bh, n);
-        stage_block<NT_C>(se, 2 * C, rec0 + (int64_t)n * R.size + R.eG, 2 * C, 1, 2 * C);
-        stage_rows<T>(sK, (const T *)p.k + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, wide);
+        stage_block<NT_C, 32>(se, 2 * C, rec0 + (int64_t)n * R.size + R.eG, 2 * C, 1, 2 * C);
+        stage_rows<T>(sK, (const T *)p.k + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, p.wide_k);
         cp_async_commit_group();
     };
-    (void)b;
-    (void)h;
-    const int m0 = 16 * warp;  // this warp's key rows
+    const int m0 = 16 * (warp & 7), n0 = 16 * (warp >> 3);                        // this warp's part of the state
+    const int r0 = 16 * (warp & 3), c0 = 16 * ((warp >> 2) & 1), half = warp >> 3;  // and of V', and of its sum
+    const int kmid = (Dkp / 2 + 7) & ~7;
     float S[1][2][4] = {};
     tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
-        if (m0 + r < p.Dk && j0 + c < p.Dv && p.S0) S[i][j][e] = p.S0[(bh * p.Dk + m0 + r) * p.Dv + j0 + c];
-        if (m0 < Dkp) sS[(m0 + r) * LS + c] = S[i][j][e];
+        r += m0;
+        c += n0;
+        if (r < p.Dk && j0 + c < p.Dv && p.S0) S[i][j][e] = p.S0[(bh * p.Dk + r) * p.Dv + j0 + c];
+        if (m0 < Dkp) sS[r * LS + c] = tf32::split2(S[i][j][e]);
     });
     stage_w(0);
     for (int n = 0; n < p.Nc; ++n) {
@@ -356,32 +419,35 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
         if (m0 < Dkp)  // the state entering the chunk
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 if (!(e & 1))
-                    *reinterpret_cast<float2 *>(rec + R.S + (int64_t)(m0 + r) * Dvp + j0 + c) =
+                    *reinterpret_cast<float2 *>(rec + R.S + (int64_t)(m0 + r) * Dvp + j0 + n0 + c) =
                         make_float2(S[i][j][e], S[i][j][e + 1]);
             });
-        float v[1][1][4] = {};
-        const int r0 = 16 * (warp & 3), c0 = 8 * (warp >> 2);
-        tf32::tile<1, 1, false, true, false, false, true>(v, sW + r0 * LD, LD, sS + c0, LS, 0, Dkp);
-        tf32::each<1, 1>([&](int i, int j, int e, int r, int c) { v[i][j][e] = sU[(r0 + r) * VS + c0 + c] - v[i][j][e]; });
+        float v[1][2][4] = {};
+        tf32::tile<1, 2, false, true, false, false, true>(v, sW + r0 * LD, LD, sS + c0, LS, half ? kmid : 0,
+                                                          half ? Dkp : kmid);
+        if (half)
+            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { sY[(r0 + r) * LO + c0 + c] = v[i][j][e]; });
         cp_async_wait<0>();  // K of chunk n
-        tf32::each<1, 1>([&](int i, int j, int e, int r, int c) {
-            if (!(e & 1))
-                *reinterpret_cast<float2 *>(rec + R.V + (int64_t)(r0 + r) * Dvp + j0 + c0 + c) =
-                    make_float2(v[i][j][e], v[i][j][e + 1]);
-        });
-        __syncthreads();  // K and e^D are there for everyone
-        tf32::each<1, 1>([&](int i, int j, int e, int r, int c) {
-            sVp[(r0 + r) * LV + c0 + c] = se[C + r0 + r] * v[i][j][e];  // e^D V'
-        });
+        __syncthreads();     // K, e^D and the other half of the sum
+        if (!half)
+            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
+                r += r0;
+                c += c0;
+                v[i][j][e] = sU[r * VS + c] - (v[i][j][e] + sY[r * LO + c]);
+                sVp[r * LV + c] = tf32::split2(se[C + r] * v[i][j][e]);  // e^D V'
+                if (e & 1)
+                    *reinterpret_cast<float2 *>(rec + R.V + (int64_t)r * Dvp + j0 + c - 1) =
+                        make_float2(v[i][j][e - 1], v[i][j][e]);
+            });
         __syncthreads();
         if (n + 1 < p.Nc) stage_w(n + 1);
         if (m0 < Dkp) {  // S <- gamma S + K^T (e^D V')
             const float gamma = se[C - 1];
             float add[1][2][4] = {};  // (its own accumulator: the tensor core truncates as it adds, S is rounded once)
-            tf32::tile<1, 2, true, true, EX, false>(add, sK + m0, LD, sVp, LV, 0, C);
+            tf32::tile<1, 2, true, true, EX, false, true>(add, sK + m0, LD, sVp + n0, LV, 0, C);
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 S[i][j][e] = fmaf(gamma, S[i][j][e], add[i][j][e]);
-                sS[(m0 + r) * LS + c] = S[i][j][e];
+                sS[(m0 + r) * LS + n0 + c] = tf32::split2(S[i][j][e]);
             });
         }
     }
@@ -390,25 +456,27 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
 // Backward: the same for dS, from the last chunk to the first.  M, K (first half of a step) and Q, W
 // (second half) are refilled with the previous chunk's as soon as their half is done.
 template <typename T>
-__device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int j0, float *sm, bool wide) {
+__device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int j0, float *sm) {
     constexpr bool EX = sizeof(T) == 2;
     constexpr int PER = C * VS / NT_C;
-    float *sM = sm, *sW = sM + C * LC, *sdO = sW + C * LD, *sdV = sdO + C * LV, *sS = sdV + C * LV, *se = sS + 128 * LS;
-    T *sK = reinterpret_cast<T *>(se + 2 * C), *sQ = sK + C * LD;
+    float *sM = sm, *sW = sM + C * LC, *sdO = sW + C * LD, *se = sdO + C * LO;
+    float2 *sgO = reinterpret_cast<float2 *>(se + 2 * C), *sdV = sgO + C * LV, *sS = sdV + C * LV;
+    T *sK = reinterpret_cast<T *>(sS + 128 * LS), *sQ = sK + C * LD;
+    float *sY = reinterpret_cast<float *>(sgO);  // the other half of a sum, before e^G dO takes the place
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int Dkp = pad16(p.Dk), Dvp = pad16(p.Dv);
+    const int Dkp = pad16(p.Dk), Dvp = pad32(p.Dv);
     const Rec R = make_rec(p.Dk, p.Dv);
     float *rec0 = p.ws + bh * p.Nc * R.size;
     auto stage_a = [&](int n) {
         const Unit u = unit_of(p, bh, n);
-        stage_block<NT_C>(sM, LC, rec0 + (int64_t)n * R.size + R.M, C, C, C);
-        stage_rows<T>(sK, (const T *)p.k + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, wide);
+        stage_block<NT_C, 16>(sM, LC, rec0 + (int64_t)n * R.size + R.M, C, C, C);
+        stage_rows<T>(sK, (const T *)p.k + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, p.wide_k);
         cp_async_commit_group();
     };
     auto stage_b = [&](int n) {
         const Unit u = unit_of(p, bh, n);
-        stage_block<NT_C>(sW, LD, rec0 + (int64_t)n * R.size + R.W, Dkp, C, Dkp);
-        stage_rows<T>(sQ, (const T *)p.q + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, wide);
+        stage_block<NT_C, 32>(sW, LD, rec0 + (int64_t)n * R.size + R.W, Dkp, C, Dkp);
+        stage_rows<T>(sQ, (const T *)p.q + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, p.wide_k);
         cp_async_commit_group();
     };
     float pre[PER], pe = 0.f;  // this thread's elements of dO's columns, and its e^G or e^D
@@ -423,10 +491,14 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
         }
         if (tid < 2 * C) pe = rec0[(int64_t)n * R.size + R.eG + tid];
     };
-    const int m0 = 16 * warp;
+    const int m0 = 16 * (warp & 7), n0 = 16 * (warp >> 3);
+    const int r0 = 16 * (warp & 3), c0 = 16 * ((warp >> 2) & 1), half = warp >> 3;
+    const int kmid = (3 * Dkp / 8) & ~7;  // the first group has the product with M, and the smaller part of K dS
     float dS[1][2][4] = {};
     tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
-        if (m0 + r < p.Dk && j0 + c < p.Dv && p.dST) dS[i][j][e] = p.dST[(bh * p.Dk + m0 + r) * p.Dv + j0 + c];
+        r += m0;
+        c += n0;
+        if (r < p.Dk && j0 + c < p.Dv && p.dST) dS[i][j][e] = p.dST[(bh * p.Dk + r) * p.Dv + j0 + c];
     });
     stage_a(p.Nc - 1);
     fetch(p.Nc - 1);
@@ -435,50 +507,55 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
         __syncthreads();  // everyone has left the previous step: its Q, W, dO, dV' and dS are read
         stage_b(n);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) sdO[(tid + i * NT_C) / VS * LV + (tid + i * NT_C) % VS] = pre[i];
+        for (int i = 0; i < PER; ++i) sdO[(tid + i * NT_C) / VS * LO + (tid + i * NT_C) % VS] = pre[i];
         if (tid < 2 * C) se[tid] = pe;
         if (m0 < Dkp)  // the gradient of the state leaving the chunk
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
-                sS[(m0 + r) * LS + c] = dS[i][j][e];
+                sS[(m0 + r) * LS + n0 + c] = tf32::split2(dS[i][j][e]);
                 if (!(e & 1))
-                    *reinterpret_cast<float2 *>(rec + R.dS + (int64_t)(m0 + r) * Dvp + j0 + c) =
+                    *reinterpret_cast<float2 *>(rec + R.dS + (int64_t)(m0 + r) * Dvp + j0 + n0 + c) =
                         make_float2(dS[i][j][e], dS[i][j][e + 1]);
             });
         cp_async_wait<1>();  // M and K of chunk n
         __syncthreads();
-        // dV' = M^T dO + e^D (K dS_next): a warp per 16 rows and 8 columns
-        const int r0 = 16 * (warp & 3), c0 = 8 * (warp >> 2);
-        float v[1][1][4] = {}, x[1][1][4] = {};
-        tf32::tile<1, 1, true, true, false, EX, true>(v, sM + r0, LC, sdO + c0, LV, r0, C);
-        tf32::tile<1, 1, false, true, EX, false, true>(x, sK + r0 * LD, LD, sS + c0, LS, 0, Dkp);
-        tf32::each<1, 1>([&](int i, int j, int e, int r, int c) {
-            v[i][j][e] = fmaf(se[C + r0 + r], x[i][j][e], v[i][j][e]);
-            sdV[(r0 + r) * LV + c0 + c] = -v[i][j][e];
-        });
-        tf32::each<1, 1>([&](int i, int j, int e, int r, int c) {
-            if (!(e & 1))
-                *reinterpret_cast<float2 *>(rec + R.dV + (int64_t)(r0 + r) * Dvp + j0 + c0 + c) =
-                    make_float2(v[i][j][e], v[i][j][e + 1]);
-        });
-        __syncthreads();  // M, K and dO are read
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int r = (tid + i * NT_C) / VS, c = (tid + i * NT_C) % VS;
-            sdO[r * LV + c] = se[r] * pre[i];  // e^G dO
-        }
+        // dV' = M^T dO + e^D (K dS_next)
+        float v[1][2][4] = {}, x[1][2][4] = {};
+        tf32::tile<1, 2, false, true, EX, false, true>(x, sK + r0 * LD, LD, sS + c0, LS, half ? kmid : 0,
+                                                       half ? Dkp : kmid);
+        if (half)
+            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { sY[(r0 + r) * LO + c0 + c] = x[i][j][e]; });
+        else
+            tf32::tile<1, 2, true, true, false, EX, true>(v, sM + r0, LC, sdO + c0, LO, r0, C);
+        __syncthreads();  // M, K and dO are read; the other half of the sum
+        if (!half)
+            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
+                r += r0;
+                c += c0;
+                v[i][j][e] = fmaf(se[C + r], x[i][j][e] + sY[r * LO + c], v[i][j][e]);
+                sdV[r * LV + c] = tf32::split2(-v[i][j][e]);
+                if (e & 1)
+                    *reinterpret_cast<float2 *>(rec + R.dV + (int64_t)r * Dvp + j0 + c - 1) =
+                        make_float2(v[i][j][e - 1], v[i][j][e]);
+            });
         if (n > 0) {
             stage_a(n - 1);
             cp_async_wait<1>();  // Q and W of chunk n
         } else {
             cp_async_wait<0>();
         }
-        __syncthreads();
+        __syncthreads();  // the sums are read: e^G dO over them
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int r = (tid + i * NT_C) / VS, c = (tid + i * NT_C) % VS;
+            sgO[r * LV + c] = tf32::split2(se[r] * pre[i]);
+        }
         if (n > 0) fetch(n - 1);
-        if (m0 < Dkp) {  // dS <- gamma dS_next + Q^T (e^G dO) - W^T dV'
+        float add[1][2][4] = {}, sub[1][2][4] = {};
+        if (m0 < Dkp) tf32::tile<1, 2, true, true, false, false, true>(sub, sW + m0, LD, sdV + n0, LV, 0, C);
+        __syncthreads();  // e^G dO
+        if (m0 < Dkp) {   // dS <- gamma dS_next + Q^T (e^G dO) - W^T dV'
             const float gamma = se[C - 1];
-            float add[1][2][4] = {}, sub[1][2][4] = {};
-            tf32::tile<1, 2, true, true, EX, false>(add, sQ + m0, LD, sdO, LV, 0, C);
-            tf32::tile<1, 2, true, true, false, false>(sub, sW + m0, LD, sdV, LV, 0, C);
+            tf32::tile<1, 2, true, true, EX, false, true>(add, sQ + m0, LD, sgO + n0, LV, 0, C);
             tf32::each<1, 2>([&](int i, int j, int e, int, int) {
                 dS[i][j][e] = fmaf(gamma, dS[i][j][e], add[i][j][e] + sub[i][j][e]);
             });
@@ -486,20 +563,22 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
     }
     if (p.dS0 && in_bounds(p.dS0 + bh * p.Dk * p.Dv, (size_t)p.Dk * p.Dv * 4, p.dS0, p.ns_bytes, p.bounds))
         tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
-            if (m0 + r < p.Dk && j0 + c < p.Dv) p.dS0[(bh * p.Dk + m0 + r) * p.Dv + j0 + c] = dS[i][j][e];
+            r += m0;
+            c += n0;
+            if (r < p.Dk && j0 + c < p.Dv) p.dS0[(bh * p.Dk + r) * p.Dv + j0 + c] = dS[i][j][e];
         });
 }
 
 template <typename T>
-__global__ void __launch_bounds__(NT_C, sizeof(T) == 2 ? 2 : 1) gb_chain_kernel(const __grid_constant__ GbArgs p, int wide) {
+__global__ void __launch_bounds__(NT_C, 1) gb_chain_kernel(const __grid_constant__ GbArgs p) {
     extern __shared__ __align__(16) uint8_t gb_sm[];
     const int64_t job = blockIdx.x >> 1, bh = job / p.nslice;
     const int j0 = (int)(job - bh * p.nslice) * VS;
     const Rec R = make_rec(p.Dk, p.Dv);
     if (!in_bounds(p.ws + bh * p.Nc * R.size, (size_t)p.Nc * R.size * 4, p.ws, p.ws_bytes, p.bounds)) return;
     float *sm = reinterpret_cast<float *>(gb_sm);
-    if (blockIdx.x & 1) chain_forward<T>(p, bh, j0, sm, wide);
-    else chain_backward<T>(p, bh, j0, sm, wide);
+    if (blockIdx.x & 1) chain_forward<T>(p, bh, j0, sm);
+    else chain_backward<T>(p, bh, j0, sm);
 }
 
 // ---------------------------------------------------------------- per chunk: the gradients
@@ -521,18 +600,18 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     const int64_t bh = blockIdx.x / p.Nc;
     const int n = (int)(blockIdx.x - bh * p.Nc);
     const Unit u = unit_of(p, bh, n);
-    const int Dk = p.Dk, Dv = p.Dv, Dkp = pad16(Dk), Dvp = pad16(Dv), len = u.len;
+    const int Dk = p.Dk, Dv = p.Dv, Dkp = pad16(Dk), Dvp = pad32(Dv), len = u.len;
     const Rec R = make_rec(Dk, Dv);
     const float *rec = p.ws + (int64_t)blockIdx.x * R.size;
     if (!in_bounds(rec, (size_t)R.size * 4, p.ws, p.ws_bytes, p.bounds)) return;
     const int64_t rk = (int64_t)p.H * Dk, rv = (int64_t)p.H * Dv;
     const T *gq = (const T *)p.q + u.row0 * Dk, *gk = (const T *)p.k + u.row0 * Dk;
 
-    stage_block<NT_P>(bS, LD, rec + R.S, Dvp, Dkp, Dvp);
-    stage_block<NT_P>(bdV, LD, rec + R.dV, Dvp, C, Dvp);
-    stage_block<NT_P>(bV, LD, rec + R.V, Dvp, C, Dvp);
+    stage_block<NT_P, 32>(bS, LD, rec + R.S, Dvp, Dkp, Dvp);
+    stage_block<NT_P, 32>(bdV, LD, rec + R.dV, Dvp, C, Dvp);
+    stage_block<NT_P, 32>(bV, LD, rec + R.V, Dvp, C, Dvp);
     cp_async_commit_group();
-    load_rows<T, NT_P>(bO, LD, (const T *)p.dO + u.row0 * Dv, rv, len, Dv, Dvp);
+    load_rows<T, NT_P>(bO, LD, (const T *)p.dO + u.row0 * Dv, rv, len, Dv, Dvp, p.wide_v);
     if (tid < C) {
         sG[tid] = reinterpret_cast<const double *>(rec + R.G)[tid];
         seG[tid] = rec[R.eG + tid];
@@ -549,12 +628,18 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     float late[2][2] = {}, early[2][2] = {}, db[2][2] = {};  // row sums of this lane's rows 16 i + g + 8 half
 
     // dQg = dO S^T (dq = e^G dQg) and dW = -dV' S^T
+    float2 at[2][2][2];  // this lane's pairs of q, then of k: on their way while the products run
+    auto fetch_pairs = [&](const T *rows) {
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
+            if (!(e & 1)) at[i][j][e >> 1] = row_pair(rows + (r0 + r) * rk, c0 + c, Dk, r0 + r < len, p.wide_k);
+        });
+    };
     if (inK) {
+        fetch_pairs(gq);
         tf32::tile<2, 2, false, false, EX, false>(dq, bO + r0 * LD, LD, bS + c0 * LD, LD, 0, Dvp);
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
             dq[i][j][e] *= seG[r0 + r];
-            const float qv = (r0 + r < len && c0 + c < Dk) ? load_elem(gq, (r0 + r) * rk + c0 + c) : 0.f;
-            late[i][e >> 1] = fmaf(dq[i][j][e], qv, late[i][e >> 1]);
+            late[i][e >> 1] = fmaf(dq[i][j][e], e & 1 ? at[i][j][e >> 1].y : at[i][j][e >> 1].x, late[i][e >> 1]);
         });
         float w[2][2][4] = {};
         tf32::tile<2, 2, false, false, false, false>(w, bdV + r0 * LD, LD, bS + c0 * LD, LD, 0, Dvp);
@@ -562,32 +647,36 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     }
     {  // dM = dO V'^T (i <= r)
         float m[2][1][4] = {};
+        float2 M[2][2];
+        tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
+            if (!(e & 1)) M[i][e >> 1] = *reinterpret_cast<const float2 *>(rec + R.M + (r0 + r) * C + c1 + c);
+        });
         if (tri) tf32::tile<2, 1, false, false, EX, false>(m, bO + r0 * LD, LD, bV + c1 * LD, LD, 0, Dvp);
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             r += r0;
             c += c1;
             const float d = c <= r ? m[i][j][e] : 0.f;
             sM[r * LC + c] = c <= r ? d * expf((float)(sG[r] - sG[c])) : 0.f;
-            if (c < r) X[i][j][e] = d * rec[R.M + r * C + c];
+            if (c < r) X[i][j][e] = d * (e & 1 ? M[i][e >> 1].y : M[i][e >> 1].x);
         });
     }
     __syncthreads();
     // dS_next over S, with <dS_next, S> on the way
     float dot = 0.f;
     {
-        const int W = Dvp / 4, m = Dkp * W;
-        for (int base = tid; base < m; base += 4 * NT_P) {
+        const int c = (tid & 31) * 4;
+        for (int base = tid >> 5; c < Dvp && base < Dkp; base += 4 * (NT_P / 32)) {
             float4 d[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = base + e * NT_P;
-                d[e] = i < m ? *reinterpret_cast<const float4 *>(rec + R.dS + 4 * (int64_t)i) : make_float4(0, 0, 0, 0);
+                const int r = base + e * (NT_P / 32);
+                d[e] = r < Dkp ? *reinterpret_cast<const float4 *>(rec + R.dS + r * Dvp + c) : make_float4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = base + e * NT_P;
-                if (i < m) {
-                    float4 *s = reinterpret_cast<float4 *>(bS + (i / W) * LD + (i % W) * 4);
+                const int r = base + e * (NT_P / 32);
+                if (r < Dkp) {
+                    float4 *s = reinterpret_cast<float4 *>(bS + r * LD + c);
                     const float4 o = *s;
                     dot = fmaf(o.x, d[e].x, fmaf(o.y, d[e].y, fmaf(o.z, d[e].z, fmaf(o.w, d[e].w, dot))));
                     *s = d[e];
@@ -597,19 +686,19 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     }
     __syncthreads();
     if (inK) {  // dKd = V' dS_next^T (dk = e^D dKd)
+        fetch_pairs(gk);
         tf32::tile<2, 2, false, false, false, false>(dk, bV + r0 * LD, LD, bS + c0 * LD, LD, 0, Dvp);
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
             dk[i][j][e] *= seD[r0 + r];
-            const float kv = (r0 + r < len && c0 + c < Dk) ? load_elem(gk, (r0 + r) * rk + c0 + c) : 0.f;
-            early[i][e >> 1] = fmaf(dk[i][j][e], kv, early[i][e >> 1]);
+            early[i][e >> 1] = fmaf(dk[i][j][e], e & 1 ? at[i][j][e >> 1].y : at[i][j][e >> 1].x, early[i][e >> 1]);
         });
     }
     __syncthreads();
     float *sV = bS, *sK = bS + C * LD, *sT = bO, *sdT = bV;
-    stage_block<NT_P>(sT, LC, rec + R.T, C, C, C);
+    stage_block<NT_P, 16>(sT, LC, rec + R.T, C, C, C);
     cp_async_commit_group();
-    load_rows<T, NT_P>(sV, LD, (const T *)p.v + u.row0 * Dv, rv, len, Dv, Dvp);
-    load_rows<T, NT_P>(sK, LD, gk, rk, len, Dk, Dkp);
+    load_rows<T, NT_P>(sV, LD, (const T *)p.v + u.row0 * Dv, rv, len, Dv, Dvp, p.wide_v);
+    load_rows<T, NT_P>(sK, LD, gk, rk, len, Dk, Dkp, p.wide_k);
     cp_async_wait<0>();
     __syncthreads();
     {  // dT = dV' Bv^T + dW Bk^T, on and below the diagonal (T has nothing above it)
@@ -632,7 +721,8 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
             r += r0;
             c += c0;
             db[i][e >> 1] = fmaf(a[i][j][e], sV[r * LD + c], db[i][e >> 1]);
-            if (r < len && c < Dv) p.dv[(u.row0 + (int64_t)r * p.H) * Dv + c] = sb[r] * a[i][j][e];
+            store_pair(p.dv + (u.row0 + (int64_t)r * p.H) * Dv, c - (e & 1), Dv, r < len && (e & 1), p.pair_v,
+                       sb[r] * a[i][j][e & 2], sb[r] * a[i][j][e | 1]);
         });
     }
     if (inK) {  // dBk = T^T dW
@@ -651,17 +741,21 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     __syncthreads();
     tf32::each<2, 1>([&](int i, int j, int e, int r, int c) { bdV[(r0 + r) * LC + c1 + c] = y[i][j][e]; });
     float *sQ = bV;
-    load_rows<T, NT_P>(sQ, LD, gq, rk, len, Dk, Dkp);
+    load_rows<T, NT_P>(sQ, LD, gq, rk, len, Dk, Dkp, p.wide_k);
     __syncthreads();
     {  // dA = -(T^T dT) T^T (i < r);  dP' = beta dA E
         float a[2][1][4] = {};
+        float2 Pp[2][2];
+        tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
+            if (!(e & 1)) Pp[i][e >> 1] = *reinterpret_cast<const float2 *>(rec + R.P + (r0 + r) * C + c1 + c);
+        });
         if (tri) tf32::tile<2, 1, false, false, false, false>(a, bdV + r0 * LC, LC, sT + c1 * LC, LC, 0, c1 + 8);
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             r += r0;
             c += c1;
             float d = 0.f;
             if (c < r) {
-                const float P = rec[R.P + r * C + c];
+                const float P = e & 1 ? Pp[i][e >> 1].y : Pp[i][e >> 1].x;
                 db[i][e >> 1] = fmaf(-a[i][j][e], P, db[i][e >> 1]);
                 d = -a[i][j][e] * sb[r];
                 X[i][j][e] = fmaf(d, P, X[i][j][e]);
@@ -679,11 +773,9 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
             r += r0;
             c += c0;
-            if (r < len && c < Dk) {
-                const int64_t at = (u.row0 + (int64_t)r * p.H) * Dk + c;
-                p.dq[at] = dq[i][j][e];
-                p.dk[at] = dk[i][j][e];
-            }
+            const int64_t row = (u.row0 + (int64_t)r * p.H) * Dk;
+            store_pair(p.dq + row, c - (e & 1), Dk, r < len && (e & 1), p.pair_k, dq[i][j][e & 2], dq[i][j][e | 1]);
+            store_pair(p.dk + row, c - (e & 1), Dk, r < len && (e & 1), p.pair_k, dk[i][j][e & 2], dk[i][j][e | 1]);
         });
     }
     // the sums over rows and pairs.  T^T dT is read: the pair sums go there; T is read: the row sums go there
@@ -759,16 +851,18 @@ size_t gdn_bwd_workspace(int64_t B, int64_t S, int H, int Dk, int Dv) {
 }
 
 template <typename T>
-kda_status_t gb_launch(const GbArgs &p, int64_t nbh, cudaStream_t st) {
+kda_status_t gb_launch(GbArgs p, int64_t nbh, cudaStream_t st) {
     const int64_t units = nbh * p.Nc, jobs = 2 * nbh * p.nslice;
     cudaFuncSetAttribute(gb_prep_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PREP_SMEM);
     cudaFuncSetAttribute(gb_chain_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain_smem<T>());
     cudaFuncSetAttribute(gb_grad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GRAD_SMEM);
-    // 16-byte pieces of the token rows of q and k
-    const int wide = p.Dk * (int)sizeof(T) % 16 == 0 && aligned_to(p.q, 16) && aligned_to(p.k, 16);
+    p.wide_k = p.Dk * (int)sizeof(T) % 16 == 0 && aligned_to(p.q, 16) && aligned_to(p.k, 16);
+    p.wide_v = p.Dv * (int)sizeof(T) % 16 == 0 && aligned_to(p.v, 16) && aligned_to(p.dO, 16);
+    p.pair_k = p.Dk % 2 == 0 && aligned_to(p.dq, 8) && aligned_to(p.dk, 8);
+    p.pair_v = p.Dv % 2 == 0 && aligned_to(p.dv, 8);
     gb_prep_kernel<T><<<(unsigned)units, NT_P, PREP_SMEM, st>>>(p);
     KDA_TRY(check_launch("gb_prep_kernel"));
-    gb_chain_kernel<T><<<(unsigned)jobs, NT_C, chain_smem<T>(), st>>>(p, wide);
+    gb_chain_kernel<T><<<(unsigned)jobs, NT_C, chain_smem<T>(), st>>>(p);
     KDA_TRY(check_launch("gb_chain_kernel"));
     gb_grad_kernel<T><<<(unsigned)units, NT_P, GRAD_SMEM, st>>>(p);
     return check_launch("gb_grad_kernel");
@@ -783,10 +877,10 @@ kda_status_t gb_validate(const kda_recurrent_bwd_args *a) {
                     a->H, a->D_k, a->D_v);
     if (a->D_k > 128 || a->D_v > 128)
         return fail(KDA_ERR_UNSUPPORTED, "D_k and D_v must be <= 128 (got %d, %d)", a->D_k, a->D_v);
-    // one CTA per (b, h, chunk), and two per (b, h, 16 value columns)
-    const int64_t nc = a->S / C + (a->S % C != 0), most = nc > 16 ? nc : 16;
+    // one CTA per (b, h, chunk), and two per (b, h, 32 value columns)
+    const int64_t nc = a->S / C + (a->S % C != 0), most = nc > 8 ? nc : 8;
     if (a->B > 0 && (a->B > 0x7fffffffLL / a->H || a->B * a->H > 0x7fffffffLL / most))
-        return fail(KDA_ERR_UNSUPPORTED, "gdn backward: B*H*max(chunks, 16) exceeds 2^31 - 1");
+        return fail(KDA_ERR_UNSUPPORTED, "gdn backward: B*H*max(chunks, 8) exceeds 2^31 - 1");
     return KDA_OK;
 }
 
@@ -820,7 +914,7 @@ kda_status_t kda_gdn_chunk_bwd(const kda_recurrent_bwd_args *a) {
     p.Dk = a->D_k;
     p.Dv = a->D_v;
     p.Nc = (int)((a->S + C - 1) / C);
-    p.nslice = pad16(a->D_v) / VS;
+    p.nslice = pad32(a->D_v) / VS;
     p.q = a->q; p.k = a->k; p.v = a->v; p.z = a->z; p.beta = a->beta; p.dO = a->d_o;
     p.log_decay = a->log_decay;
     p.g_min = a->g_min;

@@ -36,12 +36,23 @@ __device__ __forceinline__ void load2(const __nv_bfloat16 *p, float &x, float &y
     y = __uint_as_float(t & 0xffff0000u);
 }
 
+// (hi, lo) of a value, as operands kept split in shared memory hold them
+__device__ __forceinline__ float2 split2(float x) {
+    uint32_t hi, lo;
+    split(x, hi, lo);
+    return make_float2(__uint_as_float(hi), __uint_as_float(lo));
+}
+__device__ __forceinline__ float load_elem(const float2 *, int) { return 0.f; }  // (split operands are read whole)
+__device__ __forceinline__ void load2(const float2 *, float &, float &) {}
+using kda::load_elem;
+
 // acc += A B^T over k0 <= k < k1 (multiples of 8), for a warp's MT x 16 rows and NT x 8 columns:
 // acc[i][j] holds (16i + g, 8j + 2t), (.., + 1), (16i + g + 8, ..), (.., + 1) with g = lane / 4, t = lane % 4.
 //   A(m, k) = A[m * lda + k], or A[k * lda + m] with AT;  B(n, k) = B[n * ldb + k], or B[k * ldb + n] with BT.
-// AEX / BEX: tf32 holds the operand exactly.  The order of k within an instruction is free, as long as A and
+// B may be kept split (float2: hi, lo).  AEX / BEX: tf32 holds the operand exactly.  The order of k within an instruction is free, as long as A and
 // B share it: where an operand is contiguous in k, a lane takes neighbouring k (one 8-byte load).
-// Pitches of 8 mod 32 floats make the reads free of bank conflicts (mixed orientations: two-way).
+// Pitches of 8 mod 32 floats make the reads free of bank conflicts (mixed orientations: two-way); for a split B
+// read by k, 2 mod 8 pairs where A is contiguous in k, 4 mod 16 where it is not.
 // CROSS: the lo terms go to accumulators of their own (shorter dependent chains where a warp has few tiles).
 template <int MT, int NT, bool AT, bool BT, bool AEX, bool BEX, bool CROSS = false, typename TA, typename TB>
 __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int lda, const TB *B, int ldb, int k0,
@@ -74,6 +85,15 @@ __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int l
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
+            if constexpr (sizeof(TB) == 8) {
+                static_assert(BT, "split operands are read by k");
+                const float2 u = B[ka * ldb + 8 * j + g], v = B[kb * ldb + 8 * j + g];
+                bh[j][0] = __float_as_uint(u.x);
+                bl[j][0] = __float_as_uint(u.y);
+                bh[j][1] = __float_as_uint(v.x);
+                bl[j][1] = __float_as_uint(v.y);
+                continue;
+            }
             float x[2];
             if (BT) {
                 x[0] = load_elem(B, ka * ldb + 8 * j + g);

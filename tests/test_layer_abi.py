@@ -168,8 +168,8 @@ def test_gdn_bwd_refusals(mut, status):
 
 @pytest.mark.parametrize("B,S,H,Dk,Dv", [(1, 4096, 16, 128, 128), (2, 100, 3, 18, 13), (0, 5, 1, 8, 8), (2, 0, 1, 8, 8)])
 def test_gdn_bwd_workspace_is_one_record_per_chunk(B, S, H, Dk, Dv):
-    n, r16 = ctypes.c_size_t(1), lambda x: -(-x // 16) * 16
+    n, up = ctypes.c_size_t(1), lambda x, m: -(-x // m) * m
     a = gdn_bwd(B=B, S=S, H=H, D_k=Dk, D_v=Dv)
     assert L.load().kda_gdn_chunk_bwd_workspace_size(ctypes.byref(a), ctypes.byref(n)) == L.KDA_OK
-    dk, dv = r16(Dk), r16(Dv)
+    dk, dv = up(Dk, 16), up(Dv, 32)
     assert n.value == B * H * -(-S // 64) * 4 * (256 + 12288 + 64 * (dk + 2 * dv) + 2 * dk * dv)
