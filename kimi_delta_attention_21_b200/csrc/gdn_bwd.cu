@@ -41,9 +41,10 @@ constexpr int LD = 136;     // pitch of [64 or 128][D] tiles in shared memory: 8
 constexpr int LC = 72;      // pitch of [64][64] tiles
 constexpr int NT_P = 512;   // threads of the per-chunk kernels
 constexpr int NT_C = 512;   // threads of the chain kernel
+constexpr int LP = 130;     // pitch of split [64][128] tiles: 2 mod 8 pairs
 constexpr int VS = 32;      // value columns per chain CTA
-// chain pitches (conflict-free reads by k): split [Dk][32] and [64][32] tiles, plain [64][32]
-constexpr int LS = 34, LV = 36, LO = 40;
+constexpr int LS = 34;      // chain pitch of split [Dk][32] and [64][32] tiles: 2 mod 8 pairs
+constexpr int LO = 40;      // and of plain [.][32] ones
 
 __host__ __device__ inline int pad16(int x) { return (x + 15) & ~15; }
 __host__ __device__ inline int pad32(int x) { return (x + 31) & ~31; }
@@ -56,8 +57,9 @@ struct Rec {
     int64_t T, P, M;    // [64][64]
     int64_t W;          // [64][Dkp]
     int64_t V;          // [64][Dvp]: U, then V'
-    int64_t S, dS;      // [Dkp][Dvp]: the state entering the chunk, the gradient of the state leaving it
-    int64_t dV;         // [64][Dvp]: dV'
+    int64_t S;          // [Dkp][Dvp]: the state entering the chunk
+    int64_t dS;         // [Dkp][Dvp]: Q^T (e^G dO), then the gradient of the state leaving the chunk
+    int64_t dV;         // [64][Dvp]: M^T dO, then dV'
     int64_t size;
 };
 
@@ -109,62 +111,27 @@ __device__ __forceinline__ Unit unit_of(const GbArgs &p, int64_t bh, int n) {
     return u;
 }
 
-// Token rows (rs elements apart) as fp32 into [64][ld], zero past `len` rows and D columns up to Dp.  wide: D is a
-// multiple of a 16-byte vector and every row starts on 16 bytes; a thread's loads are all in flight together.
+// Token rows (rs elements apart), in their type, into [64][LD]: zero past `len` rows and D columns up to Dp.  wide: D is
+// a multiple of a 16-byte vector and every row starts on 16 bytes; the copies are asynchronous then.
 template <typename T, int NT>
-__device__ __forceinline__ void load_rows(float *dst, int ld, const T *src, int64_t rs, int len, int D, int Dp, bool wide) {
-    constexpr int E = 16 / (int)sizeof(T), VPR = 128 / E;  // vectors of a full row
-    if (wide) {
-        constexpr int U = C * VPR / NT;
-        uint4 v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = threadIdx.x + u * NT, r = i / VPR, c = i % VPR * E;
-            v[u] = (r < len && c < D) ? *reinterpret_cast<const uint4 *>(src + (int64_t)r * rs + c) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = threadIdx.x + u * NT, r = i / VPR, c = i % VPR * E;
-            if (c >= Dp) continue;
-            float4 *d = reinterpret_cast<float4 *>(dst + r * ld + c);
-            if (sizeof(T) == 4) {
-                *d = make_float4(__uint_as_float(v[u].x), __uint_as_float(v[u].y), __uint_as_float(v[u].z),
-                                 __uint_as_float(v[u].w));
-            } else {
-                d[0] = make_float4(__uint_as_float(v[u].x << 16), __uint_as_float(v[u].x & 0xffff0000u),
-                                   __uint_as_float(v[u].y << 16), __uint_as_float(v[u].y & 0xffff0000u));
-                d[1] = make_float4(__uint_as_float(v[u].z << 16), __uint_as_float(v[u].z & 0xffff0000u),
-                                   __uint_as_float(v[u].w << 16), __uint_as_float(v[u].w & 0xffff0000u));
-            }
-        }
-        return;
-    }
-    const int c = threadIdx.x & 127;
-    if (c >= Dp) return;
-#pragma unroll 8
-    for (int r = threadIdx.x >> 7; r < C; r += NT / 128)
-        dst[r * ld + c] = (r < len && c < D) ? load_elem(src, (int64_t)r * rs + c) : 0.f;
-}
-
-// The same rows kept in their type, by cp.async where 16-byte pieces are possible.
-template <typename T>
 __device__ __forceinline__ void stage_rows(T *dst, const T *src, int64_t rs, int len, int D, int Dp, bool wide) {
     if (wide) {
         constexpr int E = 16 / (int)sizeof(T), VPR = 128 / E;
 #pragma unroll
-        for (int i = threadIdx.x; i < C * VPR; i += NT_C) {
+        for (int i = threadIdx.x; i < C * VPR; i += NT) {
             const int r = i / VPR, c = i % VPR * E;
             const bool in = r < len && c < D;
             if (c < Dp)
                 cp_async16_fill(reinterpret_cast<float *>(dst + r * LD + c),
-                                reinterpret_cast<const float *>(src + (in ? (int64_t)r * rs + c : 0)), in);
+                                reinterpret_cast<const float *>(src + (in ? r * rs + c : 0)), in);
         }
         return;
     }
     const int c = threadIdx.x & 127;
     if (c < Dp)
-        for (int r = threadIdx.x >> 7; r < C; r += NT_C / 128)
-            dst[r * LD + c] = (r < len && c < D) ? src[(int64_t)r * rs + c] : T(0.f);
+#pragma unroll 4
+        for (int r = threadIdx.x >> 7; r < C; r += NT / 128)
+            dst[r * LD + c] = (r < len && c < D) ? src[r * rs + c] : T(0.f);
 }
 
 // A record block of `rows` rows of `cols` floats (a multiple of 4, at most 4 VPR; pitch `pitch`) into shared memory.
@@ -204,15 +171,19 @@ __device__ __forceinline__ void store_pair(float *row, int c, int D, bool in, bo
 }
 
 // ---------------------------------------------------------------- per chunk: P, M, T, W, U
-constexpr size_t PREP_SMEM = sizeof(float) * (3 * C * LD + 3 * C * LC + 3 * C) + sizeof(double) * C;
+template <typename T> constexpr size_t prep_smem() {
+    return sizeof(double) * C + sizeof(float) * (4 * C * LC + 2 * C) + 4 * sizeof(T) * C * LD +
+           (sizeof(T) == 2 ? sizeof(float2) * C * LP : 0);
+}
 
 template <typename T>
 __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant__ GbArgs p) {
     constexpr bool EX = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t gb_sm[];
     double *sG = reinterpret_cast<double *>(gb_sm);
-    float *sK = reinterpret_cast<float *>(sG + C), *sQ = sK + C * LD, *sV = sQ + C * LD;
-    float *sA = sV + C * LD, *sT = sA + C * LC, *sY = sT + C * LC, *sb = sY + C * LC, *seG = sb + C;
+    float *sA = reinterpret_cast<float *>(sG + C), *sT = sA + C * LC, *sY = sT + C * LC, *sM = sY + C * LC;
+    float *sb = sM + C * LC, *seG = sb + C;
+    T *sK = reinterpret_cast<T *>(seG + C), *sQ = sK + C * LD, *sV = sQ + C * LD, *sO = sV + C * LD;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t bh = blockIdx.x / p.Nc;
     const int n = (int)(blockIdx.x - bh * p.Nc);
@@ -222,9 +193,13 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
     float *rec = p.ws + (int64_t)blockIdx.x * R.size;
     if (!in_bounds(rec, (size_t)R.size * 4, p.ws, p.ws_bytes, p.bounds)) return;
 
-    load_rows<T, NT_P>(sK, LD, (const T *)p.k + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, p.wide_k);
-    load_rows<T, NT_P>(sQ, LD, (const T *)p.q + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, p.wide_k);
-    load_rows<T, NT_P>(sV, LD, (const T *)p.v + u.row0 * p.Dv, (int64_t)p.H * p.Dv, u.len, p.Dv, Dvp, p.wide_v);
+    const int64_t rk = (int64_t)p.H * p.Dk, rv = (int64_t)p.H * p.Dv;
+    stage_rows<T, NT_P>(sK, (const T *)p.k + u.row0 * p.Dk, rk, u.len, p.Dk, Dkp, p.wide_k);
+    stage_rows<T, NT_P>(sQ, (const T *)p.q + u.row0 * p.Dk, rk, u.len, p.Dk, Dkp, p.wide_k);
+    cp_async_commit_group();
+    stage_rows<T, NT_P>(sV, (const T *)p.v + u.row0 * p.Dv, rv, u.len, p.Dv, Dvp, p.wide_v);
+    stage_rows<T, NT_P>(sO, (const T *)p.dO + u.row0 * p.Dv, rv, u.len, p.Dv, Dvp, p.wide_v);
+    cp_async_commit_group();
     if (warp == 0) {  // the cumulative log-decay: two tokens per lane, a scan over the warp
         double g[2];
 #pragma unroll
@@ -262,6 +237,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
         }
     }
     for (int i = tid; i < C * LC; i += NT_P) sT[i] = 0.f;
+    cp_async_wait<1>();  // k and q
     __syncthreads();
     // P and M: warp (32 rows, 8 columns); tiles above the diagonal are zeros
     {
@@ -278,6 +254,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
             kk[i][j][e] = c < r ? kk[i][j][e] * x : 0.f;
             qk[i][j][e] = c <= r ? qk[i][j][e] * x : 0.f;
             sA[r * LC + c] = sb[r] * kk[i][j][e];
+            sM[r * LC + c] = qk[i][j][e];
             if (e & 1) {
                 *reinterpret_cast<float2 *>(rec + R.P + r * C + c - 1) = make_float2(kk[i][j][e - 1], kk[i][j][e]);
                 *reinterpret_cast<float2 *>(rec + R.M + r * C + c - 1) = make_float2(qk[i][j][e - 1], qk[i][j][e]);
@@ -336,6 +313,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
         sT[(32 + r) * LC + c] = s[0];
         sT[(48 + r) * LC + c] = s[1];
     }
+    cp_async_wait<0>();  // v and dO (made visible by the next barrier)
     __syncthreads();
     // T out; T Diag(beta e^G) over A, T Diag(beta) over the scratch: the scales of Bk's and Bv's rows
     for (int i = tid; i < C * C; i += NT_P) {
@@ -347,104 +325,154 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
     }
     __syncthreads();
     const int r0 = 32 * (warp & 1), c0 = 16 * (warp >> 1);
+    auto put = [&](float *dst, int pitch, const float (&acc)[2][2][4]) {
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
+            if (!(e & 1))
+                *reinterpret_cast<float2 *>(dst + (r0 + r) * pitch + c0 + c) = make_float2(acc[i][j][e], acc[i][j][e + 1]);
+        });
+    };
     if (c0 < Dkp) {
         float acc[2][2][4] = {};
         tf32::tile<2, 2, false, true, false, EX>(acc, sA + r0 * LC, LC, sK + c0, LD, 0, r0 + 32);
-        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
-            if (!(e & 1))
-                *reinterpret_cast<float2 *>(rec + R.W + (r0 + r) * Dkp + c0 + c) =
-                    make_float2(acc[i][j][e], acc[i][j][e + 1]);
-        });
+        put(rec + R.W, Dkp, acc);
     }
     if (c0 < Dvp) {
-        float acc[2][2][4] = {};
+        float acc[2][2][4] = {}, o[2][2][4] = {};
         tf32::tile<2, 2, false, true, false, EX>(acc, sY + r0 * LC, LC, sV + c0, LD, 0, r0 + 32);
-        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
-            if (!(e & 1))
-                *reinterpret_cast<float2 *>(rec + R.V + (r0 + r) * Dvp + c0 + c) =
-                    make_float2(acc[i][j][e], acc[i][j][e + 1]);
-        });
+        put(rec + R.V, Dvp, acc);
+        // M^T dO: what dV' has of the chunk itself
+        tf32::tile<2, 2, true, true, false, EX>(o, sM + r0, LC, sO + c0, LD, r0, C);
+        put(rec + R.dV, Dvp, o);
     }
+    // Q^T (e^G dO): what dS has of the chunk itself.  32 x 32 of [Dk][Dv] per warp, e^G on the rows of the exact side
+    // (fp32 dO: on dO, in place)
+    const int m0 = 32 * (warp & 3), n0 = 32 * (warp >> 2);
+    float h[2][4][4] = {};
+    if constexpr (EX) {
+        float2 *sgO = reinterpret_cast<float2 *>(sO + C * LD);  // e^G dO, split, 128 columns
+        for (int i = tid; i < C * 128; i += NT_P) {
+            const int r = i >> 7, c = i & 127;
+            if (c < Dvp) sgO[r * LP + c] = tf32::split2(seG[r] * load_elem(sO, r * LD + c));
+        }
+        __syncthreads();
+        if (m0 < Dkp && n0 < Dvp) tf32::tile<2, 4, true, true, EX, false>(h, sQ + m0, LD, sgO + n0, LP, 0, C);
+    } else {
+        __syncthreads();  // M^T dO has read dO
+        for (int i = tid; i < C * 128; i += NT_P) sO[(i >> 7) * LD + (i & 127)] *= seG[i >> 7];
+        __syncthreads();
+        if (m0 < Dkp && n0 < Dvp) tf32::tile<2, 4, true, true, EX, false>(h, sQ + m0, LD, sO + n0, LD, 0, C);
+    }
+    if (n0 < Dvp)
+        tf32::each<2, 4>([&](int i, int j, int e, int r, int c) {
+            if (!(e & 1) && m0 + r < Dkp)
+                *reinterpret_cast<float2 *>(rec + R.dS + (m0 + r) * Dvp + n0 + c) = make_float2(h[i][j][e], h[i][j][e + 1]);
+        });
 }
 
 // ---------------------------------------------------------------- the state and its gradient through the chunks
 template <typename T> constexpr size_t chain_smem() {
-    // backward (the larger): M, W, dO, dO split, dV' split, dS split, e^G and e^D, K, Q
-    return sizeof(float) * (C * LC + C * LD + C * LO + 2 * 2 * C * LV + 2 * 128 * LS + 2 * C) + 2 * sizeof(T) * C * LD;
+    // W, [64][32] in and sums, Q^T e^G dO, two of e^G and e^D, V' and S (or their gradients) split, K
+    return sizeof(float) * (C * LD + 2 * C * LO + 128 * LO + 4 * C + 2 * C * LS + 2 * 128 * LS) + sizeof(T) * C * LD;
 }
 
 // 16 warps: [64][32] results as 4 x 2 tiles of 16 x 16, the sum over k shared by two groups of warps; [Dk][32] ones
-// as 8 x 2 tiles.  The operands that several warps read as B are kept split in shared memory.
+// as 8 x 2 tiles.  The operands that several warps read as B are kept split in shared memory.  The state, or its
+// gradient, stays in the accumulators of the warps that own it.  Products have accumulators of their own: the tensor
+// core truncates as it adds, the state is rounded once a chunk.
+struct Chain {
+    const float *rec0;  // the records of this (b, h)
+    Rec R;
+    int Dkp, Dvp, j0;
+    int64_t row0, rk;   // token rows of the (b, h)
+    int m0, n0;         // this warp's part of a [Dk][32] result
+    int r0, c0, half;   // this warp's part of a [64][32] result, and of the sum over k
+};
 
-// Forward: the state stays in the accumulators of the warps that own it, with a split copy in shared memory as the
-// next product's operand.  W and U of the next chunk arrive while K is used, K while W is.
+__device__ __forceinline__ Chain chain_of(const GbArgs &p, int64_t bh, int j0) {
+    const int warp = threadIdx.x >> 5;
+    Chain c;
+    c.R = make_rec(p.Dk, p.Dv);
+    c.rec0 = p.ws + bh * p.Nc * c.R.size;
+    c.Dkp = pad16(p.Dk);
+    c.Dvp = pad32(p.Dv);
+    c.j0 = j0;
+    const int64_t b = bh / p.H;
+    c.row0 = b * p.S * p.H + (bh - b * p.H);
+    c.rk = (int64_t)p.H * p.Dk;
+    c.m0 = 16 * (warp & 7);
+    c.n0 = 16 * (warp >> 3);
+    c.r0 = 16 * (warp & 3);
+    c.c0 = 16 * ((warp >> 2) & 1);
+    c.half = warp >> 3;
+    return c;
+}
+
+template <typename T>
+__device__ __forceinline__ void stage_keys(const GbArgs &p, const Chain &c, T *sK, int n) {
+    const int64_t t0 = (int64_t)n * C;
+    stage_rows<T, NT_C>(sK, (const T *)p.k + (c.row0 + t0 * p.H) * p.Dk, c.rk, (int)min((int64_t)C, p.S - t0), p.Dk, c.Dkp,
+                        p.wide_k);
+}
+
+// V' = U - W S,  S <- gamma S + K^T (e^D V').  W and U of the next chunk arrive while K is used, K while W is.
 template <typename T>
 __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j0, float *sm) {
     constexpr bool EX = sizeof(T) == 2;
-    float *sW = sm, *sU = sW + C * LD, *sY = sU + C * VS, *se = sY + C * LO;
-    float2 *sVp = reinterpret_cast<float2 *>(se + 2 * C), *sS = sVp + C * LV;
+    float *sW = sm, *sU = sW + C * LD, *sY = sU + C * LO, *se = sY + C * LO;
+    float2 *sVp = reinterpret_cast<float2 *>(se + 2 * C), *sS = sVp + C * LS;
     T *sK = reinterpret_cast<T *>(sS + 128 * LS);
-    const int warp = threadIdx.x >> 5;
-    const int Dkp = pad16(p.Dk), Dvp = pad32(p.Dv);
-    const Rec R = make_rec(p.Dk, p.Dv);
-    float *rec0 = p.ws + bh * p.Nc * R.size;
-    auto stage_w = [&](int n) {
-        const float *rec = rec0 + (int64_t)n * R.size;
+    const Chain q = chain_of(p, bh, j0);
+    const Rec &R = q.R;
+    const int m0 = q.m0, n0 = q.n0, r0 = q.r0, c0 = q.c0, Dkp = q.Dkp, Dvp = q.Dvp, kmid = (Dkp / 2 + 7) & ~7;
+    const bool own = m0 < Dkp, first = !q.half;
+    auto stage_w = [&](const float *rec) {
         stage_block<NT_C, 32>(sW, LD, rec + R.W, Dkp, C, Dkp);
-        stage_block<NT_C, 8>(sU, VS, rec + R.V + j0, Dvp, C, VS);
+        stage_block<NT_C, 8>(sU, LO, rec + R.V + j0, Dvp, C, VS);
         cp_async_commit_group();
     };
-    auto stage_k = [&](int n) {
-        const Unit u = unit_of(p, bh, n);
-        stage_block<NT_C, 32>(se, 2 * C, rec0 + (int64_t)n * R.size + R.eG, 2 * C, 1, 2 * C);
-        stage_rows<T>(sK, (const T *)p.k + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, p.wide_k);
-        cp_async_commit_group();
-    };
-    const int m0 = 16 * (warp & 7), n0 = 16 * (warp >> 3);                        // this warp's part of the state
-    const int r0 = 16 * (warp & 3), c0 = 16 * ((warp >> 2) & 1), half = warp >> 3;  // and of V', and of its sum
-    const int kmid = (Dkp / 2 + 7) & ~7;
     float S[1][2][4] = {};
     tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
         r += m0;
         c += n0;
         if (r < p.Dk && j0 + c < p.Dv && p.S0) S[i][j][e] = p.S0[(bh * p.Dk + r) * p.Dv + j0 + c];
-        if (m0 < Dkp) sS[r * LS + c] = tf32::split2(S[i][j][e]);
+        if (own) sS[r * LS + c] = tf32::split2(S[i][j][e]);
     });
-    stage_w(0);
-    for (int n = 0; n < p.Nc; ++n) {
-        float *rec = rec0 + (int64_t)n * R.size;
+    float *rec = const_cast<float *>(q.rec0);
+    stage_w(rec);
+    for (int n = 0; n < p.Nc; ++n, rec += R.size) {
         cp_async_wait<0>();  // W and U of chunk n
         __syncthreads();
-        stage_k(n);
-        if (m0 < Dkp)  // the state entering the chunk
+        stage_block<NT_C, 32>(se, 2 * C, rec + R.eG, 2 * C, 1, 2 * C);
+        stage_keys<T>(p, q, sK, n);
+        cp_async_commit_group();
+        if (own)  // the state entering the chunk
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 if (!(e & 1))
-                    *reinterpret_cast<float2 *>(rec + R.S + (int64_t)(m0 + r) * Dvp + j0 + n0 + c) =
+                    *reinterpret_cast<float2 *>(rec + R.S + (m0 + r) * Dvp + j0 + n0 + c) =
                         make_float2(S[i][j][e], S[i][j][e + 1]);
             });
         float v[1][2][4] = {};
-        tf32::tile<1, 2, false, true, false, false, true>(v, sW + r0 * LD, LD, sS + c0, LS, half ? kmid : 0,
-                                                          half ? Dkp : kmid);
-        if (half)
+        tf32::tile<1, 2, false, true, false, false, true>(v, sW + r0 * LD, LD, sS + c0, LS, first ? 0 : kmid,
+                                                          first ? kmid : Dkp);
+        if (!first)
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { sY[(r0 + r) * LO + c0 + c] = v[i][j][e]; });
         cp_async_wait<0>();  // K of chunk n
         __syncthreads();     // K, e^D and the other half of the sum
-        if (!half)
+        if (first)
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 r += r0;
                 c += c0;
-                v[i][j][e] = sU[r * VS + c] - (v[i][j][e] + sY[r * LO + c]);
-                sVp[r * LV + c] = tf32::split2(se[C + r] * v[i][j][e]);  // e^D V'
+                v[i][j][e] = sU[r * LO + c] - (v[i][j][e] + sY[r * LO + c]);
+                sVp[r * LS + c] = tf32::split2(se[C + r] * v[i][j][e]);  // e^D V'
                 if (e & 1)
-                    *reinterpret_cast<float2 *>(rec + R.V + (int64_t)r * Dvp + j0 + c - 1) =
-                        make_float2(v[i][j][e - 1], v[i][j][e]);
+                    *reinterpret_cast<float2 *>(rec + R.V + r * Dvp + j0 + c - 1) = make_float2(v[i][j][e - 1], v[i][j][e]);
             });
         __syncthreads();
-        if (n + 1 < p.Nc) stage_w(n + 1);
-        if (m0 < Dkp) {  // S <- gamma S + K^T (e^D V')
+        if (n + 1 < p.Nc) stage_w(rec + R.size);
+        if (own) {
             const float gamma = se[C - 1];
-            float add[1][2][4] = {};  // (its own accumulator: the tensor core truncates as it adds, S is rounded once)
-            tf32::tile<1, 2, true, true, EX, false, true>(add, sK + m0, LD, sVp + n0, LV, 0, C);
+            float add[1][2][4] = {};
+            tf32::tile<1, 2, true, true, EX, false, true>(add, sK + m0, LD, sVp + n0, LS, 0, C);
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 S[i][j][e] = fmaf(gamma, S[i][j][e], add[i][j][e]);
                 sS[(m0 + r) * LS + n0 + c] = tf32::split2(S[i][j][e]);
@@ -453,111 +481,77 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
     }
 }
 
-// Backward: the same for dS, from the last chunk to the first.  M, K (first half of a step) and Q, W
-// (second half) are refilled with the previous chunk's as soon as their half is done.
+// dV' = M^T dO + e^D (K dS),  dS <- gamma dS + Q^T (e^G dO) - W^T dV', from the last chunk to the first; the two terms
+// with dO are in the record.  K and M^T dO (first half of a step) and W and Q^T (e^G dO) (second half) are refilled with
+// the previous chunk's as soon as their half is done.
 template <typename T>
 __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int j0, float *sm) {
     constexpr bool EX = sizeof(T) == 2;
-    constexpr int PER = C * VS / NT_C;
-    float *sM = sm, *sW = sM + C * LC, *sdO = sW + C * LD, *se = sdO + C * LO;
-    float2 *sgO = reinterpret_cast<float2 *>(se + 2 * C), *sdV = sgO + C * LV, *sS = sdV + C * LV;
-    T *sK = reinterpret_cast<T *>(sS + 128 * LS), *sQ = sK + C * LD;
-    float *sY = reinterpret_cast<float *>(sgO);  // the other half of a sum, before e^G dO takes the place
-    const int tid = threadIdx.x, warp = tid >> 5;
-    const int Dkp = pad16(p.Dk), Dvp = pad32(p.Dv);
-    const Rec R = make_rec(p.Dk, p.Dv);
-    float *rec0 = p.ws + bh * p.Nc * R.size;
-    auto stage_a = [&](int n) {
-        const Unit u = unit_of(p, bh, n);
-        stage_block<NT_C, 16>(sM, LC, rec0 + (int64_t)n * R.size + R.M, C, C, C);
-        stage_rows<T>(sK, (const T *)p.k + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, p.wide_k);
+    float *sW = sm, *sU = sW + C * LD, *sY = sU + C * LO, *se = sY + C * LO, *sH = se + 4 * C;
+    float2 *sdV = reinterpret_cast<float2 *>(sH + 128 * LO), *sS = sdV + C * LS;
+    T *sK = reinterpret_cast<T *>(sS + 128 * LS);
+    const Chain q = chain_of(p, bh, j0);
+    const Rec &R = q.R;
+    const int m0 = q.m0, n0 = q.n0, r0 = q.r0, c0 = q.c0, Dkp = q.Dkp, Dvp = q.Dvp, kmid = (Dkp / 2 + 7) & ~7;
+    const bool own = m0 < Dkp, first = !q.half;
+    auto stage_a = [&](const float *rec, int n) {
+        stage_block<NT_C, 32>(se + (n & 1) * 2 * C, 2 * C, rec + R.eG, 2 * C, 1, 2 * C);
+        stage_block<NT_C, 8>(sU, LO, rec + R.dV + j0, Dvp, C, VS);
+        stage_keys<T>(p, q, sK, n);
         cp_async_commit_group();
     };
-    auto stage_b = [&](int n) {
-        const Unit u = unit_of(p, bh, n);
-        stage_block<NT_C, 32>(sW, LD, rec0 + (int64_t)n * R.size + R.W, Dkp, C, Dkp);
-        stage_rows<T>(sQ, (const T *)p.q + u.row0 * p.Dk, (int64_t)p.H * p.Dk, u.len, p.Dk, Dkp, p.wide_k);
-        cp_async_commit_group();
-    };
-    float pre[PER], pe = 0.f;  // this thread's elements of dO's columns, and its e^G or e^D
-    auto fetch = [&](int n) {
-        const Unit u = unit_of(p, bh, n);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int r = (tid + i * NT_C) / VS, c = (tid + i * NT_C) % VS;
-            pre[i] = (r < u.len && j0 + c < p.Dv)
-                         ? load_elem((const T *)p.dO, (u.row0 + (int64_t)r * p.H) * p.Dv + j0 + c)
-                         : 0.f;
-        }
-        if (tid < 2 * C) pe = rec0[(int64_t)n * R.size + R.eG + tid];
-    };
-    const int m0 = 16 * (warp & 7), n0 = 16 * (warp >> 3);
-    const int r0 = 16 * (warp & 3), c0 = 16 * ((warp >> 2) & 1), half = warp >> 3;
-    const int kmid = (3 * Dkp / 8) & ~7;  // the first group has the product with M, and the smaller part of K dS
     float dS[1][2][4] = {};
     tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
         r += m0;
         c += n0;
         if (r < p.Dk && j0 + c < p.Dv && p.dST) dS[i][j][e] = p.dST[(bh * p.Dk + r) * p.Dv + j0 + c];
     });
-    stage_a(p.Nc - 1);
-    fetch(p.Nc - 1);
-    for (int n = p.Nc - 1; n >= 0; --n) {
-        float *rec = rec0 + (int64_t)n * R.size;
-        __syncthreads();  // everyone has left the previous step: its Q, W, dO, dV' and dS are read
-        stage_b(n);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) sdO[(tid + i * NT_C) / VS * LO + (tid + i * NT_C) % VS] = pre[i];
-        if (tid < 2 * C) se[tid] = pe;
-        if (m0 < Dkp)  // the gradient of the state leaving the chunk
+    float *rec = const_cast<float *>(q.rec0) + (int64_t)(p.Nc - 1) * R.size;
+    stage_a(rec, p.Nc - 1);
+    for (int n = p.Nc - 1; n >= 0; --n, rec -= R.size) {
+        const float *en = se + (n & 1) * 2 * C;
+        __syncthreads();  // everyone has left the previous step: its W, Q^T e^G dO, dV' and dS are read
+        stage_block<NT_C, 32>(sW, LD, rec + R.W, Dkp, C, Dkp);
+        stage_block<NT_C, 8>(sH, LO, rec + R.dS + j0, Dvp, Dkp, VS);
+        cp_async_commit_group();
+        if (own)
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 sS[(m0 + r) * LS + n0 + c] = tf32::split2(dS[i][j][e]);
-                if (!(e & 1))
-                    *reinterpret_cast<float2 *>(rec + R.dS + (int64_t)(m0 + r) * Dvp + j0 + n0 + c) =
-                        make_float2(dS[i][j][e], dS[i][j][e + 1]);
             });
-        cp_async_wait<1>();  // M and K of chunk n
+        cp_async_wait<1>();  // K and M^T dO of chunk n
         __syncthreads();
-        // dV' = M^T dO + e^D (K dS_next)
-        float v[1][2][4] = {}, x[1][2][4] = {};
-        tf32::tile<1, 2, false, true, EX, false, true>(x, sK + r0 * LD, LD, sS + c0, LS, half ? kmid : 0,
-                                                       half ? Dkp : kmid);
-        if (half)
-            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { sY[(r0 + r) * LO + c0 + c] = x[i][j][e]; });
-        else
-            tf32::tile<1, 2, true, true, false, EX, true>(v, sM + r0, LC, sdO + c0, LO, r0, C);
-        __syncthreads();  // M, K and dO are read; the other half of the sum
-        if (!half)
+        float x[1][2][4] = {}, v[1][2][4] = {};
+        tf32::tile<1, 2, false, true, EX, false, true>(x, sK + r0 * LD, LD, sS + c0, LS, first ? 0 : kmid,
+                                                       first ? kmid : Dkp);
+        tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
+            if (first) v[i][j][e] = sU[(r0 + r) * LO + c0 + c];
+            else sY[(r0 + r) * LO + c0 + c] = x[i][j][e];
+        });
+        __syncthreads();  // K and M^T dO are read; the other half of the sum
+        if (n > 0) stage_a(rec - R.size, n - 1);
+        if (first)
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 r += r0;
                 c += c0;
-                v[i][j][e] = fmaf(se[C + r], x[i][j][e] + sY[r * LO + c], v[i][j][e]);
-                sdV[r * LV + c] = tf32::split2(-v[i][j][e]);
+                v[i][j][e] = fmaf(en[C + r], x[i][j][e] + sY[r * LO + c], v[i][j][e]);
+                sdV[r * LS + c] = tf32::split2(-v[i][j][e]);
                 if (e & 1)
-                    *reinterpret_cast<float2 *>(rec + R.dV + (int64_t)r * Dvp + j0 + c - 1) =
-                        make_float2(v[i][j][e - 1], v[i][j][e]);
+                    *reinterpret_cast<float2 *>(rec + R.dV + r * Dvp + j0 + c - 1) = make_float2(v[i][j][e - 1], v[i][j][e]);
             });
-        if (n > 0) {
-            stage_a(n - 1);
-            cp_async_wait<1>();  // Q and W of chunk n
-        } else {
-            cp_async_wait<0>();
-        }
-        __syncthreads();  // the sums are read: e^G dO over them
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int r = (tid + i * NT_C) / VS, c = (tid + i * NT_C) % VS;
-            sgO[r * LV + c] = tf32::split2(se[r] * pre[i]);
-        }
-        if (n > 0) fetch(n - 1);
-        float add[1][2][4] = {}, sub[1][2][4] = {};
-        if (m0 < Dkp) tf32::tile<1, 2, true, true, false, false, true>(sub, sW + m0, LD, sdV + n0, LV, 0, C);
-        __syncthreads();  // e^G dO
-        if (m0 < Dkp) {   // dS <- gamma dS_next + Q^T (e^G dO) - W^T dV'
-            const float gamma = se[C - 1];
-            tf32::tile<1, 2, true, true, EX, false, true>(add, sQ + m0, LD, sgO + n0, LV, 0, C);
-            tf32::each<1, 2>([&](int i, int j, int e, int, int) {
-                dS[i][j][e] = fmaf(gamma, dS[i][j][e], add[i][j][e] + sub[i][j][e]);
+        if (n > 0) cp_async_wait<1>();  // W and Q^T e^G dO of chunk n
+        else cp_async_wait<0>();
+        __syncthreads();
+        if (own) {
+            const float gamma = en[C - 1];
+            float sub[1][2][4] = {};
+            tf32::tile<1, 2, true, true, false, false, true>(sub, sW + m0, LD, sdV + n0, LS, 0, C);
+            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
+                if (!(e & 1))  // the gradient of the state leaving the chunk, over Q^T e^G dO, which has been copied
+                    *reinterpret_cast<float2 *>(rec + R.dS + (m0 + r) * Dvp + j0 + n0 + c) =
+                        make_float2(dS[i][j][e], dS[i][j][e + 1]);
+            });
+            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
+                dS[i][j][e] = fmaf(gamma, dS[i][j][e], sH[(m0 + r) * LO + n0 + c] + sub[i][j][e]);
             });
         }
     }
@@ -589,8 +583,8 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     constexpr bool EX = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t gb_sm[];
     double *sG = reinterpret_cast<double *>(gb_sm);
-    float *bS = reinterpret_cast<float *>(sG + C);        // S, then dS_next [128][LD]; then V and K [64][LD]
-    float *bO = bS + 128 * LD;                             // dO [64][LD]; then T [64][LC]; then row sums
+    float *bS = reinterpret_cast<float *>(sG + C);        // S, then dS_next [128][LD]; then V and K (their type) [64][LD]
+    float *bO = bS + 128 * LD;                             // dO (its type) [64][LD]; then T [64][LC]; then row sums
     float *bdV = bO + C * LD;                              // dV' [64][LD]; then T^T dT [64][LC]; then pair sums
     float *bdW = bdV + C * LD;                             // dW [64][LD]; then dP' [64][LC]
     float *bV = bdW + C * LD;                              // V' [64][LD]; then dT [64][LC]; then Q [64][LD]
@@ -610,8 +604,9 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     stage_block<NT_P, 32>(bS, LD, rec + R.S, Dvp, Dkp, Dvp);
     stage_block<NT_P, 32>(bdV, LD, rec + R.dV, Dvp, C, Dvp);
     stage_block<NT_P, 32>(bV, LD, rec + R.V, Dvp, C, Dvp);
+    T *sO = reinterpret_cast<T *>(bO);
+    stage_rows<T, NT_P>(sO, (const T *)p.dO + u.row0 * Dv, rv, len, Dv, Dvp, p.wide_v);
     cp_async_commit_group();
-    load_rows<T, NT_P>(bO, LD, (const T *)p.dO + u.row0 * Dv, rv, len, Dv, Dvp, p.wide_v);
     if (tid < C) {
         sG[tid] = reinterpret_cast<const double *>(rec + R.G)[tid];
         seG[tid] = rec[R.eG + tid];
@@ -636,7 +631,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     };
     if (inK) {
         fetch_pairs(gq);
-        tf32::tile<2, 2, false, false, EX, false>(dq, bO + r0 * LD, LD, bS + c0 * LD, LD, 0, Dvp);
+        tf32::tile<2, 2, false, false, EX, false>(dq, sO + r0 * LD, LD, bS + c0 * LD, LD, 0, Dvp);
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
             dq[i][j][e] *= seG[r0 + r];
             late[i][e >> 1] = fmaf(dq[i][j][e], e & 1 ? at[i][j][e >> 1].y : at[i][j][e >> 1].x, late[i][e >> 1]);
@@ -651,7 +646,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             if (!(e & 1)) M[i][e >> 1] = *reinterpret_cast<const float2 *>(rec + R.M + (r0 + r) * C + c1 + c);
         });
-        if (tri) tf32::tile<2, 1, false, false, EX, false>(m, bO + r0 * LD, LD, bV + c1 * LD, LD, 0, Dvp);
+        if (tri) tf32::tile<2, 1, false, false, EX, false>(m, sO + r0 * LD, LD, bV + c1 * LD, LD, 0, Dvp);
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             r += r0;
             c += c1;
@@ -694,11 +689,12 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
         });
     }
     __syncthreads();
-    float *sV = bS, *sK = bS + C * LD, *sT = bO, *sdT = bV;
+    T *sV = reinterpret_cast<T *>(bS), *sK = sV + C * LD;
+    float *sT = bO, *sdT = bV;
     stage_block<NT_P, 16>(sT, LC, rec + R.T, C, C, C);
+    stage_rows<T, NT_P>(sV, (const T *)p.v + u.row0 * Dv, rv, len, Dv, Dvp, p.wide_v);
+    stage_rows<T, NT_P>(sK, gk, rk, len, Dk, Dkp, p.wide_k);
     cp_async_commit_group();
-    load_rows<T, NT_P>(sV, LD, (const T *)p.v + u.row0 * Dv, rv, len, Dv, Dvp, p.wide_v);
-    load_rows<T, NT_P>(sK, LD, gk, rk, len, Dk, Dkp, p.wide_k);
     cp_async_wait<0>();
     __syncthreads();
     {  // dT = dV' Bv^T + dW Bk^T, on and below the diagonal (T has nothing above it)
@@ -720,7 +716,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
             r += r0;
             c += c0;
-            db[i][e >> 1] = fmaf(a[i][j][e], sV[r * LD + c], db[i][e >> 1]);
+            db[i][e >> 1] = fmaf(a[i][j][e], load_elem(sV, r * LD + c), db[i][e >> 1]);
             store_pair(p.dv + (u.row0 + (int64_t)r * p.H) * Dv, c - (e & 1), Dv, r < len && (e & 1), p.pair_v,
                        sb[r] * a[i][j][e & 2], sb[r] * a[i][j][e | 1]);
         });
@@ -730,7 +726,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
         tf32::tile<2, 2, true, true, false, false>(a, sT + r0, LC, bdW + c0, LD, r0, C);
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
             r += r0;
-            const float x = a[i][j][e] * seG[r], xk = x * sK[r * LD + c0 + c];
+            const float x = a[i][j][e] * seG[r], xk = x * load_elem(sK, r * LD + c0 + c);
             db[i][e >> 1] += xk;
             late[i][e >> 1] = fmaf(sb[r], xk, late[i][e >> 1]);
             dk[i][j][e] = fmaf(sb[r], x, dk[i][j][e]);
@@ -740,8 +736,9 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     tf32::tile<2, 1, true, true, false, false>(y, sT + r0, LC, sdT + c1, LC, r0, C);
     __syncthreads();
     tf32::each<2, 1>([&](int i, int j, int e, int r, int c) { bdV[(r0 + r) * LC + c1 + c] = y[i][j][e]; });
-    float *sQ = bV;
-    load_rows<T, NT_P>(sQ, LD, gq, rk, len, Dk, Dkp, p.wide_k);
+    T *sQ = reinterpret_cast<T *>(bV);
+    stage_rows<T, NT_P>(sQ, gq, rk, len, Dk, Dkp, p.wide_k);
+    cp_async_commit_group();
     __syncthreads();
     {  // dA = -(T^T dT) T^T (i < r);  dP' = beta dA E
         float a[2][1][4] = {};
@@ -764,6 +761,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
             bdW[r * LC + c] = d;
         });
     }
+    cp_async_wait<0>();  // q
     __syncthreads();
     if (inK) {
         tf32::tile<2, 2, false, true, false, EX>(dq, sM + r0 * LC, LC, sK + c0, LD, 0, r0 + 32);
@@ -853,14 +851,14 @@ size_t gdn_bwd_workspace(int64_t B, int64_t S, int H, int Dk, int Dv) {
 template <typename T>
 kda_status_t gb_launch(GbArgs p, int64_t nbh, cudaStream_t st) {
     const int64_t units = nbh * p.Nc, jobs = 2 * nbh * p.nslice;
-    cudaFuncSetAttribute(gb_prep_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PREP_SMEM);
+    cudaFuncSetAttribute(gb_prep_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep_smem<T>());
     cudaFuncSetAttribute(gb_chain_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain_smem<T>());
     cudaFuncSetAttribute(gb_grad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GRAD_SMEM);
     p.wide_k = p.Dk * (int)sizeof(T) % 16 == 0 && aligned_to(p.q, 16) && aligned_to(p.k, 16);
     p.wide_v = p.Dv * (int)sizeof(T) % 16 == 0 && aligned_to(p.v, 16) && aligned_to(p.dO, 16);
     p.pair_k = p.Dk % 2 == 0 && aligned_to(p.dq, 8) && aligned_to(p.dk, 8);
     p.pair_v = p.Dv % 2 == 0 && aligned_to(p.dv, 8);
-    gb_prep_kernel<T><<<(unsigned)units, NT_P, PREP_SMEM, st>>>(p);
+    gb_prep_kernel<T><<<(unsigned)units, NT_P, prep_smem<T>(), st>>>(p);
     KDA_TRY(check_launch("gb_prep_kernel"));
     gb_chain_kernel<T><<<(unsigned)jobs, NT_C, chain_smem<T>(), st>>>(p);
     KDA_TRY(check_launch("gb_chain_kernel"));

@@ -42,69 +42,112 @@ __device__ __forceinline__ float2 split2(float x) {
     split(x, hi, lo);
     return make_float2(__uint_as_float(hi), __uint_as_float(lo));
 }
-__device__ __forceinline__ float load_elem(const float2 *, int) { return 0.f; }  // (split operands are read whole)
-__device__ __forceinline__ void load2(const float2 *, float &, float &) {}
-using kda::load_elem;
+
+// Neighbouring bf16 rows k = 2t, 2t + 1 of column g of an 8 x 8 block, packed into one register per block; each lane
+// gives the address of a row of 16 bytes (lanes 8b .. 8b + 7: block b).
+__device__ __forceinline__ void ldsm_trans(uint32_t (&r)[1], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x1.trans.shared.b16 {%0}, [%1];" : "=r"(r[0]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm_trans(uint32_t (&r)[2], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
 
 // acc += A B^T over k0 <= k < k1 (multiples of 8), for a warp's MT x 16 rows and NT x 8 columns:
 // acc[i][j] holds (16i + g, 8j + 2t), (.., + 1), (16i + g + 8, ..), (.., + 1) with g = lane / 4, t = lane % 4.
 //   A(m, k) = A[m * lda + k], or A[k * lda + m] with AT;  B(n, k) = B[n * ldb + k], or B[k * ldb + n] with BT.
-// B may be kept split (float2: hi, lo).  AEX / BEX: tf32 holds the operand exactly.  The order of k within an instruction is free, as long as A and
-// B share it: where an operand is contiguous in k, a lane takes neighbouring k (one 8-byte load).
-// Pitches of 8 mod 32 floats make the reads free of bank conflicts (mixed orientations: two-way); for a split B
-// read by k, 2 mod 8 pairs where A is contiguous in k, 4 mod 16 where it is not.
+// Operands are fp32, bf16 (exact; read by k they come through ldmatrix, from rows on 16-byte boundaries) or, B read
+// by k, kept split (float2: hi, lo).  AEX / BEX: tf32 holds the operand exactly.  The order of k within an
+// instruction is free, as long as A and B share it: unless both are fp32 and read by k, a lane takes neighbouring k
+// (one load where the operand is contiguous in k).
+// Pitches of 8 mod 32 floats make the reads free of bank conflicts (fp32 read by k in pairs: two-way); for a split B,
+// 2 mod 8 pairs where k comes in pairs, 4 mod 16 where it does not.
 // CROSS: the lo terms go to accumulators of their own (shorter dependent chains where a warp has few tiles).
 template <int MT, int NT, bool AT, bool BT, bool AEX, bool BEX, bool CROSS = false, typename TA, typename TB>
 __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int lda, const TB *B, int ldb, int k0,
                                      int k1) {
-    constexpr bool PAIR = !(AT && BT);
+    constexpr bool A16 = sizeof(TA) == 2 && AT, B16 = sizeof(TB) == 2 && BT;
+    constexpr bool PAIR = !(AT && BT) || A16 || B16;
+    static_assert(sizeof(TB) != 8 || BT, "split operands are read by k");
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float cross[CROSS ? MT : 1][CROSS ? NT : 1][4] = {};
+    uint32_t arow = 0, brow = 0;  // this lane's row for ldmatrix: k + lane % 8, of block lane / 8
+    if constexpr (A16)
+        arow = (uint32_t)__cvta_generic_to_shared(A + (k0 + (lane & 7)) * lda + ((lane >> 3) & (2 * MT - 1)) * 8);
+    if constexpr (B16) brow = (uint32_t)__cvta_generic_to_shared(B + (k0 + (lane & 7)) * ldb + ((lane >> 3) & (NT - 1)) * 8);
 #pragma unroll 2
     for (int k = k0; k < k1; k += 8) {
         const int ka = PAIR ? k + 2 * t : k + t, kb = PAIR ? ka + 1 : ka + 4;
         uint32_t ah[MT][4], al[MT][4], bh[NT][2], bl[NT][2];
+        if constexpr (A16) {
+            uint32_t r[2 * MT];
+            ldsm_trans(r, arow);
+            arow += 16 * lda;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            float x[4];
-            if (AT) {
-                const TA *p = A + ka * lda + 16 * i + g, *q = A + kb * lda + 16 * i + g;
-                x[0] = load_elem(p, 0);
-                x[1] = load_elem(p, 8);
-                x[2] = load_elem(q, 0);
-                x[3] = load_elem(q, 8);
-            } else if (PAIR) {
-                load2(A + (16 * i + g) * lda + ka, x[0], x[2]);
-                load2(A + (16 * i + g + 8) * lda + ka, x[1], x[3]);
+            for (int i = 0; i < MT; ++i) {
+                ah[i][0] = r[2 * i] << 16;
+                ah[i][2] = r[2 * i] & 0xffff0000u;
+                ah[i][1] = r[2 * i + 1] << 16;
+                ah[i][3] = r[2 * i + 1] & 0xffff0000u;
             }
+        } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (AEX) ah[i][e] = __float_as_uint(x[e]);
-                else split(x[e], ah[i][e], al[i][e]);
+            for (int i = 0; i < MT; ++i) {
+                float x[4];
+                if (AT) {
+                    const TA *p = A + ka * lda + 16 * i + g, *q = A + kb * lda + 16 * i + g;
+                    x[0] = load_elem(p, 0);
+                    x[1] = load_elem(p, 8);
+                    x[2] = load_elem(q, 0);
+                    x[3] = load_elem(q, 8);
+                } else {
+                    load2(A + (16 * i + g) * lda + ka, x[0], x[2]);
+                    load2(A + (16 * i + g + 8) * lda + ka, x[1], x[3]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (AEX) ah[i][e] = __float_as_uint(x[e]);
+                    else split(x[e], ah[i][e], al[i][e]);
+                }
             }
         }
+        if constexpr (B16) {
+            uint32_t r[NT];
+            ldsm_trans(r, brow);
+            brow += 16 * ldb;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            if constexpr (sizeof(TB) == 8) {
-                static_assert(BT, "split operands are read by k");
-                const float2 u = B[ka * ldb + 8 * j + g], v = B[kb * ldb + 8 * j + g];
-                bh[j][0] = __float_as_uint(u.x);
-                bl[j][0] = __float_as_uint(u.y);
-                bh[j][1] = __float_as_uint(v.x);
-                bl[j][1] = __float_as_uint(v.y);
-                continue;
+            for (int j = 0; j < NT; ++j) {
+                bh[j][0] = r[j] << 16;
+                bh[j][1] = r[j] & 0xffff0000u;
             }
-            float x[2];
-            if (BT) {
-                x[0] = load_elem(B, ka * ldb + 8 * j + g);
-                x[1] = load_elem(B, kb * ldb + 8 * j + g);
-            } else {
-                load2(B + (8 * j + g) * ldb + ka, x[0], x[1]);
-            }
+        } else {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (BEX) bh[j][e] = __float_as_uint(x[e]);
-                else split(x[e], bh[j][e], bl[j][e]);
+            for (int j = 0; j < NT; ++j) {
+                if constexpr (sizeof(TB) == 8) {
+                    const float2 u = B[ka * ldb + 8 * j + g], v = B[kb * ldb + 8 * j + g];
+                    bh[j][0] = __float_as_uint(u.x);
+                    bl[j][0] = __float_as_uint(u.y);
+                    bh[j][1] = __float_as_uint(v.x);
+                    bl[j][1] = __float_as_uint(v.y);
+                } else {
+                    float x[2];
+                    if (BT) {
+                        x[0] = load_elem(B, ka * ldb + 8 * j + g);
+                        x[1] = load_elem(B, kb * ldb + 8 * j + g);
+                    } else {
+                        load2(B + (8 * j + g) * ldb + ka, x[0], x[1]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (BEX) bh[j][e] = __float_as_uint(x[e]);
+                        else split(x[e], bh[j][e], bl[j][e]);
+                    }
+                }
             }
         }
 #pragma unroll
