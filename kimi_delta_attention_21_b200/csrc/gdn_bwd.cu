@@ -43,8 +43,8 @@ constexpr int NT_P = 512;   // threads of the per-chunk kernels
 constexpr int NT_C = 512;   // threads of the chain kernel
 constexpr int LP = 130;     // pitch of split [64][128] tiles: 2 mod 8 pairs
 constexpr int VS = 32;      // value columns per chain CTA
-constexpr int LS = 34;      // chain pitch of split [Dk][32] and [64][32] tiles: 2 mod 8 pairs
-constexpr int LO = 40;      // and of plain [.][32] ones
+constexpr int LS = 34;      // chain pitch of the split [Dk][32] state: 2 mod 8 pairs (read in pairs of k)
+constexpr int LO = 36;      // and of plain [.][32] ones
 
 __host__ __device__ inline int pad16(int x) { return (x + 15) & ~15; }
 __host__ __device__ inline int pad32(int x) { return (x + 31) & ~31; }
@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
         const int r0 = 32 * (warp & 1), c0 = 8 * (warp >> 1);
         float kk[2][1][4] = {}, qk[2][1][4] = {};
         if (c0 < r0 + 32) {
-            tf32::tile<2, 1, false, false, EX, EX>(kk, sK + r0 * LD, LD, sK + c0 * LD, LD, 0, Dkp);
-            tf32::tile<2, 1, false, false, EX, EX>(qk, sQ + r0 * LD, LD, sK + c0 * LD, LD, 0, Dkp);
+            tf32::tile<2, 1, false, false, EX, EX>(kk, sK + r0 * LD, LD, sK + c0 * LD, LD, Dkp);
+            tf32::tile<2, 1, false, false, EX, EX>(qk, sQ + r0 * LD, LD, sK + c0 * LD, LD, Dkp);
         }
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             r += r0;
@@ -333,15 +333,15 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
     };
     if (c0 < Dkp) {
         float acc[2][2][4] = {};
-        tf32::tile<2, 2, false, true, false, EX>(acc, sA + r0 * LC, LC, sK + c0, LD, 0, r0 + 32);
+        tf32::tile<2, 2, false, true, false, EX>(acc, sA + r0 * LC, LC, sK + c0, LD, r0 + 32);
         put(rec + R.W, Dkp, acc);
     }
     if (c0 < Dvp) {
         float acc[2][2][4] = {}, o[2][2][4] = {};
-        tf32::tile<2, 2, false, true, false, EX>(acc, sY + r0 * LC, LC, sV + c0, LD, 0, r0 + 32);
+        tf32::tile<2, 2, false, true, false, EX>(acc, sY + r0 * LC, LC, sV + c0, LD, r0 + 32);
         put(rec + R.V, Dvp, acc);
         // M^T dO: what dV' has of the chunk itself
-        tf32::tile<2, 2, true, true, false, EX>(o, sM + r0, LC, sO + c0, LD, r0, C);
+        tf32::tile<2, 2, true, true, false, EX>(o, sM + r0 + r0 * LC, LC, sO + c0 + r0 * LD, LD, C - r0);
         put(rec + R.dV, Dvp, o);
     }
     // Q^T (e^G dO): what dS has of the chunk itself.  32 x 32 of [Dk][Dv] per warp, e^G on the rows of the exact side
@@ -355,12 +355,12 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
             if (c < Dvp) sgO[r * LP + c] = tf32::split2(seG[r] * load_elem(sO, r * LD + c));
         }
         __syncthreads();
-        if (m0 < Dkp && n0 < Dvp) tf32::tile<2, 4, true, true, EX, false>(h, sQ + m0, LD, sgO + n0, LP, 0, C);
+        if (m0 < Dkp && n0 < Dvp) tf32::tile<2, 4, true, true, EX, false>(h, sQ + m0, LD, sgO + n0, LP, C);
     } else {
         __syncthreads();  // M^T dO has read dO
         for (int i = tid; i < C * 128; i += NT_P) sO[(i >> 7) * LD + (i & 127)] *= seG[i >> 7];
         __syncthreads();
-        if (m0 < Dkp && n0 < Dvp) tf32::tile<2, 4, true, true, EX, false>(h, sQ + m0, LD, sO + n0, LD, 0, C);
+        if (m0 < Dkp && n0 < Dvp) tf32::tile<2, 4, true, true, EX, false>(h, sQ + m0, LD, sO + n0, LD, C);
     }
     if (n0 < Dvp)
         tf32::each<2, 4>([&](int i, int j, int e, int r, int c) {
@@ -370,9 +370,25 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
 }
 
 // ---------------------------------------------------------------- the state and its gradient through the chunks
+// What a step reads of its chunk: e^G and e^D, W, K, U or M^T dO, and backwards Q^T (e^G dO).  Two sets: the next
+// chunk's arrive while this one's are used (fp32 keys leave room for one set of K only).
+template <typename T> struct Stage {
+    static constexpr int KEYS = sizeof(T) == 2 ? 2 : 1;
+    float *e, *W, *U, *H;
+    T *K;
+    __device__ Stage(float *base, int set) {
+        e = base + set * 2 * C;
+        W = base + 4 * C + set * C * LD;
+        U = base + 4 * C + 2 * C * LD + set * C * LO;
+        H = base + 4 * C + 2 * C * LD + 2 * C * LO + set * 128 * LO;
+        K = reinterpret_cast<T *>(base + FLOATS) + (KEYS == 2 ? set * C * LD : 0);
+    }
+    static constexpr int FLOATS = 4 * C + 2 * C * LD + 2 * C * LO + 2 * 128 * LO;
+    static constexpr size_t BYTES = FLOATS * sizeof(float) + KEYS * sizeof(T) * C * LD;
+};
 template <typename T> constexpr size_t chain_smem() {
-    // W, [64][32] in and sums, Q^T e^G dO, two of e^G and e^D, V' and S (or their gradients) split, K
-    return sizeof(float) * (C * LD + 2 * C * LO + 128 * LO + 4 * C + 2 * C * LS + 2 * 128 * LS) + sizeof(T) * C * LD;
+    // the two sets, the other half of a sum, V' and S (or their gradients) split
+    return Stage<T>::BYTES + sizeof(float) * (C * LO + 2 * C * 36 + 2 * 128 * LS);
 }
 
 // 16 warps: [64][32] results as 4 x 2 tiles of 16 x 16, the sum over k shared by two groups of warps; [Dk][32] ones
@@ -385,7 +401,8 @@ struct Chain {
     int Dkp, Dvp, j0;
     int64_t row0, rk;   // token rows of the (b, h)
     int m0, n0;         // this warp's part of a [Dk][32] result
-    int r0, c0, half;   // this warp's part of a [64][32] result, and of the sum over k
+    int r0, c0, half;   // this warp's part of a [64][32] result, and its half of the sum over the key channels:
+    int kh, kn;         // kn of them from kh
 };
 
 __device__ __forceinline__ Chain chain_of(const GbArgs &p, int64_t bh, int j0) {
@@ -404,6 +421,9 @@ __device__ __forceinline__ Chain chain_of(const GbArgs &p, int64_t bh, int j0) {
     c.r0 = 16 * (warp & 3);
     c.c0 = 16 * ((warp >> 2) & 1);
     c.half = warp >> 3;
+    const int mid = (c.Dkp / 2 + 7) & ~7;
+    c.kh = c.half ? mid : 0;
+    c.kn = c.half ? c.Dkp - mid : mid;
     return c;
 }
 
@@ -414,20 +434,29 @@ __device__ __forceinline__ void stage_keys(const GbArgs &p, const Chain &c, T *s
                         p.wide_k);
 }
 
-// V' = U - W S,  S <- gamma S + K^T (e^D V').  W and U of the next chunk arrive while K is used, K while W is.
-template <typename T>
+// Two neighbouring values, split, as one 16-byte store (an even column).
+__device__ __forceinline__ void put_split(float2 *dst, float x, float y) {
+    const float2 a = tf32::split2(x), b = tf32::split2(y);
+    *reinterpret_cast<float4 *>(dst) = make_float4(a.x, a.y, b.x, b.y);
+}
+
+// V' = U - W S,  S <- gamma S + K^T (e^D V').  FULL: D_k pads to 128.
+template <typename T, bool FULL>
 __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j0, float *sm) {
     constexpr bool EX = sizeof(T) == 2;
-    float *sW = sm, *sU = sW + C * LD, *sY = sU + C * LO, *se = sY + C * LO;
-    float2 *sVp = reinterpret_cast<float2 *>(se + 2 * C), *sS = sVp + C * LS;
-    T *sK = reinterpret_cast<T *>(sS + 128 * LS);
+    float *sY = sm + Stage<T>::BYTES / sizeof(float);
+    constexpr int LV = EX ? 34 : 36;  // K comes in pairs of k (2 mod 8 pairs) where it comes through ldmatrix
+    float2 *sVp = reinterpret_cast<float2 *>(sY + C * LO), *sS = sVp + C * 36;
     const Chain q = chain_of(p, bh, j0);
     const Rec &R = q.R;
-    const int m0 = q.m0, n0 = q.n0, r0 = q.r0, c0 = q.c0, Dkp = q.Dkp, Dvp = q.Dvp, kmid = (Dkp / 2 + 7) & ~7;
-    const bool own = m0 < Dkp, first = !q.half;
-    auto stage_w = [&](const float *rec) {
-        stage_block<NT_C, 32>(sW, LD, rec + R.W, Dkp, C, Dkp);
-        stage_block<NT_C, 8>(sU, LO, rec + R.V + j0, Dvp, C, VS);
+    const int m0 = q.m0, n0 = q.n0, r0 = q.r0, c0 = q.c0, Dkp = FULL ? 128 : q.Dkp, Dvp = q.Dvp;
+    const bool own = FULL || m0 < Dkp, first = !q.half;
+    auto stage = [&](const float *rec, int n) {
+        const Stage<T> g(sm, n & 1);
+        stage_block<NT_C, 32>(g.e, 2 * C, rec + R.eG, 2 * C, 1, 2 * C);
+        stage_block<NT_C, 32>(g.W, LD, rec + R.W, Dkp, C, Dkp);
+        stage_block<NT_C, 8>(g.U, LO, rec + R.V + j0, Dvp, C, VS);
+        if (EX) stage_keys<T>(p, q, g.K, n);
         cp_async_commit_group();
     };
     float S[1][2][4] = {};
@@ -438,13 +467,16 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
         if (own) sS[r * LS + c] = tf32::split2(S[i][j][e]);
     });
     float *rec = const_cast<float *>(q.rec0);
-    stage_w(rec);
+    stage(rec, 0);
     for (int n = 0; n < p.Nc; ++n, rec += R.size) {
-        cp_async_wait<0>();  // W and U of chunk n
+        const Stage<T> g(sm, n & 1);
+        cp_async_wait<0>();  // this chunk's set
         __syncthreads();
-        stage_block<NT_C, 32>(se, 2 * C, rec + R.eG, 2 * C, 1, 2 * C);
-        stage_keys<T>(p, q, sK, n);
-        cp_async_commit_group();
+        if (n + 1 < p.Nc) stage(rec + R.size, n + 1);
+        if (!EX) {
+            stage_keys<T>(p, q, g.K, n);
+            cp_async_commit_group();
+        }
         if (own)  // the state entering the chunk
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 if (!(e & 1))
@@ -452,52 +484,54 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
                         make_float2(S[i][j][e], S[i][j][e + 1]);
             });
         float v[1][2][4] = {};
-        tf32::tile<1, 2, false, true, false, false, true>(v, sW + r0 * LD, LD, sS + c0, LS, first ? 0 : kmid,
-                                                          first ? kmid : Dkp);
+        tf32::tile<1, 2, false, true, false, false, true, 8>(v, g.W + r0 * LD + q.kh, LD, sS + c0 + q.kh * LS, LS,
+                                                             FULL ? C : q.kn);
         if (!first)
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { sY[(r0 + r) * LO + c0 + c] = v[i][j][e]; });
-        cp_async_wait<0>();  // K of chunk n
-        __syncthreads();     // K, e^D and the other half of the sum
+        if (!EX) cp_async_wait<0>();
+        __syncthreads();  // the other half of the sum
         if (first)
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 r += r0;
                 c += c0;
-                v[i][j][e] = sU[r * LO + c] - (v[i][j][e] + sY[r * LO + c]);
-                sVp[r * LS + c] = tf32::split2(se[C + r] * v[i][j][e]);  // e^D V'
-                if (e & 1)
+                v[i][j][e] = g.U[r * LO + c] - (v[i][j][e] + sY[r * LO + c]);
+                if (e & 1) {
+                    put_split(sVp + r * LV + c - 1, g.e[C + r] * v[i][j][e - 1], g.e[C + r] * v[i][j][e]);  // e^D V'
                     *reinterpret_cast<float2 *>(rec + R.V + r * Dvp + j0 + c - 1) = make_float2(v[i][j][e - 1], v[i][j][e]);
+                }
             });
         __syncthreads();
-        if (n + 1 < p.Nc) stage_w(rec + R.size);
         if (own) {
-            const float gamma = se[C - 1];
+            const float gamma = g.e[C - 1];
             float add[1][2][4] = {};
-            tf32::tile<1, 2, true, true, EX, false, true>(add, sK + m0, LD, sVp + n0, LS, 0, C);
+            tf32::tile<1, 2, true, true, EX, false, true, 8>(add, g.K + m0, LD, sVp + n0, LV, C);
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 S[i][j][e] = fmaf(gamma, S[i][j][e], add[i][j][e]);
-                sS[(m0 + r) * LS + n0 + c] = tf32::split2(S[i][j][e]);
+                if (e & 1) put_split(sS + (m0 + r) * LS + n0 + c - 1, S[i][j][e - 1], S[i][j][e]);
             });
         }
     }
 }
 
 // dV' = M^T dO + e^D (K dS),  dS <- gamma dS + Q^T (e^G dO) - W^T dV', from the last chunk to the first; the two terms
-// with dO are in the record.  K and M^T dO (first half of a step) and W and Q^T (e^G dO) (second half) are refilled with
-// the previous chunk's as soon as their half is done.
-template <typename T>
+// with dO are in the record, where their results take their place.
+template <typename T, bool FULL>
 __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int j0, float *sm) {
     constexpr bool EX = sizeof(T) == 2;
-    float *sW = sm, *sU = sW + C * LD, *sY = sU + C * LO, *se = sY + C * LO, *sH = se + 4 * C;
-    float2 *sdV = reinterpret_cast<float2 *>(sH + 128 * LO), *sS = sdV + C * LS;
-    T *sK = reinterpret_cast<T *>(sS + 128 * LS);
+    float *sY = sm + Stage<T>::BYTES / sizeof(float);
+    constexpr int LV = 36;  // W is read by single k: 4 mod 16 pairs
+    float2 *sdV = reinterpret_cast<float2 *>(sY + C * LO), *sS = sdV + C * 36;
     const Chain q = chain_of(p, bh, j0);
     const Rec &R = q.R;
-    const int m0 = q.m0, n0 = q.n0, r0 = q.r0, c0 = q.c0, Dkp = q.Dkp, Dvp = q.Dvp, kmid = (Dkp / 2 + 7) & ~7;
-    const bool own = m0 < Dkp, first = !q.half;
-    auto stage_a = [&](const float *rec, int n) {
-        stage_block<NT_C, 32>(se + (n & 1) * 2 * C, 2 * C, rec + R.eG, 2 * C, 1, 2 * C);
-        stage_block<NT_C, 8>(sU, LO, rec + R.dV + j0, Dvp, C, VS);
-        stage_keys<T>(p, q, sK, n);
+    const int m0 = q.m0, n0 = q.n0, r0 = q.r0, c0 = q.c0, Dkp = FULL ? 128 : q.Dkp, Dvp = q.Dvp;
+    const bool own = FULL || m0 < Dkp, first = !q.half;
+    auto stage = [&](const float *rec, int n) {
+        const Stage<T> g(sm, n & 1);
+        stage_block<NT_C, 32>(g.e, 2 * C, rec + R.eG, 2 * C, 1, 2 * C);
+        stage_block<NT_C, 32>(g.W, LD, rec + R.W, Dkp, C, Dkp);
+        stage_block<NT_C, 8>(g.U, LO, rec + R.dV + j0, Dvp, C, VS);
+        stage_block<NT_C, 8>(g.H, LO, rec + R.dS + j0, Dvp, Dkp, VS);
+        if (EX) stage_keys<T>(p, q, g.K, n);
         cp_async_commit_group();
     };
     float dS[1][2][4] = {};
@@ -505,53 +539,50 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
         r += m0;
         c += n0;
         if (r < p.Dk && j0 + c < p.Dv && p.dST) dS[i][j][e] = p.dST[(bh * p.Dk + r) * p.Dv + j0 + c];
+        if (own) sS[r * LS + c] = tf32::split2(dS[i][j][e]);
     });
     float *rec = const_cast<float *>(q.rec0) + (int64_t)(p.Nc - 1) * R.size;
-    stage_a(rec, p.Nc - 1);
+    if (!EX) stage_keys<T>(p, q, Stage<T>(sm, 0).K, p.Nc - 1);
+    stage(rec, p.Nc - 1);
     for (int n = p.Nc - 1; n >= 0; --n, rec -= R.size) {
-        const float *en = se + (n & 1) * 2 * C;
-        __syncthreads();  // everyone has left the previous step: its W, Q^T e^G dO, dV' and dS are read
-        stage_block<NT_C, 32>(sW, LD, rec + R.W, Dkp, C, Dkp);
-        stage_block<NT_C, 8>(sH, LO, rec + R.dS + j0, Dvp, Dkp, VS);
-        cp_async_commit_group();
-        if (own)
-            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
-                sS[(m0 + r) * LS + n0 + c] = tf32::split2(dS[i][j][e]);
-            });
-        cp_async_wait<1>();  // K and M^T dO of chunk n
+        const Stage<T> g(sm, n & 1);
+        cp_async_wait<0>();  // this chunk's set
         __syncthreads();
-        float x[1][2][4] = {}, v[1][2][4] = {};
-        tf32::tile<1, 2, false, true, EX, false, true>(x, sK + r0 * LD, LD, sS + c0, LS, first ? 0 : kmid,
-                                                       first ? kmid : Dkp);
-        tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
-            if (first) v[i][j][e] = sU[(r0 + r) * LO + c0 + c];
-            else sY[(r0 + r) * LO + c0 + c] = x[i][j][e];
-        });
-        __syncthreads();  // K and M^T dO are read; the other half of the sum
-        if (n > 0) stage_a(rec - R.size, n - 1);
+        if (n > 0) stage(rec - R.size, n - 1);
+        if (own)  // the gradient of the state leaving the chunk
+            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
+                if (!(e & 1))
+                    *reinterpret_cast<float2 *>(rec + R.dS + (m0 + r) * Dvp + j0 + n0 + c) =
+                        make_float2(dS[i][j][e], dS[i][j][e + 1]);
+            });
+        float x[1][2][4] = {};
+        tf32::tile<1, 2, false, true, EX, false, true, 8>(x, g.K + r0 * LD + q.kh, LD, sS + c0 + q.kh * LS, LS,
+                                                          FULL ? C : q.kn);
+        if (!first)
+            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { sY[(r0 + r) * LO + c0 + c] = x[i][j][e]; });
+        __syncthreads();  // the other half of the sum; K is read
+        if (!EX && n > 0) {
+            stage_keys<T>(p, q, g.K, n - 1);
+            cp_async_commit_group();
+        }
         if (first)
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 r += r0;
                 c += c0;
-                v[i][j][e] = fmaf(en[C + r], x[i][j][e] + sY[r * LO + c], v[i][j][e]);
-                sdV[r * LS + c] = tf32::split2(-v[i][j][e]);
-                if (e & 1)
-                    *reinterpret_cast<float2 *>(rec + R.dV + r * Dvp + j0 + c - 1) = make_float2(v[i][j][e - 1], v[i][j][e]);
+                x[i][j][e] = fmaf(g.e[C + r], x[i][j][e] + sY[r * LO + c], g.U[r * LO + c]);
+                if (e & 1) {
+                    put_split(sdV + r * LV + c - 1, -x[i][j][e - 1], -x[i][j][e]);
+                    *reinterpret_cast<float2 *>(rec + R.dV + r * Dvp + j0 + c - 1) = make_float2(x[i][j][e - 1], x[i][j][e]);
+                }
             });
-        if (n > 0) cp_async_wait<1>();  // W and Q^T e^G dO of chunk n
-        else cp_async_wait<0>();
         __syncthreads();
         if (own) {
-            const float gamma = en[C - 1];
+            const float gamma = g.e[C - 1];
             float sub[1][2][4] = {};
-            tf32::tile<1, 2, true, true, false, false, true>(sub, sW + m0, LD, sdV + n0, LS, 0, C);
+            tf32::tile<1, 2, true, true, false, false, true, 8>(sub, g.W + m0, LD, sdV + n0, LV, C);
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
-                if (!(e & 1))  // the gradient of the state leaving the chunk, over Q^T e^G dO, which has been copied
-                    *reinterpret_cast<float2 *>(rec + R.dS + (m0 + r) * Dvp + j0 + n0 + c) =
-                        make_float2(dS[i][j][e], dS[i][j][e + 1]);
-            });
-            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
-                dS[i][j][e] = fmaf(gamma, dS[i][j][e], sH[(m0 + r) * LO + n0 + c] + sub[i][j][e]);
+                dS[i][j][e] = fmaf(gamma, dS[i][j][e], g.H[(m0 + r) * LO + n0 + c] + sub[i][j][e]);
+                if (e & 1) put_split(sS + (m0 + r) * LS + n0 + c - 1, dS[i][j][e - 1], dS[i][j][e]);
             });
         }
     }
@@ -563,7 +594,7 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
         });
 }
 
-template <typename T>
+template <typename T, bool FULL>
 __global__ void __launch_bounds__(NT_C, 1) gb_chain_kernel(const __grid_constant__ GbArgs p) {
     extern __shared__ __align__(16) uint8_t gb_sm[];
     const int64_t job = blockIdx.x >> 1, bh = job / p.nslice;
@@ -571,8 +602,8 @@ __global__ void __launch_bounds__(NT_C, 1) gb_chain_kernel(const __grid_constant
     const Rec R = make_rec(p.Dk, p.Dv);
     if (!in_bounds(p.ws + bh * p.Nc * R.size, (size_t)p.Nc * R.size * 4, p.ws, p.ws_bytes, p.bounds)) return;
     float *sm = reinterpret_cast<float *>(gb_sm);
-    if (blockIdx.x & 1) chain_forward<T>(p, bh, j0, sm);
-    else chain_backward<T>(p, bh, j0, sm);
+    if (blockIdx.x & 1) chain_forward<T, FULL>(p, bh, j0, sm);
+    else chain_backward<T, FULL>(p, bh, j0, sm);
 }
 
 // ---------------------------------------------------------------- per chunk: the gradients
@@ -631,13 +662,13 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     };
     if (inK) {
         fetch_pairs(gq);
-        tf32::tile<2, 2, false, false, EX, false>(dq, sO + r0 * LD, LD, bS + c0 * LD, LD, 0, Dvp);
+        tf32::tile<2, 2, false, false, EX, false>(dq, sO + r0 * LD, LD, bS + c0 * LD, LD, Dvp);
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
             dq[i][j][e] *= seG[r0 + r];
             late[i][e >> 1] = fmaf(dq[i][j][e], e & 1 ? at[i][j][e >> 1].y : at[i][j][e >> 1].x, late[i][e >> 1]);
         });
         float w[2][2][4] = {};
-        tf32::tile<2, 2, false, false, false, false>(w, bdV + r0 * LD, LD, bS + c0 * LD, LD, 0, Dvp);
+        tf32::tile<2, 2, false, false, false, false>(w, bdV + r0 * LD, LD, bS + c0 * LD, LD, Dvp);
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) { bdW[(r0 + r) * LD + c0 + c] = -w[i][j][e]; });
     }
     {  // dM = dO V'^T (i <= r)
@@ -646,7 +677,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             if (!(e & 1)) M[i][e >> 1] = *reinterpret_cast<const float2 *>(rec + R.M + (r0 + r) * C + c1 + c);
         });
-        if (tri) tf32::tile<2, 1, false, false, EX, false>(m, sO + r0 * LD, LD, bV + c1 * LD, LD, 0, Dvp);
+        if (tri) tf32::tile<2, 1, false, false, EX, false>(m, sO + r0 * LD, LD, bV + c1 * LD, LD, Dvp);
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             r += r0;
             c += c1;
@@ -682,7 +713,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     __syncthreads();
     if (inK) {  // dKd = V' dS_next^T (dk = e^D dKd)
         fetch_pairs(gk);
-        tf32::tile<2, 2, false, false, false, false>(dk, bV + r0 * LD, LD, bS + c0 * LD, LD, 0, Dvp);
+        tf32::tile<2, 2, false, false, false, false>(dk, bV + r0 * LD, LD, bS + c0 * LD, LD, Dvp);
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
             dk[i][j][e] *= seD[r0 + r];
             early[i][e >> 1] = fmaf(dk[i][j][e], e & 1 ? at[i][j][e >> 1].y : at[i][j][e >> 1].x, early[i][e >> 1]);
@@ -700,8 +731,8 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     {  // dT = dV' Bv^T + dW Bk^T, on and below the diagonal (T has nothing above it)
         float a[2][1][4] = {}, b[2][1][4] = {};
         if (tri) {
-            tf32::tile<2, 1, false, false, false, EX>(a, bdV + r0 * LD, LD, sV + c1 * LD, LD, 0, Dvp);
-            tf32::tile<2, 1, false, false, false, EX>(b, bdW + r0 * LD, LD, sK + c1 * LD, LD, 0, Dkp);
+            tf32::tile<2, 1, false, false, false, EX>(a, bdV + r0 * LD, LD, sV + c1 * LD, LD, Dvp);
+            tf32::tile<2, 1, false, false, false, EX>(b, bdW + r0 * LD, LD, sK + c1 * LD, LD, Dkp);
         }
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             r += r0;
@@ -712,7 +743,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     __syncthreads();
     if (inV) {  // dBv = T^T dV'
         float a[2][2][4] = {};
-        tf32::tile<2, 2, true, true, false, false>(a, sT + r0, LC, bdV + c0, LD, r0, C);
+        tf32::tile<2, 2, true, true, false, false>(a, sT + r0 + r0 * LC, LC, bdV + c0 + r0 * LD, LD, C - r0);
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
             r += r0;
             c += c0;
@@ -723,7 +754,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     }
     if (inK) {  // dBk = T^T dW
         float a[2][2][4] = {};
-        tf32::tile<2, 2, true, true, false, false>(a, sT + r0, LC, bdW + c0, LD, r0, C);
+        tf32::tile<2, 2, true, true, false, false>(a, sT + r0 + r0 * LC, LC, bdW + c0 + r0 * LD, LD, C - r0);
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
             r += r0;
             const float x = a[i][j][e] * seG[r], xk = x * load_elem(sK, r * LD + c0 + c);
@@ -733,7 +764,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
         });
     }
     float y[2][1][4] = {};  // T^T dT
-    tf32::tile<2, 1, true, true, false, false>(y, sT + r0, LC, sdT + c1, LC, r0, C);
+    tf32::tile<2, 1, true, true, false, false>(y, sT + r0 + r0 * LC, LC, sdT + c1 + r0 * LC, LC, C - r0);
     __syncthreads();
     tf32::each<2, 1>([&](int i, int j, int e, int r, int c) { bdV[(r0 + r) * LC + c1 + c] = y[i][j][e]; });
     T *sQ = reinterpret_cast<T *>(bV);
@@ -746,7 +777,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             if (!(e & 1)) Pp[i][e >> 1] = *reinterpret_cast<const float2 *>(rec + R.P + (r0 + r) * C + c1 + c);
         });
-        if (tri) tf32::tile<2, 1, false, false, false, false>(a, bdV + r0 * LC, LC, sT + c1 * LC, LC, 0, c1 + 8);
+        if (tri) tf32::tile<2, 1, false, false, false, false>(a, bdV + r0 * LC, LC, sT + c1 * LC, LC, c1 + 8);
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             r += r0;
             c += c1;
@@ -764,10 +795,10 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     cp_async_wait<0>();  // q
     __syncthreads();
     if (inK) {
-        tf32::tile<2, 2, false, true, false, EX>(dq, sM + r0 * LC, LC, sK + c0, LD, 0, r0 + 32);
-        tf32::tile<2, 2, false, true, false, EX>(dk, bdW + r0 * LC, LC, sK + c0, LD, 0, r0 + 32);
-        tf32::tile<2, 2, true, true, false, EX>(dk, bdW + r0, LC, sK + c0, LD, r0, C);
-        tf32::tile<2, 2, true, true, false, EX>(dk, sM + r0, LC, sQ + c0, LD, r0, C);
+        tf32::tile<2, 2, false, true, false, EX>(dq, sM + r0 * LC, LC, sK + c0, LD, r0 + 32);
+        tf32::tile<2, 2, false, true, false, EX>(dk, bdW + r0 * LC, LC, sK + c0, LD, r0 + 32);
+        tf32::tile<2, 2, true, true, false, EX>(dk, bdW + r0 + r0 * LC, LC, sK + c0 + r0 * LD, LD, C - r0);
+        tf32::tile<2, 2, true, true, false, EX>(dk, sM + r0 + r0 * LC, LC, sQ + c0 + r0 * LD, LD, C - r0);
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
             r += r0;
             c += c0;
@@ -852,7 +883,8 @@ template <typename T>
 kda_status_t gb_launch(GbArgs p, int64_t nbh, cudaStream_t st) {
     const int64_t units = nbh * p.Nc, jobs = 2 * nbh * p.nslice;
     cudaFuncSetAttribute(gb_prep_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep_smem<T>());
-    cudaFuncSetAttribute(gb_chain_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain_smem<T>());
+    const auto chain = pad16(p.Dk) == 128 ? gb_chain_kernel<T, true> : gb_chain_kernel<T, false>;
+    cudaFuncSetAttribute(chain, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain_smem<T>());
     cudaFuncSetAttribute(gb_grad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GRAD_SMEM);
     p.wide_k = p.Dk * (int)sizeof(T) % 16 == 0 && aligned_to(p.q, 16) && aligned_to(p.k, 16);
     p.wide_v = p.Dv * (int)sizeof(T) % 16 == 0 && aligned_to(p.v, 16) && aligned_to(p.dO, 16);
@@ -860,7 +892,7 @@ kda_status_t gb_launch(GbArgs p, int64_t nbh, cudaStream_t st) {
     p.pair_v = p.Dv % 2 == 0 && aligned_to(p.dv, 8);
     gb_prep_kernel<T><<<(unsigned)units, NT_P, prep_smem<T>(), st>>>(p);
     KDA_TRY(check_launch("gb_prep_kernel"));
-    gb_chain_kernel<T><<<(unsigned)jobs, NT_C, chain_smem<T>(), st>>>(p);
+    chain<<<(unsigned)jobs, NT_C, chain_smem<T>(), st>>>(p);
     KDA_TRY(check_launch("gb_chain_kernel"));
     gb_grad_kernel<T><<<(unsigned)units, NT_P, GRAD_SMEM, st>>>(p);
     return check_launch("gb_grad_kernel");

@@ -58,7 +58,7 @@ __device__ __forceinline__ void ldsm_trans(uint32_t (&r)[4], uint32_t addr) {
                  : "memory");
 }
 
-// acc += A B^T over k0 <= k < k1 (multiples of 8), for a warp's MT x 16 rows and NT x 8 columns:
+// acc += A B^T over k < K (a multiple of 8; UNROLL steps of 8 at a time), for a warp's MT x 16 rows and NT x 8 columns:
 // acc[i][j] holds (16i + g, 8j + 2t), (.., + 1), (16i + g + 8, ..), (.., + 1) with g = lane / 4, t = lane % 4.
 //   A(m, k) = A[m * lda + k], or A[k * lda + m] with AT;  B(n, k) = B[n * ldb + k], or B[k * ldb + n] with BT.
 // Operands are fp32, bf16 (exact; read by k they come through ldmatrix, from rows on 16-byte boundaries) or, B read
@@ -68,20 +68,21 @@ __device__ __forceinline__ void ldsm_trans(uint32_t (&r)[4], uint32_t addr) {
 // Pitches of 8 mod 32 floats make the reads free of bank conflicts (fp32 read by k in pairs: two-way); for a split B,
 // 2 mod 8 pairs where k comes in pairs, 4 mod 16 where it does not.
 // CROSS: the lo terms go to accumulators of their own (shorter dependent chains where a warp has few tiles).
-template <int MT, int NT, bool AT, bool BT, bool AEX, bool BEX, bool CROSS = false, typename TA, typename TB>
-__device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int lda, const TB *B, int ldb, int k0,
-                                     int k1) {
+template <int MT, int NT, bool AT, bool BT, bool AEX, bool BEX, bool CROSS = false, int UNROLL = 2, typename TA,
+          typename TB>
+__device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int lda, const TB *B, int ldb,
+                                     int K) {
     constexpr bool A16 = sizeof(TA) == 2 && AT, B16 = sizeof(TB) == 2 && BT;
     constexpr bool PAIR = !(AT && BT) || A16 || B16;
     static_assert(sizeof(TB) != 8 || BT, "split operands are read by k");
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float cross[CROSS ? MT : 1][CROSS ? NT : 1][4] = {};
-    uint32_t arow = 0, brow = 0;  // this lane's row for ldmatrix: k + lane % 8, of block lane / 8
+    float cross[2][CROSS ? MT : 1][CROSS ? NT : 1][4] = {};
+    uint32_t arow = 0, brow = 0;  // this lane's row for ldmatrix: k = lane % 8, of block lane / 8
     if constexpr (A16)
-        arow = (uint32_t)__cvta_generic_to_shared(A + (k0 + (lane & 7)) * lda + ((lane >> 3) & (2 * MT - 1)) * 8);
-    if constexpr (B16) brow = (uint32_t)__cvta_generic_to_shared(B + (k0 + (lane & 7)) * ldb + ((lane >> 3) & (NT - 1)) * 8);
-#pragma unroll 2
-    for (int k = k0; k < k1; k += 8) {
+        arow = (uint32_t)__cvta_generic_to_shared(A + (lane & 7) * lda + ((lane >> 3) & (2 * MT - 1)) * 8);
+    if constexpr (B16) brow = (uint32_t)__cvta_generic_to_shared(B + (lane & 7) * ldb + ((lane >> 3) & (NT - 1)) * 8);
+#pragma unroll UNROLL
+    for (int k = 0; k < K; k += 8) {
         const int ka = PAIR ? k + 2 * t : k + t, kb = PAIR ? ka + 1 : ka + 4;
         uint32_t ah[MT][4], al[MT][4], bh[NT][2], bl[NT][2];
         if constexpr (A16) {
@@ -154,8 +155,8 @@ __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int l
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                if (!BEX) mma(CROSS ? cross[CROSS ? i : 0][CROSS ? j : 0] : acc[i][j], ah[i], bl[j]);
-                if (!AEX) mma(CROSS ? cross[CROSS ? i : 0][CROSS ? j : 0] : acc[i][j], al[i], bh[j]);
+                if (!BEX) mma(CROSS ? cross[0][CROSS ? i : 0][CROSS ? j : 0] : acc[i][j], ah[i], bl[j]);
+                if (!AEX) mma(CROSS ? cross[1][CROSS ? i : 0][CROSS ? j : 0] : acc[i][j], al[i], bh[j]);
             }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -168,7 +169,8 @@ __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int l
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] += cross[CROSS ? i : 0][CROSS ? j : 0][e];
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] += cross[0][CROSS ? i : 0][CROSS ? j : 0][e] + cross[1][CROSS ? i : 0][CROSS ? j : 0][e];
     }
 }
 
