@@ -484,7 +484,7 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
                         make_float2(S[i][j][e], S[i][j][e + 1]);
             });
         float v[1][2][4] = {};
-        tf32::tile<1, 2, false, true, false, false, true, 8>(v, g.W + r0 * LD + q.kh, LD, sS + c0 + q.kh * LS, LS,
+        tf32::tile<1, 2, false, true, false, false, 2, 8>(v, g.W + r0 * LD + q.kh, LD, sS + c0 + q.kh * LS, LS,
                                                              FULL ? C : q.kn);
         if (!first)
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { sY[(r0 + r) * LO + c0 + c] = v[i][j][e]; });
@@ -504,7 +504,7 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
         if (own) {
             const float gamma = g.e[C - 1];
             float add[1][2][4] = {};
-            tf32::tile<1, 2, true, true, EX, false, true, 8>(add, g.K + m0, LD, sVp + n0, LV, C);
+            tf32::tile<1, 2, true, true, EX, false, 2, 8>(add, g.K + m0, LD, sVp + n0, LV, C);
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 S[i][j][e] = fmaf(gamma, S[i][j][e], add[i][j][e]);
                 if (e & 1) put_split(sS + (m0 + r) * LS + n0 + c - 1, S[i][j][e - 1], S[i][j][e]);
@@ -556,7 +556,7 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
                         make_float2(dS[i][j][e], dS[i][j][e + 1]);
             });
         float x[1][2][4] = {};
-        tf32::tile<1, 2, false, true, EX, false, true, 8>(x, g.K + r0 * LD + q.kh, LD, sS + c0 + q.kh * LS, LS,
+        tf32::tile<1, 2, false, true, EX, false, 2, 8>(x, g.K + r0 * LD + q.kh, LD, sS + c0 + q.kh * LS, LS,
                                                           FULL ? C : q.kn);
         if (!first)
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { sY[(r0 + r) * LO + c0 + c] = x[i][j][e]; });
@@ -579,7 +579,7 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
         if (own) {
             const float gamma = g.e[C - 1];
             float sub[1][2][4] = {};
-            tf32::tile<1, 2, true, true, false, false, true, 8>(sub, g.W + m0, LD, sdV + n0, LV, C);
+            tf32::tile<1, 2, true, true, false, false, 2, 8>(sub, g.W + m0, LD, sdV + n0, LV, C);
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 dS[i][j][e] = fmaf(gamma, dS[i][j][e], g.H[(m0 + r) * LO + n0 + c] + sub[i][j][e]);
                 if (e & 1) put_split(sS + (m0 + r) * LS + n0 + c - 1, dS[i][j][e - 1], dS[i][j][e]);

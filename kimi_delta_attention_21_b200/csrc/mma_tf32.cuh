@@ -67,8 +67,10 @@ __device__ __forceinline__ void ldsm_trans(uint32_t (&r)[4], uint32_t addr) {
 // (one load where the operand is contiguous in k).
 // Pitches of 8 mod 32 floats make the reads free of bank conflicts (fp32 read by k in pairs: two-way); for a split B,
 // 2 mod 8 pairs where k comes in pairs, 4 mod 16 where it does not.
-// CROSS: the lo terms go to accumulators of their own (shorter dependent chains where a warp has few tiles).
-template <int MT, int NT, bool AT, bool BT, bool AEX, bool BEX, bool CROSS = false, int UNROLL = 2, typename TA,
+// The lo terms have accumulators of their own, so that the tensor core, which truncates as it adds, does so once per
+// step of 8 on the large sums; CROSS = 2 keeps the two kinds apart (shorter dependent chains where a warp has few
+// tiles).
+template <int MT, int NT, bool AT, bool BT, bool AEX, bool BEX, int CROSS = 1, int UNROLL = 2, typename TA,
           typename TB>
 __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int lda, const TB *B, int ldb,
                                      int K) {
@@ -76,7 +78,7 @@ __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int l
     constexpr bool PAIR = !(AT && BT) || A16 || B16;
     static_assert(sizeof(TB) != 8 || BT, "split operands are read by k");
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float cross[2][CROSS ? MT : 1][CROSS ? NT : 1][4] = {};
+    float cross[CROSS][MT][NT][4] = {};
     uint32_t arow = 0, brow = 0;  // this lane's row for ldmatrix: k = lane % 8, of block lane / 8
     if constexpr (A16)
         arow = (uint32_t)__cvta_generic_to_shared(A + (lane & 7) * lda + ((lane >> 3) & (2 * MT - 1)) * 8);
@@ -155,22 +157,22 @@ __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int l
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                if (!BEX) mma(CROSS ? cross[0][CROSS ? i : 0][CROSS ? j : 0] : acc[i][j], ah[i], bl[j]);
-                if (!AEX) mma(CROSS ? cross[1][CROSS ? i : 0][CROSS ? j : 0] : acc[i][j], al[i], bh[j]);
+                if (!BEX) mma(cross[0][i][j], ah[i], bl[j]);
+                if (!AEX) mma(cross[CROSS - 1][i][j], al[i], bh[j]);
             }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j) mma(acc[i][j], ah[i], bh[j]);
     }
-    if (CROSS && !(AEX && BEX)) {
+    if (!(AEX && BEX)) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] += cross[0][CROSS ? i : 0][CROSS ? j : 0][e] + cross[1][CROSS ? i : 0][CROSS ? j : 0][e];
+                    acc[i][j][e] += CROSS == 2 ? cross[0][i][j][e] + cross[CROSS - 1][i][j][e] : cross[0][i][j][e];
     }
 }
 
