@@ -607,20 +607,42 @@ __global__ void __launch_bounds__(NT_C, 1) gb_chain_kernel(const __grid_constant
 }
 
 // ---------------------------------------------------------------- per chunk: the gradients
-constexpr size_t GRAD_SMEM = sizeof(float) * (128 * LD + 4 * C * LD + C * LC + 3 * C + 32) + sizeof(double) * C;
+// The products over the value channels (dQg, dKd, dW, dM, the first part of dT) are summed over pieces of 32 channels,
+// whose operands arrive while the piece before them is used; fp32 inputs leave room for one set of them.
+constexpr int LQ = 40;  // pitch of the pieces: 8 mod 32, and for bf16 pairs distinct banks
+template <typename T> struct Piece {
+    static constexpr int SETS = sizeof(T) == 2 ? 2 : 1;
+    static constexpr size_t BYTES = sizeof(float) * (2 * 128 + 2 * C) * LQ + 2 * sizeof(T) * C * LQ;
+    float *S, *dS, *dV, *V;  // [128][LQ], [64][LQ]
+    T *dO, *v;
+    __device__ Piece(uint8_t *base, int i) {
+        S = reinterpret_cast<float *>(base + (SETS == 2 ? (i & 1) * BYTES : 0));
+        dS = S + 128 * LQ;
+        dV = dS + 128 * LQ;
+        V = dV + C * LQ;
+        dO = reinterpret_cast<T *>(V + C * LQ);
+        v = dO + C * LQ;
+    }
+};
+// what takes their place afterwards: dW and dV' [64][LD], dT and T^T dT [64][LC]
+constexpr size_t AFTER_BYTES = sizeof(float) * (2 * C * LD + 2 * C * LC);
+template <typename T> constexpr size_t grad_area() {
+    return Piece<T>::SETS * Piece<T>::BYTES > AFTER_BYTES ? Piece<T>::SETS * Piece<T>::BYTES : AFTER_BYTES;
+}
+template <typename T> constexpr size_t grad_smem() {
+    return sizeof(double) * C + sizeof(float) * (2 * C * LC + 3 * C + 32) + 2 * sizeof(T) * C * LD + grad_area<T>();
+}
 
 template <typename T>
 __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant__ GbArgs p) {
     constexpr bool EX = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t gb_sm[];
     double *sG = reinterpret_cast<double *>(gb_sm);
-    float *bS = reinterpret_cast<float *>(sG + C);        // S, then dS_next [128][LD]; then V and K (their type) [64][LD]
-    float *bO = bS + 128 * LD;                             // dO (its type) [64][LD]; then T [64][LC]; then row sums
-    float *bdV = bO + C * LD;                              // dV' [64][LD]; then T^T dT [64][LC]; then pair sums
-    float *bdW = bdV + C * LD;                             // dW [64][LD]; then dP' [64][LC]
-    float *bV = bdW + C * LD;                              // V' [64][LD]; then dT [64][LC]; then Q [64][LD]
-    float *sM = bV + C * LD;                               // dM * E [64][LC]
+    float *sT = reinterpret_cast<float *>(sG + C), *sM = sT + C * LC;  // T, dM * E [64][LC]
     float *seG = sM + C * LC, *seD = seG + C, *sb = seD + C, *sred = sb + C;
+    T *sK = reinterpret_cast<T *>(sred + 32), *sQ = sK + C * LD;        // [64][LD]
+    uint8_t *area = reinterpret_cast<uint8_t *>(sQ + C * LD);
+    float *sdW = reinterpret_cast<float *>(area), *sdV = sdW + C * LD, *sdT = sdV + C * LD, *sY = sdT + C * LC;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int64_t bh = blockIdx.x / p.Nc;
     const int n = (int)(blockIdx.x - bh * p.Nc);
@@ -630,13 +652,39 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     const float *rec = p.ws + (int64_t)blockIdx.x * R.size;
     if (!in_bounds(rec, (size_t)R.size * 4, p.ws, p.ws_bytes, p.bounds)) return;
     const int64_t rk = (int64_t)p.H * Dk, rv = (int64_t)p.H * Dv;
-    const T *gq = (const T *)p.q + u.row0 * Dk, *gk = (const T *)p.k + u.row0 * Dk;
+    const T *gv = (const T *)p.v + u.row0 * Dv, *gO = (const T *)p.dO + u.row0 * Dv;
 
-    stage_block<NT_P, 32>(bS, LD, rec + R.S, Dvp, Dkp, Dvp);
-    stage_block<NT_P, 32>(bdV, LD, rec + R.dV, Dvp, C, Dvp);
-    stage_block<NT_P, 32>(bV, LD, rec + R.V, Dvp, C, Dvp);
-    T *sO = reinterpret_cast<T *>(bO);
-    stage_rows<T, NT_P>(sO, (const T *)p.dO + u.row0 * Dv, rv, len, Dv, Dvp, p.wide_v);
+    auto stage_cols = [&](T *dst, const T *src, int j0) {  // 32 columns of token rows
+        if (p.wide_v) {
+            constexpr int E = 16 / (int)sizeof(T), VPR = 32 / E;
+            const int i = tid, r = i / VPR, c = i % VPR * E;
+            if (i < C * VPR) {
+                const bool in = r < len && j0 + c < Dv;
+                cp_async16_fill(reinterpret_cast<float *>(dst + r * LQ + c),
+                                reinterpret_cast<const float *>(src + (in ? r * rv + j0 + c : 0)), in);
+            }
+        } else {
+            const int c = tid & 31;
+#pragma unroll
+            for (int r = tid >> 5; r < C; r += NT_P / 32)
+                dst[r * LQ + c] = (r < len && j0 + c < Dv) ? src[r * rv + j0 + c] : T(0.f);
+        }
+    };
+    auto stage = [&](int i) {
+        const Piece<T> q(area, i);
+        const int j0 = 32 * i;
+        stage_block<NT_P, 8>(q.S, LQ, rec + R.S + j0, Dvp, Dkp, 32);
+        stage_block<NT_P, 8>(q.dS, LQ, rec + R.dS + j0, Dvp, Dkp, 32);
+        stage_block<NT_P, 8>(q.dV, LQ, rec + R.dV + j0, Dvp, C, 32);
+        stage_block<NT_P, 8>(q.V, LQ, rec + R.V + j0, Dvp, C, 32);
+        stage_cols(q.dO, gO, j0);
+        stage_cols(q.v, gv, j0);
+        cp_async_commit_group();
+    };
+    stage(0);
+    stage_rows<T, NT_P>(sK, (const T *)p.k + u.row0 * Dk, rk, len, Dk, Dkp, p.wide_k);
+    stage_rows<T, NT_P>(sQ, (const T *)p.q + u.row0 * Dk, rk, len, Dk, Dkp, p.wide_k);
+    stage_block<NT_P, 16>(sT, LC, rec + R.T, C, C, C);
     cp_async_commit_group();
     if (tid < C) {
         sG[tid] = reinterpret_cast<const double *>(rec + R.G)[tid];
@@ -644,117 +692,79 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
         seD[tid] = rec[R.eD + tid];
         sb[tid] = tid < len ? load_elem((const T *)p.beta, u.row0 + (int64_t)tid * p.H) : 0.f;
     }
-    cp_async_wait<0>();
-    __syncthreads();
 
     // every warp: 32 rows from r0; 16 columns from c0 of [64][D] results, 8 from c1 of [64][64] ones
     const int r0 = 32 * (warp & 1), c0 = 16 * (warp >> 1), c1 = 8 * (warp >> 1);
     const bool inK = c0 < Dkp, inV = c0 < Dvp, tri = c1 < r0 + 32;  // tri: the tile reaches below the diagonal
     float dq[2][2][4] = {}, dk[2][2][4] = {}, X[2][1][4] = {};
     float late[2][2] = {}, early[2][2] = {}, db[2][2] = {};  // row sums of this lane's rows 16 i + g + 8 half
-
-    // dQg = dO S^T (dq = e^G dQg) and dW = -dV' S^T
-    float2 at[2][2][2];  // this lane's pairs of q, then of k: on their way while the products run
-    auto fetch_pairs = [&](const T *rows) {
-        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
-            if (!(e & 1)) at[i][j][e >> 1] = row_pair(rows + (r0 + r) * rk, c0 + c, Dk, r0 + r < len, p.wide_k);
-        });
-    };
-    if (inK) {
-        fetch_pairs(gq);
-        tf32::tile<2, 2, false, false, EX, false>(dq, sO + r0 * LD, LD, bS + c0 * LD, LD, Dvp);
-        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
-            dq[i][j][e] *= seG[r0 + r];
-            late[i][e >> 1] = fmaf(dq[i][j][e], e & 1 ? at[i][j][e >> 1].y : at[i][j][e >> 1].x, late[i][e >> 1]);
-        });
-        float w[2][2][4] = {};
-        tf32::tile<2, 2, false, false, false, false>(w, bdV + r0 * LD, LD, bS + c0 * LD, LD, Dvp);
-        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) { bdW[(r0 + r) * LD + c0 + c] = -w[i][j][e]; });
-    }
-    {  // dM = dO V'^T (i <= r)
-        float m[2][1][4] = {};
+    float dot = 0.f;                                          // <dS_next, S>
+    {
+        float w[2][2][4] = {}, m[2][1][4] = {}, d[2][1][4] = {};
+        const int np = Dvp / 32;
+        for (int i = 0; i < np; ++i) {
+            if (i == 0) cp_async_wait<1>();  // the first piece; k, q and T may still be on their way
+            else cp_async_wait<0>();
+            __syncthreads();
+            if (Piece<T>::SETS == 2 && i + 1 < np) stage(i + 1);
+            const Piece<T> q(area, i);
+            if (inK) {
+                tf32::tile<2, 2, false, false, EX, false>(dq, q.dO + r0 * LQ, LQ, q.S + c0 * LQ, LQ, 32);
+                tf32::tile<2, 2, false, false, false, false>(w, q.dV + r0 * LQ, LQ, q.S + c0 * LQ, LQ, 32);
+                tf32::tile<2, 2, false, false, false, false>(dk, q.V + r0 * LQ, LQ, q.dS + c0 * LQ, LQ, 32);
+            }
+            if (tri) {
+                tf32::tile<2, 1, false, false, EX, false>(m, q.dO + r0 * LQ, LQ, q.V + c1 * LQ, LQ, 32);
+                tf32::tile<2, 1, false, false, false, EX>(d, q.dV + r0 * LQ, LQ, q.v + c1 * LQ, LQ, 32);
+            }
+            for (int r = tid >> 3, c = (tid & 7) * 4; r < Dkp; r += NT_P / 8) {
+                const float4 x = *reinterpret_cast<const float4 *>(q.S + r * LQ + c);
+                const float4 y = *reinterpret_cast<const float4 *>(q.dS + r * LQ + c);
+                dot = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot))));
+            }
+            if (Piece<T>::SETS == 1 && i + 1 < np) {
+                __syncthreads();
+                stage(i + 1);
+            }
+        }
+        cp_async_wait<0>();
+        __syncthreads();  // the pieces are read; k, q and T are there
+        stage_block<NT_P, 32>(sdV, LD, rec + R.dV, Dvp, C, Dvp);
+        cp_async_commit_group();
         float2 M[2][2];
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             if (!(e & 1)) M[i][e >> 1] = *reinterpret_cast<const float2 *>(rec + R.M + (r0 + r) * C + c1 + c);
         });
-        if (tri) tf32::tile<2, 1, false, false, EX, false>(m, sO + r0 * LD, LD, bV + c1 * LD, LD, Dvp);
+        if (inK)  // dq = e^G dQg, dk = e^D dKd, dW
+            tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
+                r += r0;
+                c += c0;
+                dq[i][j][e] *= seG[r];
+                dk[i][j][e] *= seD[r];
+                late[i][e >> 1] = fmaf(dq[i][j][e], load_elem(sQ, r * LD + c), late[i][e >> 1]);
+                early[i][e >> 1] = fmaf(dk[i][j][e], load_elem(sK, r * LD + c), early[i][e >> 1]);
+                if (e & 1) *reinterpret_cast<float2 *>(sdW + r * LD + c - 1) = make_float2(-w[i][j][e - 1], -w[i][j][e]);
+            });
+        tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {  // dM (i <= r)
+            r += r0;
+            c += c1;
+            const float x = c <= r ? m[i][j][e] : 0.f;
+            sM[r * LC + c] = c <= r ? x * expf((float)(sG[r] - sG[c])) : 0.f;
+            if (c < r) X[i][j][e] = x * (e & 1 ? M[i][e >> 1].y : M[i][e >> 1].x);
+        });
+        __syncthreads();
+        // dT = dV' Bv^T + dW Bk^T, on and below the diagonal (T has nothing above it)
+        float b[2][1][4] = {};
+        if (tri) tf32::tile<2, 1, false, false, false, EX>(b, sdW + r0 * LD, LD, sK + c1 * LD, LD, Dkp);
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             r += r0;
             c += c1;
-            const float d = c <= r ? m[i][j][e] : 0.f;
-            sM[r * LC + c] = c <= r ? d * expf((float)(sG[r] - sG[c])) : 0.f;
-            if (c < r) X[i][j][e] = d * (e & 1 ? M[i][e >> 1].y : M[i][e >> 1].x);
-        });
-    }
-    __syncthreads();
-    // dS_next over S, with <dS_next, S> on the way
-    float dot = 0.f;
-    {
-        const int c = (tid & 31) * 4;
-        for (int base = tid >> 5; c < Dvp && base < Dkp; base += 4 * (NT_P / 32)) {
-            float4 d[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = base + e * (NT_P / 32);
-                d[e] = r < Dkp ? *reinterpret_cast<const float4 *>(rec + R.dS + r * Dvp + c) : make_float4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = base + e * (NT_P / 32);
-                if (r < Dkp) {
-                    float4 *s = reinterpret_cast<float4 *>(bS + r * LD + c);
-                    const float4 o = *s;
-                    dot = fmaf(o.x, d[e].x, fmaf(o.y, d[e].y, fmaf(o.z, d[e].z, fmaf(o.w, d[e].w, dot))));
-                    *s = d[e];
-                }
-            }
-        }
-    }
-    __syncthreads();
-    if (inK) {  // dKd = V' dS_next^T (dk = e^D dKd)
-        fetch_pairs(gk);
-        tf32::tile<2, 2, false, false, false, false>(dk, bV + r0 * LD, LD, bS + c0 * LD, LD, Dvp);
-        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
-            dk[i][j][e] *= seD[r0 + r];
-            early[i][e >> 1] = fmaf(dk[i][j][e], e & 1 ? at[i][j][e >> 1].y : at[i][j][e >> 1].x, early[i][e >> 1]);
-        });
-    }
-    __syncthreads();
-    T *sV = reinterpret_cast<T *>(bS), *sK = sV + C * LD;
-    float *sT = bO, *sdT = bV;
-    stage_block<NT_P, 16>(sT, LC, rec + R.T, C, C, C);
-    stage_rows<T, NT_P>(sV, (const T *)p.v + u.row0 * Dv, rv, len, Dv, Dvp, p.wide_v);
-    stage_rows<T, NT_P>(sK, gk, rk, len, Dk, Dkp, p.wide_k);
-    cp_async_commit_group();
-    cp_async_wait<0>();
-    __syncthreads();
-    {  // dT = dV' Bv^T + dW Bk^T, on and below the diagonal (T has nothing above it)
-        float a[2][1][4] = {}, b[2][1][4] = {};
-        if (tri) {
-            tf32::tile<2, 1, false, false, false, EX>(a, bdV + r0 * LD, LD, sV + c1 * LD, LD, Dvp);
-            tf32::tile<2, 1, false, false, false, EX>(b, bdW + r0 * LD, LD, sK + c1 * LD, LD, Dkp);
-        }
-        tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
-            r += r0;
-            c += c1;
-            sdT[r * LC + c] = c <= r ? sb[c] * fmaf(seG[c], b[i][j][e], a[i][j][e]) : 0.f;
-        });
-    }
-    __syncthreads();
-    if (inV) {  // dBv = T^T dV'
-        float a[2][2][4] = {};
-        tf32::tile<2, 2, true, true, false, false>(a, sT + r0 + r0 * LC, LC, bdV + c0 + r0 * LD, LD, C - r0);
-        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
-            r += r0;
-            c += c0;
-            db[i][e >> 1] = fmaf(a[i][j][e], load_elem(sV, r * LD + c), db[i][e >> 1]);
-            store_pair(p.dv + (u.row0 + (int64_t)r * p.H) * Dv, c - (e & 1), Dv, r < len && (e & 1), p.pair_v,
-                       sb[r] * a[i][j][e & 2], sb[r] * a[i][j][e | 1]);
+            sdT[r * LC + c] = c <= r ? sb[c] * fmaf(seG[c], b[i][j][e], d[i][j][e]) : 0.f;
         });
     }
     if (inK) {  // dBk = T^T dW
         float a[2][2][4] = {};
-        tf32::tile<2, 2, true, true, false, false>(a, sT + r0 + r0 * LC, LC, bdW + c0 + r0 * LD, LD, C - r0);
+        tf32::tile<2, 2, true, true, false, false>(a, sT + r0 + r0 * LC, LC, sdW + c0 + r0 * LD, LD, C - r0);
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
             r += r0;
             const float x = a[i][j][e] * seG[r], xk = x * load_elem(sK, r * LD + c0 + c);
@@ -763,41 +773,56 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
             dk[i][j][e] = fmaf(sb[r], x, dk[i][j][e]);
         });
     }
-    float y[2][1][4] = {};  // T^T dT
-    tf32::tile<2, 1, true, true, false, false>(y, sT + r0 + r0 * LC, LC, sdT + c1 + r0 * LC, LC, C - r0);
+    cp_async_wait<0>();  // dV'
     __syncthreads();
-    tf32::each<2, 1>([&](int i, int j, int e, int r, int c) { bdV[(r0 + r) * LC + c1 + c] = y[i][j][e]; });
-    T *sQ = reinterpret_cast<T *>(bV);
-    stage_rows<T, NT_P>(sQ, gq, rk, len, Dk, Dkp, p.wide_k);
-    cp_async_commit_group();
+    if (inV) {  // dBv = T^T dV'
+        float2 vv[2][2][2];
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
+            if (!(e & 1)) vv[i][j][e >> 1] = row_pair(gv + (r0 + r) * rv, c0 + c, Dv, r0 + r < len, p.wide_v);
+        });
+        float a[2][2][4] = {};
+        tf32::tile<2, 2, true, true, false, false>(a, sT + r0 + r0 * LC, LC, sdV + c0 + r0 * LD, LD, C - r0);
+        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
+            r += r0;
+            c += c0;
+            db[i][e >> 1] = fmaf(a[i][j][e], e & 1 ? vv[i][j][e >> 1].y : vv[i][j][e >> 1].x, db[i][e >> 1]);
+            store_pair(p.dv + (u.row0 + (int64_t)r * p.H) * Dv, c - (e & 1), Dv, r < len && (e & 1), p.pair_v,
+                       sb[r] * a[i][j][e & 2], sb[r] * a[i][j][e | 1]);
+        });
+    }
+    {
+        float y[2][1][4] = {};  // T^T dT
+        tf32::tile<2, 1, true, true, false, false>(y, sT + r0 + r0 * LC, LC, sdT + c1 + r0 * LC, LC, C - r0);
+        tf32::each<2, 1>([&](int i, int j, int e, int r, int c) { sY[(r0 + r) * LC + c1 + c] = y[i][j][e]; });
+    }
+    float2 Pp[2][2];
+    tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
+        if (!(e & 1)) Pp[i][e >> 1] = *reinterpret_cast<const float2 *>(rec + R.P + (r0 + r) * C + c1 + c);
+    });
     __syncthreads();
+    float *sdP = sdW;  // [64][LC]; dW is read
     {  // dA = -(T^T dT) T^T (i < r);  dP' = beta dA E
         float a[2][1][4] = {};
-        float2 Pp[2][2];
-        tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
-            if (!(e & 1)) Pp[i][e >> 1] = *reinterpret_cast<const float2 *>(rec + R.P + (r0 + r) * C + c1 + c);
-        });
-        if (tri) tf32::tile<2, 1, false, false, false, false>(a, bdV + r0 * LC, LC, sT + c1 * LC, LC, c1 + 8);
+        if (tri) tf32::tile<2, 1, false, false, false, false>(a, sY + r0 * LC, LC, sT + c1 * LC, LC, c1 + 8);
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             r += r0;
             c += c1;
-            float d = 0.f;
+            float x = 0.f;
             if (c < r) {
                 const float P = e & 1 ? Pp[i][e >> 1].y : Pp[i][e >> 1].x;
                 db[i][e >> 1] = fmaf(-a[i][j][e], P, db[i][e >> 1]);
-                d = -a[i][j][e] * sb[r];
-                X[i][j][e] = fmaf(d, P, X[i][j][e]);
-                d *= expf((float)(sG[r] - sG[c]));
+                x = -a[i][j][e] * sb[r];
+                X[i][j][e] = fmaf(x, P, X[i][j][e]);
+                x *= expf((float)(sG[r] - sG[c]));
             }
-            bdW[r * LC + c] = d;
+            sdP[r * LC + c] = x;
         });
     }
-    cp_async_wait<0>();  // q
     __syncthreads();
     if (inK) {
         tf32::tile<2, 2, false, true, false, EX>(dq, sM + r0 * LC, LC, sK + c0, LD, r0 + 32);
-        tf32::tile<2, 2, false, true, false, EX>(dk, bdW + r0 * LC, LC, sK + c0, LD, r0 + 32);
-        tf32::tile<2, 2, true, true, false, EX>(dk, bdW + r0 + r0 * LC, LC, sK + c0 + r0 * LD, LD, C - r0);
+        tf32::tile<2, 2, false, true, false, EX>(dk, sdP + r0 * LC, LC, sK + c0, LD, r0 + 32);
+        tf32::tile<2, 2, true, true, false, EX>(dk, sdP + r0 + r0 * LC, LC, sK + c0 + r0 * LD, LD, C - r0);
         tf32::tile<2, 2, true, true, false, EX>(dk, sM + r0 + r0 * LC, LC, sQ + c0 + r0 * LD, LD, C - r0);
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
             r += r0;
@@ -807,8 +832,8 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
             store_pair(p.dk + row, c - (e & 1), Dk, r < len && (e & 1), p.pair_k, dk[i][j][e & 2], dk[i][j][e | 1]);
         });
     }
-    // the sums over rows and pairs.  T^T dT is read: the pair sums go there; T is read: the row sums go there
-    float *sX = bdV, *part = bO;  // part: [late, early, db][8 column groups][64]
+    // the sums over rows and pairs, in the places of T^T dT and dV', which are read
+    float *sX = sY, *part = sdV;  // part: [late, early, db][8 column groups][64]
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -885,7 +910,7 @@ kda_status_t gb_launch(GbArgs p, int64_t nbh, cudaStream_t st) {
     cudaFuncSetAttribute(gb_prep_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep_smem<T>());
     const auto chain = pad16(p.Dk) == 128 ? gb_chain_kernel<T, true> : gb_chain_kernel<T, false>;
     cudaFuncSetAttribute(chain, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain_smem<T>());
-    cudaFuncSetAttribute(gb_grad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GRAD_SMEM);
+    cudaFuncSetAttribute(gb_grad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad_smem<T>());
     p.wide_k = p.Dk * (int)sizeof(T) % 16 == 0 && aligned_to(p.q, 16) && aligned_to(p.k, 16);
     p.wide_v = p.Dv * (int)sizeof(T) % 16 == 0 && aligned_to(p.v, 16) && aligned_to(p.dO, 16);
     p.pair_k = p.Dk % 2 == 0 && aligned_to(p.dq, 8) && aligned_to(p.dk, 8);
@@ -894,7 +919,7 @@ kda_status_t gb_launch(GbArgs p, int64_t nbh, cudaStream_t st) {
     KDA_TRY(check_launch("gb_prep_kernel"));
     chain<<<(unsigned)jobs, NT_C, chain_smem<T>(), st>>>(p);
     KDA_TRY(check_launch("gb_chain_kernel"));
-    gb_grad_kernel<T><<<(unsigned)units, NT_P, GRAD_SMEM, st>>>(p);
+    gb_grad_kernel<T><<<(unsigned)units, NT_P, grad_smem<T>(), st>>>(p);
     return check_launch("gb_grad_kernel");
 }
 
