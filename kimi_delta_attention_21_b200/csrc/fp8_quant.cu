@@ -124,7 +124,8 @@ template <> struct Q8Vec<__nv_bfloat16> {
 // lanes per block, 16 bytes of o and of the gate per lane; `hl` lanes share a head's norm.  Four blocks per group
 // are in flight together.  2 * es + 1 bytes per channel pass HBM; about 30 instructions per channel would take the
 // SMs as long, which is why the sigmoid is the fast one and the division by the scale a product with its inverse.
-template <typename T>
+// FLAT: K is a multiple of 128, so that the blocks follow one another without gaps (no division per block).
+template <typename T, bool FLAT>
 __global__ void __launch_bounds__(256) norm_gate_fp8_vec_kernel(const T *__restrict__ o, const T *__restrict__ gate,
                                                                 int64_t N, int K, int nb, int hl, float inv_dv,
                                                                 float eps, uint8_t *__restrict__ out,
@@ -139,10 +140,16 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_vec_kernel(const T *__restr
     bool in[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t unit = u0 + u * PER, tok = unit / nb;
-        const int c = (int)(unit - tok * nb) * 128 + lane * VEC;
-        in[u] = unit < units && c < K;
-        at[u] = tok * K + c;
+        const int64_t unit = u0 + u * PER;
+        if (FLAT) {
+            in[u] = unit < units;
+            at[u] = unit * 128 + lane * VEC;
+        } else {
+            const int64_t tok = unit / nb;
+            const int c = (int)(unit - tok * nb) * 128 + lane * VEC;
+            in[u] = unit < units && c < K;
+            at[u] = tok * K + c;
+        }
         ov[u] = in[u] ? __ldcs(reinterpret_cast<const uint4 *>(o + at[u])) : make_uint4(0, 0, 0, 0);
         gv[u] = in[u] ? __ldcs(reinterpret_cast<const uint4 *>(gate + at[u])) : make_uint4(0, 0, 0, 0);
     }
@@ -221,7 +228,7 @@ cudaError_t ng8_launch(const void *o, const void *gl, int64_t N, int H, int Dv, 
     if (Dv >= VEC && Dv <= 128 && (Dv & (Dv - 1)) == 0 && aligned_to(o, 16) && aligned_to(gl, 16) && aligned_to(x8, VEC)) {
         const int64_t ctas = (N * nb + 8 * VEC - 1) / (8 * VEC);  // 256 threads: 2 VEC groups of four blocks
         if (ctas <= 0x7fffffffLL)
-            return launch_pdl(norm_gate_fp8_vec_kernel<T>, dim3((unsigned)ctas), dim3(256), 0, st, (const T *)o,
+            return launch_pdl(K % 128 ? norm_gate_fp8_vec_kernel<T, false> : norm_gate_fp8_vec_kernel<T, true>, dim3((unsigned)ctas), dim3(256), 0, st, (const T *)o,
                               (const T *)gl, N, K, nb, Dv / VEC, 1.0f / (float)Dv, eps, (uint8_t *)x8, scales);
     }
     return launch_pdl(norm_gate_fp8_kernel<T>, dim3((unsigned)N), dim3(256), (size_t)H * 4, st, (const T *)o,
