@@ -111,14 +111,16 @@ __device__ __forceinline__ Unit unit_of(const GbArgs &p, int64_t bh, int n) {
     return u;
 }
 
-// Token rows (rs elements apart), in their type, into [64][LD]: zero past `len` rows and D columns up to Dp.  wide: D is
+// Staging by NT threads, tid of them.  Token rows (rs elements apart), in their type, into [64][LD]: zero past `len`
+// rows and D columns up to Dp.  wide: D is
 // a multiple of a 16-byte vector and every row starts on 16 bytes; the copies are asynchronous then.
 template <typename T, int NT>
-__device__ __forceinline__ void stage_rows(T *dst, const T *src, int64_t rs, int len, int D, int Dp, bool wide) {
+__device__ __forceinline__ void stage_rows(T *dst, const T *src, int64_t rs, int len, int D, int Dp, bool wide,
+                                           int tid = threadIdx.x) {
     if (wide) {
         constexpr int E = 16 / (int)sizeof(T), VPR = 128 / E;
 #pragma unroll
-        for (int i = threadIdx.x; i < C * VPR; i += NT) {
+        for (int i = tid; i < C * VPR; i += NT) {
             const int r = i / VPR, c = i % VPR * E;
             const bool in = r < len && c < D;
             if (c < Dp)
@@ -127,18 +129,19 @@ __device__ __forceinline__ void stage_rows(T *dst, const T *src, int64_t rs, int
         }
         return;
     }
-    const int c = threadIdx.x & 127;
+    const int c = tid & 127;
     if (c < Dp)
 #pragma unroll 4
-        for (int r = threadIdx.x >> 7; r < C; r += NT / 128)
+        for (int r = tid >> 7; r < C; r += NT / 128)
             dst[r * LD + c] = (r < len && c < D) ? src[r * rs + c] : T(0.f);
 }
 
 // A record block of `rows` rows of `cols` floats (a multiple of 4, at most 4 VPR; pitch `pitch`) into shared memory.
 template <int NT, int VPR>
-__device__ __forceinline__ void stage_block(float *dst, int ld, const float *src, int pitch, int rows, int cols) {
+__device__ __forceinline__ void stage_block(float *dst, int ld, const float *src, int pitch, int rows, int cols,
+                                            int tid = threadIdx.x) {
 #pragma unroll 4
-    for (int i = threadIdx.x; i < rows * VPR; i += NT) {
+    for (int i = tid; i < rows * VPR; i += NT) {
         const int r = i / VPR, c = i % VPR * 4;
         if (c < cols) cp_async16_fill(dst + r * ld + c, src + (int64_t)r * pitch + c);
     }
@@ -430,8 +433,8 @@ __device__ __forceinline__ Chain chain_of(const GbArgs &p, int64_t bh, int j0) {
 template <typename T>
 __device__ __forceinline__ void stage_keys(const GbArgs &p, const Chain &c, T *sK, int n) {
     const int64_t t0 = (int64_t)n * C;
-    stage_rows<T, NT_C>(sK, (const T *)p.k + (c.row0 + t0 * p.H) * p.Dk, c.rk, (int)min((int64_t)C, p.S - t0), p.Dk, c.Dkp,
-                        p.wide_k);
+    stage_rows<T, NT_C / 2>(sK, (const T *)p.k + (c.row0 + t0 * p.H) * p.Dk, c.rk, (int)min((int64_t)C, p.S - t0), p.Dk, c.Dkp,
+                            p.wide_k, threadIdx.x & (NT_C / 2 - 1));
 }
 
 // Two neighbouring values, split, as one 16-byte store (an even column).
@@ -451,11 +454,12 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
     const Rec &R = q.R;
     const int m0 = q.m0, n0 = q.n0, r0 = q.r0, c0 = q.c0, Dkp = FULL ? 128 : q.Dkp, Dvp = q.Dvp;
     const bool own = FULL || m0 < Dkp, first = !q.half;
-    auto stage = [&](const float *rec, int n) {
+    const int ht = threadIdx.x & (NT_C / 2 - 1);
+    auto stage = [&](const float *rec, int n) {  // by the second group of warps
         const Stage<T> g(sm, n & 1);
-        stage_block<NT_C, 32>(g.e, 2 * C, rec + R.eG, 2 * C, 1, 2 * C);
-        stage_block<NT_C, 32>(g.W, LD, rec + R.W, Dkp, C, Dkp);
-        stage_block<NT_C, 8>(g.U, LO, rec + R.V + j0, Dvp, C, VS);
+        stage_block<NT_C / 2, 32>(g.e, 2 * C, rec + R.eG, 2 * C, 1, 2 * C, ht);
+        stage_block<NT_C / 2, 32>(g.W, LD, rec + R.W, Dkp, C, Dkp, ht);
+        stage_block<NT_C / 2, 8>(g.U, LO, rec + R.V + j0, Dvp, C, VS, ht);
         if (EX) stage_keys<T>(p, q, g.K, n);
         cp_async_commit_group();
     };
@@ -467,13 +471,12 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
         if (own) sS[r * LS + c] = tf32::split2(S[i][j][e]);
     });
     float *rec = const_cast<float *>(q.rec0);
-    stage(rec, 0);
+    if (!first) stage(rec, 0);
     for (int n = 0; n < p.Nc; ++n, rec += R.size) {
         const Stage<T> g(sm, n & 1);
         cp_async_wait<0>();  // this chunk's set
         __syncthreads();
-        if (n + 1 < p.Nc) stage(rec + R.size, n + 1);
-        if (!EX) {
+        if (!EX && !first) {
             stage_keys<T>(p, q, g.K, n);
             cp_async_commit_group();
         }
@@ -500,6 +503,8 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
                     *reinterpret_cast<float2 *>(rec + R.V + r * Dvp + j0 + c - 1) = make_float2(v[i][j][e - 1], v[i][j][e]);
                 }
             });
+        else if (n + 1 < p.Nc)  // (the set was last read two steps ago)
+            stage(rec + R.size, n + 1);
         __syncthreads();
         if (own) {
             const float gamma = g.e[C - 1];
@@ -525,12 +530,13 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
     const Rec &R = q.R;
     const int m0 = q.m0, n0 = q.n0, r0 = q.r0, c0 = q.c0, Dkp = FULL ? 128 : q.Dkp, Dvp = q.Dvp;
     const bool own = FULL || m0 < Dkp, first = !q.half;
-    auto stage = [&](const float *rec, int n) {
+    const int ht = threadIdx.x & (NT_C / 2 - 1);
+    auto stage = [&](const float *rec, int n) {  // by the second group of warps
         const Stage<T> g(sm, n & 1);
-        stage_block<NT_C, 32>(g.e, 2 * C, rec + R.eG, 2 * C, 1, 2 * C);
-        stage_block<NT_C, 32>(g.W, LD, rec + R.W, Dkp, C, Dkp);
-        stage_block<NT_C, 8>(g.U, LO, rec + R.dV + j0, Dvp, C, VS);
-        stage_block<NT_C, 8>(g.H, LO, rec + R.dS + j0, Dvp, Dkp, VS);
+        stage_block<NT_C / 2, 32>(g.e, 2 * C, rec + R.eG, 2 * C, 1, 2 * C, ht);
+        stage_block<NT_C / 2, 32>(g.W, LD, rec + R.W, Dkp, C, Dkp, ht);
+        stage_block<NT_C / 2, 8>(g.U, LO, rec + R.dV + j0, Dvp, C, VS, ht);
+        stage_block<NT_C / 2, 8>(g.H, LO, rec + R.dS + j0, Dvp, Dkp, VS, ht);
         if (EX) stage_keys<T>(p, q, g.K, n);
         cp_async_commit_group();
     };
@@ -542,13 +548,14 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
         if (own) sS[r * LS + c] = tf32::split2(dS[i][j][e]);
     });
     float *rec = const_cast<float *>(q.rec0) + (int64_t)(p.Nc - 1) * R.size;
-    if (!EX) stage_keys<T>(p, q, Stage<T>(sm, 0).K, p.Nc - 1);
-    stage(rec, p.Nc - 1);
+    if (!first) {
+        if (!EX) stage_keys<T>(p, q, Stage<T>(sm, 0).K, p.Nc - 1);
+        stage(rec, p.Nc - 1);
+    }
     for (int n = p.Nc - 1; n >= 0; --n, rec -= R.size) {
         const Stage<T> g(sm, n & 1);
         cp_async_wait<0>();  // this chunk's set
         __syncthreads();
-        if (n > 0) stage(rec - R.size, n - 1);
         if (own)  // the gradient of the state leaving the chunk
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 if (!(e & 1))
@@ -561,10 +568,6 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
         if (!first)
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { sY[(r0 + r) * LO + c0 + c] = x[i][j][e]; });
         __syncthreads();  // the other half of the sum; K is read
-        if (!EX && n > 0) {
-            stage_keys<T>(p, q, g.K, n - 1);
-            cp_async_commit_group();
-        }
         if (first)
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 r += r0;
@@ -575,6 +578,10 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
                     *reinterpret_cast<float2 *>(rec + R.dV + r * Dvp + j0 + c - 1) = make_float2(x[i][j][e - 1], x[i][j][e]);
                 }
             });
+        else if (n > 0) {  // (the set was last read two steps ago, a single K just now)
+            if (!EX) stage_keys<T>(p, q, g.K, n - 1);
+            stage(rec - R.size, n - 1);
+        }
         __syncthreads();
         if (own) {
             const float gamma = g.e[C - 1];

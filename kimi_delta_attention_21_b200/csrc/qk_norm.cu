@@ -513,7 +513,7 @@ unsigned qn_grid(const QnArgs &p, int per_cta, int64_t cap) {
     return (unsigned)(n < cap ? n : cap);
 }
 
-constexpr int QN_BWD_CTAS_PER_SM = 4;  // per side: the weight gradients' partial sums are one row per CTA
+constexpr int QN_BWD_CTAS_PER_SM = 2;  // per side: both sides resident at once (4 per side: 209 us against 205 us)
 
 template <typename T, typename GT, int G, int NV>
 cudaError_t qn_launch_rot(const QnArgs &p, int rot, bool bwd, dim3 grid, cudaStream_t st) {

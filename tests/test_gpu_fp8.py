@@ -122,7 +122,8 @@ def tolerance(want, size, Kd, dtype):
 
 
 SIZES = [(1, 128, 64), (1, 16, 8), (5, 128, 256), (64, 4096, 4096), (130, 272, 136), (200, 1040, 1000), (257, 384, 520),
-         (300, 2048, 2048), (33, 4096, 264), (1000, 640, 4096), (2500, 512, 4104), (128, 8192, 128)]
+         (300, 2048, 2048), (33, 4096, 264), (1000, 640, 4096), (2500, 512, 4104), (128, 8192, 128), (20, 4240, 512),
+         (1, 2048, 4096), (20, 1168, 520), (1500, 1040, 2000)]
 
 
 @pytest.mark.parametrize("out", [BF16, F32])
