@@ -577,8 +577,8 @@ kda_status_t kda_norm_gate_fp8(const void *o, const void *gate_logits, int64_t N
  *   W8 (D_model, K) e4m3, W_scale (ceil(D_model / 128), ceil(K / 128)) fp32
  *   y (N, D_model) out_dtype
  * Blocks of the sum are exact products accumulated in fp32, and are scaled and
- * added in fp32.  K % 16 == 0, 16-byte rows of y and 16-byte aligned pointers
- * run on the tcgen05 tensor cores; anything else on an exact-fp32 SIMT kernel.
+ * added in fp32.  K % 16 == 0 with 16-byte aligned x8 and W8 runs on the tcgen05
+ * tensor cores (any N and D_model); anything else on an exact-fp32 SIMT kernel.
  */
 kda_status_t kda_out_proj_fp8(const void *x8, const float *x_scale, const void *W8, const float *W_scale, int64_t N,
                               int32_t K, int32_t D_model, void *y, kda_dtype_t out_dtype, void *stream);

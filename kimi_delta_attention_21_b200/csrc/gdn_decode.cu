@@ -32,9 +32,9 @@ struct GdArgs {
     unsigned int *bounds;
 };
 
-// FULL: D_k = D_v = 128 with a 16-byte aligned state; lane l owns columns 4l .. 4l + 3.  Otherwise the
-// columns l, l + 32, l + 64, l + 96 within D_v and the rows within D_k.
-template <typename T, bool FULL>
+// VEC: D_v is a multiple of 4 and the state 16-byte aligned; lane l owns columns 4l .. 4l + 3.  Otherwise the columns
+// l, l + 32, l + 64, l + 96.  FULL: D_k = D_v = 128 besides, nothing to mask.
+template <typename T, bool VEC, bool FULL>
 __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constant__ GdArgs p) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
@@ -51,13 +51,14 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
         return;
     }
     float *S = p.state + (slot * p.H + h) * (int64_t)Dk * Dv;
-    auto col = [&](int j) { return FULL ? 4 * l + j : l + 32 * j; };
+    auto col = [&](int j) { return VEC ? 4 * l + j : l + 32 * j; };
     float s[GD_RPW][4];
 #pragma unroll
     for (int i = 0; i < GD_RPW; ++i) {
         const int c = w + GD_NW * i;
-        if (FULL) {
-            const float4 t = __ldcs(reinterpret_cast<const float4 *>(S + c * GD_MAXD + 4 * l));
+        if (VEC) {
+            const float4 t = FULL || (c < Dk && 4 * l < Dv) ? __ldcs(reinterpret_cast<const float4 *>(S + c * Dv + 4 * l))
+                                                            : make_float4(0.f, 0.f, 0.f, 0.f);
             s[i][0] = t.x; s[i][1] = t.y; s[i][2] = t.z; s[i][3] = t.w;
         } else {
 #pragma unroll
@@ -154,8 +155,9 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < GD_RPW; ++i) {
         const int c = w + GD_NW * i;
-        if (FULL) {
-            __stcs(reinterpret_cast<float4 *>(S + c * GD_MAXD + 4 * l), make_float4(s[i][0], s[i][1], s[i][2], s[i][3]));
+        if (VEC) {
+            if (FULL || (c < Dk && 4 * l < Dv))
+                __stcs(reinterpret_cast<float4 *>(S + c * Dv + 4 * l), make_float4(s[i][0], s[i][1], s[i][2], s[i][3]));
         } else if (c < Dk) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -167,9 +169,11 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
 template <typename T>
 cudaError_t gd_launch(const kda_gdn_decode_args &a, const GdArgs &p, cudaStream_t st) {
     const dim3 grid((unsigned)(a.B * a.H));
-    if (a.D_k == GD_MAXD && a.D_v == GD_MAXD && aligned_to(a.state, 16))
-        return launch_pdl(gdn_decode_kernel<T, true>, grid, dim3(256), 0, st, p);
-    return launch_pdl(gdn_decode_kernel<T, false>, grid, dim3(256), 0, st, p);
+    const bool vec = a.D_v % 4 == 0 && aligned_to(a.state, 16);
+    if (vec && a.D_k == GD_MAXD && a.D_v == GD_MAXD)
+        return launch_pdl(gdn_decode_kernel<T, true, true>, grid, dim3(256), 0, st, p);
+    if (vec) return launch_pdl(gdn_decode_kernel<T, true, false>, grid, dim3(256), 0, st, p);
+    return launch_pdl(gdn_decode_kernel<T, false, false>, grid, dim3(256), 0, st, p);
 }
 
 }  // namespace

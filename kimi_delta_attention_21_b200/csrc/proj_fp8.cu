@@ -145,7 +145,7 @@ template <typename OT>
 __global__ void __launch_bounds__(PF_NT, 1)
 proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmY, const float *__restrict__ xs, const float *__restrict__ ws,
-                int M, int N, int K, unsigned int *timeouts) {
+                int M, int N, int K, OT *__restrict__ y, int tma_y, unsigned int *timeouts) {
     pdl_trigger();
     pdl_wait();
     constexpr int ST = Tile::STAGES, NB = Tile::BUFS, BN = Tile::BN, HC = BN / 2;  // HC: columns per epilogue warp
@@ -279,11 +279,25 @@ proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     *reinterpret_cast<uint4 *>(out + lane * 128 + ((g ^ (lane & 7)) << 4)) =
                         make_uint4(pv[0], pv[1], pv[2], pv[3]);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0 && m0 + 32 * q < M && c0 + c < N) {
-                    tma_store_2d(&tmY, out, c0 + c, m0 + 32 * q);
-                    bulk_commit();
+                if (tma_y) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && m0 + 32 * q < M && c0 + c < N) {
+                        tma_store_2d(&tmY, out, c0 + c, m0 + 32 * q);
+                        bulk_commit();
+                    }
+                } else {  // rows of y that do not start on 16 bytes: row by row, neighbouring lanes neighbouring columns
+                    __syncwarp();
+                    const OT *buf = reinterpret_cast<const OT *>(out);
+                    for (int r = 0; r < 32 && m0 + 32 * q + r < M; ++r) {
+                        OT *dst = y + (int64_t)(m0 + 32 * q + r) * N + c0 + c;
+#pragma unroll
+                        for (int i = 0; i < PER; i += 32) {
+                            const int j = lane + i;
+                            if (c0 + c + j < N) dst[j] = buf[r * PER + (((j / E) ^ (r & 7)) * E + j % E)];
+                        }
+                    }
+                    __syncwarp();
                 }
             }
         }
@@ -311,7 +325,7 @@ template <typename OT>
 __global__ void __launch_bounds__(PF_NT, 1)
 proj_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const float *__restrict__ xs, const float *__restrict__ ws, int M, int N, int K, int parts,
-                      OT *__restrict__ y, unsigned int *timeouts) {
+                      OT *__restrict__ y, int vec_y, unsigned int *timeouts) {
     pdl_trigger();
     pdl_wait();
     constexpr int ST = Split::STAGES, NB = Split::BUFS, BN = Split::BN, HC = BN / 2, LY = Split::LY;
@@ -419,7 +433,12 @@ proj_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             t.w += v.w;
         }
         OT *dst = y + (int64_t)(m0 + r) * N + col;
-        if (col + 4 <= N) {  // (N is a multiple of 4, the rows are aligned)
+        if (!vec_y || col + 4 > N) {
+            const float f[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (col + i < N) store_elem(dst, i, f[i]);
+        } else {
             if (sizeof(OT) == 4) {
                 *reinterpret_cast<float4 *>(dst) = t;
             } else {
@@ -525,9 +544,8 @@ kda_status_t map_bytes(CUtensorMap *m, const void *base, int64_t rows, int K, ui
 
 template <typename OT>
 kda_status_t launch_proj_fp8(const P8Args &a, cudaStream_t st) {
-    // whole 16-byte vectors in the rows of x, W and y, and aligned bases: what the TMA maps ask for
-    const bool tc = a.K % 16 == 0 && a.M % (16 / (int)sizeof(OT)) == 0 && aligned_to(a.x, 16) && aligned_to(a.w, 16) &&
-                    aligned_to(a.y, 16);
+    // whole 16-byte vectors in the rows of x and W, and aligned bases: what the TMA maps ask for
+    const bool tc = a.K % 16 == 0 && aligned_to(a.x, 16) && aligned_to(a.w, 16);
     if (!tc) {
         const int64_t ctas = ((a.N + 63) / 64) * ((a.M + 63) / 64);
         const cudaError_t e = launch_pdl(proj_fp8_simt_kernel<OT>, dim3((unsigned)ctas), dim3(256), 0, st,
@@ -549,18 +567,22 @@ kda_status_t launch_proj_fp8(const P8Args &a, cudaStream_t st) {
         while (parts < 8 && tiles * parts * 2 <= sms && KB >= 8 * parts) parts *= 2;
         const cudaError_t e = launch_cluster(proj_fp8_split_kernel<OT>, (unsigned)(tiles * parts), (unsigned)parts, Split::SMEM,
                                              st, ta, tb, a.xs, a.ws, (int)a.N, a.M, a.K, parts, (OT *)a.y,
-                                             device_timeout_counter());
+                                             (int)(a.M % 4 == 0 && aligned_to(a.y, 4 * sizeof(OT))), device_timeout_counter());
         if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "proj_fp8_split_kernel: %s", cudaGetErrorString(e));
         return check_launch("proj_fp8_split_kernel");
     }
     KDA_TRY(map_bytes(&tb, a.w, a.M, a.K, Tile::BN));
-    KDA_TRY(make_tmap_2d(&ty, a.y, sizeof(OT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                         (int)sizeof(OT), (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.M, 32, 128 / sizeof(OT),
-                         CU_TENSOR_MAP_SWIZZLE_128B));
+    const int tma_y = a.M % (16 / (int)sizeof(OT)) == 0 && aligned_to(a.y, 16);
+    if (tma_y)
+        KDA_TRY(make_tmap_2d(&ty, a.y, sizeof(OT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                             (int)sizeof(OT), (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.M, 32, 128 / sizeof(OT),
+                             CU_TENSOR_MAP_SWIZZLE_128B));
+    else
+        ty = ta;  // (not read)
     const int64_t big = ((a.N + PM - 1) / PM) * ((a.M + Tile::BN - 1) / Tile::BN);
     cudaFuncSetAttribute(proj_fp8_kernel<OT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tile::SMEM);
     const cudaError_t e = launch_pdl(proj_fp8_kernel<OT>, dim3((unsigned)(big < sms ? big : sms)), dim3(PF_NT), Tile::SMEM, st,
-                                     ta, tb, ty, a.xs, a.ws, (int)a.N, a.M, a.K, device_timeout_counter());
+                                     ta, tb, ty, a.xs, a.ws, (int)a.N, a.M, a.K, (OT *)a.y, tma_y, device_timeout_counter());
     if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "proj_fp8_kernel: %s", cudaGetErrorString(e));
     return check_launch("proj_fp8_kernel");
 }

@@ -70,7 +70,7 @@ def test_blocks_of_zeros_and_non_finite(K):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("N,H,Dv", [(1, 1, 128), (7, 5, 128), (256, 32, 128), (33, 3, 64), (5, 7, 48), (9, 3, 100), (2, 2, 300),
-                                    (4, 1, 1), (3, 131, 16)])
+                                    (4, 1, 1), (3, 131, 16), (6, 48, 96), (3, 200, 48), (2, 85, 104)])
 def test_norm_gate_quantises_its_result(K, N, H, Dv, dtype):
     g = gen(N * H + Dv)
     o, gate = randn(g, N, H, Dv, dtype=dtype, std=0.3), randn(g, N, H, Dv, dtype=dtype, std=2.0)
@@ -141,14 +141,26 @@ def test_product_on_the_tensor_cores(K, N, Kd, M, out):
 
 
 @pytest.mark.parametrize("out", [BF16, F32])
-@pytest.mark.parametrize("N,Kd,M", [(1, 1, 1), (3, 130, 5), (65, 200, 67), (70, 136, 129), (30, 1000, 300)])
-def test_product_of_odd_sizes(K, N, Kd, M, out):
+@pytest.mark.parametrize("N,Kd,M", [(1, 1, 1), (3, 130, 5), (65, 200, 67), (70, 136, 129), (30, 1000, 300)])  # K % 16
+def test_product_on_the_simt_kernel(K, N, Kd, M, out):
     x, xs, w, ws = operands(N, Kd, M, seed=N + M)
-    gy = Guarded((N, M), out, offset=1)          # rows that start off 16 bytes
+    gy = Guarded((N, M), out, offset=1)
     K.out_proj_fp8(x, xs, w, ws, out_dtype=out, out=gy.t)
     gy.check("y")
     want, size = product64(x, xs, w, ws)
     assert_within(gy.t, want, tolerance(want, size, Kd, out), "y")
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("N,Kd,M", [(1, 128, 1), (5, 272, 67), (300, 1040, 129), (2600, 512, 2049), (2600, 256, 2047)])
+def test_product_with_rows_off_sixteen_bytes(K, N, Kd, M, out):
+    x, xs, w, ws = operands(N, Kd, M, seed=N + M)
+    for offset in (0, 1):
+        gy = Guarded((N, M), out, offset=offset)
+        K.out_proj_fp8(x, xs, w, ws, out_dtype=out, out=gy.t)
+        gy.check("y")
+        want, size = product64(x, xs, w, ws)
+        assert_within(gy.t, want, tolerance(want, size, Kd, out), "y")
 
 
 def test_non_finite_rows_stay_in_their_row_and_column(K):
