@@ -40,20 +40,23 @@ def _start(t, name):
     return t.get_device(), code
 
 
-def _need(t, name, index, dtype, shape, contiguous=True):
-    """The address of a tensor of the call (0 for None), which must be as described."""
+def _need(t, name, index, dtype, shape):
+    """The address of a tensor of the call (0 for None), which must be as described.  (The calls of single tokens make the
+    same test in place, and come here when it fails.)"""
     if t is None:
         return 0
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index and
-            (not contiguous or t.is_contiguous())):
-        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or t.get_device() != index:
         raise ValueError(f"{name} must be a tensor on cuda:{index}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    raise ValueError(f"{name} must be contiguous")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+_entry = {}  # the library's functions by name, as they are first called
 
 
 def _addr(t):
@@ -62,7 +65,9 @@ def _addr(t):
 
 def _call(name, index, *args):
     """Calls an entry point with device `index` current, and raises on a status other than KDA_OK."""
-    fn = getattr(_lib.load(), name)
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(_lib.load(), name)
     if _current_device() == index:
         st = fn(*args)
     else:
@@ -115,16 +120,21 @@ def _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleav
         if positions is None:
             raise ValueError("positions and inv_freq go together")
         n = inv_freq.numel()
-        pos = _need(positions, "positions", ix, torch.int64, (B, S) if q.dim() == 4 else (S,))
-        inv = _need(inv_freq, "inv_freq", ix, _F32, (n,))
-        rot = 2 * n
+        if (positions.dtype is not torch.int64 or positions.shape != q.shape[:-2] or positions.get_device() != ix or
+                not positions.is_contiguous()):
+            _need(positions, "positions", ix, torch.int64, q.shape[:-2])
+        pos, inv, rot = positions.data_ptr(), _need(inv_freq, "inv_freq", ix, _F32, (n,)), 2 * n
     elif positions is not None:
         raise ValueError("positions and inv_freq go together")
     kind = NORMS.get(norm)
     if kind is None:
         raise ValueError(f"norm must be one of {sorted(NORMS)} (got {norm!r})")
-    return ix, (B, S, Hq, Hk, D, code, q.data_ptr(), k.data_ptr(), qb, qs, kb, ks, kind, eps,
-                _need(q_weight, "q_weight", ix, _F32, (D,)), _need(k_weight, "k_weight", ix, _F32, (D,)), pos, inv, rot,
+    qw = kw = 0
+    if q_weight is not None:
+        qw = _need(q_weight, "q_weight", ix, _F32, (D,))
+    if k_weight is not None:
+        kw = _need(k_weight, "k_weight", ix, _F32, (D,))
+    return ix, (B, S, Hq, Hk, D, code, q.data_ptr(), k.data_ptr(), qb, qs, kb, ks, kind, eps, qw, kw, pos, inv, rot,
                 1 if interleaved else 0)
 
 
@@ -198,23 +208,36 @@ def gdn_decode_step(q, k, v, beta, state, *, z=None, log_decay=None, g_min=-5.0,
         raise ValueError("q must be contiguous")
     Dv = v.shape[-1]
     val = (*tok, Dv)
-    if beta.dim() == len(tok) + 1 and beta.shape[-1] == 1:
-        beta = beta.view(tok)
-    if not isinstance(state, torch.Tensor) or state.dim() != 4:
-        raise ValueError("state must have shape (num_slots, H, D_k, D_v)")
-    pv = _need(v, "v", ix, dt, val)
+    if k.dtype is not dt or k.shape != shape or k.get_device() != ix or not k.is_contiguous():
+        _need(k, "k", ix, dt, shape)
+    if v.dtype is not dt or v.shape != val or v.get_device() != ix or not v.is_contiguous():
+        _need(v, "v", ix, dt, val)
+    if beta.dtype is not dt or beta.shape != tok or beta.get_device() != ix or not beta.is_contiguous():
+        if beta.dim() == len(tok) + 1 and beta.shape[-1] == 1:
+            beta = beta.view(tok)
+        _need(beta, "beta", ix, dt, tok)
+    n = state.shape[0]
+    if (state.dtype is not _F32 or state.shape != (n, H, Dk, Dv) or state.get_device() != ix or
+            not state.is_contiguous()):
+        _need(state, "state", ix, _F32, (n, H, Dk, Dv))
+    pz = pl = ps = pg = pd = 0
+    if z is not None:
+        pz = _need(z, "z", ix, dt, tok)
+    if log_decay is not None:
+        pl = _need(log_decay, "log_decay", ix, _F32, tok)
+    if slots is not None:
+        ps = _need(slots, "slots", ix, torch.int32, (B,))
+    if gate_logits is not None:
+        pg = _need(gate_logits, "gate_logits", ix, dt, val)
+    if dev_status is not None:
+        pd = _need(dev_status, "dev_status", ix, torch.int32, dev_status.shape)
     if out is None:
         out = _empty_like(v)
-        po = out.data_ptr()
     else:
-        po = _need(out, "out", ix, dt, val)
-    n = state.shape[0]
+        _need(out, "out", ix, dt, val)
     _call("kda_gdn_decode_step", ix, _pack_gdn_decode(
-        B, n, T, H, Dk, Dv, code, q.data_ptr(), _need(k, "k", ix, dt, shape), pv, _need(z, "z", ix, dt, tok),
-        _need(log_decay, "log_decay", ix, _F32, tok), g_min, _need(beta, "beta", ix, dt, tok),
-        _need(state, "state", ix, _F32, (n, H, Dk, Dv)), _need(slots, "slots", ix, torch.int32, (B,)),
-        _need(gate_logits, "gate_logits", ix, dt, val), eps, po,
-        0 if dev_status is None else _need(dev_status, "dev_status", ix, torch.int32, dev_status.shape), _raw_stream(ix)))
+        B, n, T, H, Dk, Dv, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), pz, pl, g_min, beta.data_ptr(),
+        state.data_ptr(), ps, pg, eps, out.data_ptr(), pd, _raw_stream(ix)))
     return out
 
 
