@@ -6,7 +6,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # KDA_LIBRARY picks another in-tree build of the same ABI by file name (libkda_checked.so: the
@@ -115,21 +114,6 @@ class GdnDecodeArgs(ctypes.Structure):
     ]
 
 
-def packer(structure):
-    """The native struct.Struct of a ctypes.Structure of plain fields: packing positional values into bytes costs a
-    fraction of filling the Structure, for calls that take microseconds.  Addresses are integers (0 for NULL)."""
-    codes = {_p: "P", _i64: "q", _i32: "i", ctypes.c_int: "i", _f32: "f", ctypes.c_size_t: "N"}
-
-    def fields(st):
-        return "".join(fields(t) if isinstance(t, type) and issubclass(t, ctypes.Structure) else codes[t]
-                       for _, t in st._fields_)
-
-    made = struct.Struct("@" + fields(structure))
-    if made.size > ctypes.sizeof(structure):  # (a C struct may end in padding that the packed bytes do not need)
-        raise TypeError(f"{structure.__name__} is not a plain struct")
-    return made
-
-
 # name -> (restype, argtypes); every symbol declared in include/kda.h
 SIGNATURES = {
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -152,10 +136,10 @@ SIGNATURES = {
     "kda_dplr_recurrent_fwd": (ctypes.c_int, [ctypes.POINTER(DplrArgs)]),
     "kda_dplr_chunk_workspace_size": (ctypes.c_int, [ctypes.POINTER(DplrArgs), ctypes.POINTER(ctypes.c_size_t)]),
     "kda_dplr_chunk_fwd": (ctypes.c_int, [ctypes.POINTER(DplrArgs), ctypes.c_void_p, ctypes.c_size_t]),
-    "kda_qk_norm_fwd": (ctypes.c_int, [_p]),  # a QkNormArgs, or its packed bytes
+    "kda_qk_norm_fwd": (ctypes.c_int, [ctypes.POINTER(QkNormArgs)]),
     "kda_qk_norm_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(QkNormBwdArgs), ctypes.POINTER(ctypes.c_size_t)]),
     "kda_qk_norm_bwd": (ctypes.c_int, [ctypes.POINTER(QkNormBwdArgs)]),
-    "kda_gdn_decode_step": (ctypes.c_int, [_p]),  # a GdnDecodeArgs, or its packed bytes
+    "kda_gdn_decode_step": (ctypes.c_int, [ctypes.POINTER(GdnDecodeArgs)]),
     "kda_gdn_chunk_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(RecBwdArgs), ctypes.POINTER(ctypes.c_size_t)]),
     "kda_gdn_chunk_bwd": (ctypes.c_int, [ctypes.POINTER(RecBwdArgs)]),
     "kda_quant_fp8": (ctypes.c_int, [_p, ctypes.c_int, _i64, _i64, _i32, _p, _p, _p]),

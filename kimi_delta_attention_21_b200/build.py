@@ -9,6 +9,10 @@ or any header changed.  --checked builds the bounds-checked variant
 through an offset the library computes is tested against its buffer and, if it
 would leave it, skipped and counted (kda_device_bounds_errors).  The binding
 loads it when KDA_LIBRARY names it.
+
+csrc_py/marshal.cpp, the argument marshalling of the operators whose calls take
+microseconds, compiles with g++ against torch's headers into _marshal.so (the
+library itself knows nothing of torch).
 """
 from __future__ import annotations
 
@@ -57,6 +61,29 @@ def _compile(src, ptxas_verbose, build_dir=BUILD, extra=()):
     return obj, r.stderr
 
 
+def build_marshal() -> str:
+    """Compile csrc_py/marshal.cpp into the importable _marshal.so."""
+    src, so = os.path.join(PKG, "csrc_py", "marshal.cpp"), os.path.join(PKG, "_marshal.so")
+    if not _stale(so, [src] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        return so
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    system = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+              os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    tmp = so + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp, src, "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], *(a for d in system for a in ("-isystem", d)),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-L" + os.path.join(root, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, so)
+    return so
+
+
 def build(ptxas_verbose: bool = False, quiet: bool = True, checked: bool = False) -> str:
     build_dir, lib = (BUILD_CHECKED, LIB_CHECKED) if checked else (BUILD, LIB)
     extra = ("-DKDA_CHECKED",) if checked else ()
@@ -76,6 +103,8 @@ def build(ptxas_verbose: bool = False, quiet: bool = True, checked: bool = False
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
+    if not checked:
+        build_marshal()
     return lib
 
 

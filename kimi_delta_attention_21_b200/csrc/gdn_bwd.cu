@@ -664,8 +664,8 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     auto stage_cols = [&](T *dst, const T *src, int j0) {  // 32 columns of token rows
         if (p.wide_v) {
             constexpr int E = 16 / (int)sizeof(T), VPR = 32 / E;
-            const int i = tid, r = i / VPR, c = i % VPR * E;
-            if (i < C * VPR) {
+            const int r = tid / VPR, c = tid % VPR * E;
+            if (tid < C * VPR) {
                 const bool in = r < len && j0 + c < Dv;
                 cp_async16_fill(reinterpret_cast<float *>(dst + r * LQ + c),
                                 reinterpret_cast<const float *>(src + (in ? r * rv + j0 + c : 0)), in);
@@ -716,13 +716,13 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
             if (Piece<T>::SETS == 2 && i + 1 < np) stage(i + 1);
             const Piece<T> q(area, i);
             if (inK) {
-                tf32::tile<2, 2, false, false, EX, false>(dq, q.dO + r0 * LQ, LQ, q.S + c0 * LQ, LQ, 32);
-                tf32::tile<2, 2, false, false, false, false>(w, q.dV + r0 * LQ, LQ, q.S + c0 * LQ, LQ, 32);
-                tf32::tile<2, 2, false, false, false, false>(dk, q.V + r0 * LQ, LQ, q.dS + c0 * LQ, LQ, 32);
+                tf32::tile<2, 2, false, false, EX, false, 1, 4>(dq, q.dO + r0 * LQ, LQ, q.S + c0 * LQ, LQ, 32);
+                tf32::tile<2, 2, false, false, false, false, 1, 4>(w, q.dV + r0 * LQ, LQ, q.S + c0 * LQ, LQ, 32);
+                tf32::tile<2, 2, false, false, false, false, 1, 4>(dk, q.V + r0 * LQ, LQ, q.dS + c0 * LQ, LQ, 32);
             }
             if (tri) {
-                tf32::tile<2, 1, false, false, EX, false>(m, q.dO + r0 * LQ, LQ, q.V + c1 * LQ, LQ, 32);
-                tf32::tile<2, 1, false, false, false, EX>(d, q.dV + r0 * LQ, LQ, q.v + c1 * LQ, LQ, 32);
+                tf32::tile<2, 1, false, false, EX, false, 1, 4>(m, q.dO + r0 * LQ, LQ, q.V + c1 * LQ, LQ, 32);
+                tf32::tile<2, 1, false, false, false, EX, 1, 4>(d, q.dV + r0 * LQ, LQ, q.v + c1 * LQ, LQ, 32);
             }
             for (int r = tid >> 3, c = (tid & 7) * 4; r < Dkp; r += NT_P / 8) {
                 const float4 x = *reinterpret_cast<const float4 *>(q.S + r * LQ + c);
@@ -734,14 +734,14 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
                 stage(i + 1);
             }
         }
-        cp_async_wait<0>();
-        __syncthreads();  // the pieces are read; k, q and T are there
-        stage_block<NT_P, 32>(sdV, LD, rec + R.dV, Dvp, C, Dvp);
-        cp_async_commit_group();
         float2 M[2][2];
         tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
             if (!(e & 1)) M[i][e >> 1] = *reinterpret_cast<const float2 *>(rec + R.M + (r0 + r) * C + c1 + c);
         });
+        cp_async_wait<0>();
+        __syncthreads();  // the pieces are read; k, q and T are there
+        stage_block<NT_P, 32>(sdV, LD, rec + R.dV, Dvp, C, Dvp);
+        cp_async_commit_group();
         if (inK)  // dq = e^G dQg, dk = e^D dKd, dW
             tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
                 r += r0;
@@ -769,6 +769,10 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
             sdT[r * LC + c] = c <= r ? sb[c] * fmaf(seG[c], b[i][j][e], d[i][j][e]) : 0.f;
         });
     }
+    float2 vv[2][2][2];  // this lane's pairs of v, on their way meanwhile
+    tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
+        if (!(e & 1)) vv[i][j][e >> 1] = row_pair(gv + (r0 + r) * rv, c0 + c, Dv, r0 + r < len, p.wide_v);
+    });
     if (inK) {  // dBk = T^T dW
         float a[2][2][4] = {};
         tf32::tile<2, 2, true, true, false, false>(a, sT + r0 + r0 * LC, LC, sdW + c0 + r0 * LD, LD, C - r0);
@@ -783,10 +787,6 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     cp_async_wait<0>();  // dV'
     __syncthreads();
     if (inV) {  // dBv = T^T dV'
-        float2 vv[2][2][2];
-        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
-            if (!(e & 1)) vv[i][j][e >> 1] = row_pair(gv + (r0 + r) * rv, c0 + c, Dv, r0 + r < len, p.wide_v);
-        });
         float a[2][2][4] = {};
         tf32::tile<2, 2, true, true, false, false>(a, sT + r0 + r0 * LC, LC, sdV + c0 + r0 * LD, LD, C - r0);
         tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
@@ -881,17 +881,23 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
         sums[tid] = s;
     }
     __syncthreads();
-    if (tid < C) {
-        const int t = tid;
-        float s = 0.f, before = 0.f, pairs = 0.f, d = 0.f;
-        for (int r = t; r < C; ++r) {
-            s += sums[r];
-            pairs += t > 0 ? sX[r * LC + t - 1] : 0.f;
-        }
-        for (int i = 0; i < t; ++i) before += sums[C + i];
+    {  // eight lanes per token share its sums
+        const int t = tid >> 3, part = tid & 7;
+        float dg = 0.f;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) d += sred[w];
-        const float dg = s + pairs + before + seG[C - 1] * d;
+        for (int i = 0; i < C / 8; ++i) {
+            const int r = part + 8 * i;
+            if (r >= t) dg += sums[r] + (t > 0 ? sX[r * LC + t - 1] : 0.f);
+            else dg += sums[C + r];
+        }
+        float d = sred[part] + sred[part + 8];
+#pragma unroll
+        for (int m = 4; m > 0; m >>= 1) {
+            dg += __shfl_xor_sync(0xffffffffu, dg, m);
+            d += __shfl_xor_sync(0xffffffffu, d, m);
+        }
+        dg = fmaf(seG[C - 1], d, dg);
+        if (part) return;
         if (t < len) {
             const int64_t at = u.row0 + (int64_t)t * p.H;
             p.dbeta[at] = sums[2 * C + t];
