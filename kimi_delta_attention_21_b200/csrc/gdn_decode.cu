@@ -8,6 +8,9 @@
 // (sequence, head): lane l of warp w owns the key rows w, w + 8, ... and four value columns, so that a
 // warp reads whole rows; the sums over key rows are partial sums of 8 warps joined in shared memory, one
 // barrier each (the buffers alternate, so the next token's sums need no second one).
+// Measured (bf16, D = 128, 32 heads): 256 sequences 183 us, 5.9 TB/s (90% of a copy's rate; a plain in-place
+// update of as many bytes takes 159 us); with three CTAs on an SM instead of two it spills (233 us), with plain
+// stores instead of streaming ones 218 us.  One sequence: 5 us, the call's own time.
 #include "host_check.cuh"
 #include "kda_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -52,6 +55,32 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
     }
     float *S = p.state + (slot * p.H + h) * (int64_t)Dk * Dv;
     auto col = [&](int j) { return VEC ? 4 * l + j : l + 32 * j; };
+    const int64_t tok0 = b * p.T * p.H + h;  // (token, head) index of token 0; p.H further for each token
+    auto fetch = [&](int t) {                // this thread's element of token t's q (threads < 128) or k
+        const int c = tid & 127;
+        const T *src = (const T *)(tid < 128 ? p.q : p.k);
+        return c < Dk ? load_elem(src, (tok0 + (int64_t)t * p.H) * Dk + c) : 0.f;
+    };
+    struct Token {  // what this thread needs of a token besides q and k
+        T v[4], gate[4], beta, z;
+        float log_decay;
+    };
+    auto token = [&](int t) {
+        const int64_t th = tok0 + (int64_t)t * p.H;
+        Token n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool in = FULL || col(j) < Dv;
+            n.v[j] = in ? ((const T *)p.v)[th * Dv + col(j)] : T(0.f);
+            n.gate[j] = (in && p.gate) ? ((const T *)p.gate)[th * Dv + col(j)] : T(0.f);
+        }
+        n.beta = ((const T *)p.beta)[th];
+        if (p.log_decay) n.log_decay = p.log_decay[th];
+        else n.z = ((const T *)p.z)[th];
+        return n;
+    };
+    float pre = fetch(0);  // ahead of the state: behind it they would wait for all of it (203 -> 183 us at 256 x 32)
+    Token now = token(0);
     float s[GD_RPW][4];
 #pragma unroll
     for (int i = 0; i < GD_RPW; ++i) {
@@ -73,13 +102,6 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
             return;
         }
     }
-    const int64_t tok0 = b * p.T * p.H + h;  // (token, head) index of token 0; p.H further for each token
-    auto fetch = [&](int t) {                // this thread's element of token t's q (threads < 128) or k
-        const int c = tid & 127;
-        const T *src = (const T *)(tid < 128 ? p.q : p.k);
-        return c < Dk ? load_elem(src, (tok0 + (int64_t)t * p.H) * Dk + c) : 0.f;
-    };
-    float pre = fetch(0);
     for (int t = 0; t < p.T; ++t) {
         const int64_t th = tok0 + (int64_t)t * p.H;
         const int buf = t & 1;
@@ -87,14 +109,11 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
         float v[4], gt[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const bool in = FULL || col(j) < Dv;
-            v[j] = in ? load_elem((const T *)p.v, th * Dv + col(j)) : 0.f;
-            gt[j] = (in && p.gate) ? load_elem((const T *)p.gate, th * Dv + col(j)) : 0.f;
+            v[j] = (float)now.v[j];
+            gt[j] = (float)now.gate[j];
         }
-        const float bt = load_elem((const T *)p.beta, th);
-        const float g = p.log_decay ? clamp_log_decay(p.log_decay[th], p.g_min)
-                                    : log_alpha_of(load_elem((const T *)p.z, th), p.g_min);
-        const float a = expf(g);
+        const float bt = (float)now.beta;
+        const float a = expf(p.log_decay ? clamp_log_decay(now.log_decay, p.g_min) : log_alpha_of((float)now.z, p.g_min));
         if (t + 1 < p.T) pre = fetch(t + 1);
         __syncthreads();  // q and k of token t
         float qk = 0.f, pp[4] = {0.f, 0.f, 0.f, 0.f}, qs[4] = {0.f, 0.f, 0.f, 0.f};
@@ -150,6 +169,7 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
             for (int j = 0; j < 4; ++j)
                 if (FULL || col(j) < Dv) store_elem((T *)p.o, th * Dv + col(j), o[j]);
         }
+        if (t + 1 < p.T) now = token(t + 1);  // here, not above: its registers beside the sums cost 8% of eight tokens
     }
     if (!in_bounds(S, (size_t)Dk * Dv * 4, p.state, p.state_bytes, p.bounds)) return;
 #pragma unroll
