@@ -152,7 +152,14 @@ PyObject *wrap(const at::Tensor &t) {
 PyObject *tuple_of(std::initializer_list<at::Tensor> ts) {
     PyObject *r = PyTuple_New((Py_ssize_t)ts.size());
     Py_ssize_t i = 0;
-    for (const at::Tensor &t : ts) PyTuple_SET_ITEM(r, i++, wrap(t));
+    for (const at::Tensor &t : ts) {
+        PyObject *o = r ? wrap(t) : nullptr;
+        if (!o) {
+            Py_XDECREF(r);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(r, i++, o);
+    }
     return r;
 }
 

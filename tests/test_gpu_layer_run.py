@@ -76,10 +76,8 @@ def test_training_gradients_to_the_raw_projections(K):
     q, k, v, beta, z, _, pos, inv = raw(B, S, H, D, F32, 3)
     g = gen(4)
     s0, d_o = randn(g, B, H, D, D, std=0.1), randn(g, B, S, H, D)
-    w = 1 + randn(g, D, std=0.1)
+    w = D ** -0.5 * (1 + randn(g, D, std=0.1))       # unit keys from the RMS norm: the weight carries 1 / sqrt(D)
     kw = dict(norm="rms", q_weight=w, k_weight=w, positions=pos, inv_freq=inv)
-    scale = D ** -0.5                                # unit keys from the RMS norm: the weight carries 1 / sqrt(D)
-    kw["q_weight"] = kw["k_weight"] = (w * scale).contiguous()
     qn, kn = K.qk_norm(q, k, **kw)
     core = K.gdn_chunk_bwd(qn, kn, v, beta, d_o, z=z, g_min=-1.0, initial_state=s0)
     front = K.qk_norm_bwd(q, k, core["dq"], core["dk"], **kw)

@@ -6,7 +6,9 @@ import os
 import subprocess
 
 import pytest
+import torch
 
+import kimi_delta_attention_21_b200 as K
 from kimi_delta_attention_21_b200 import _lib as L
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -173,3 +175,25 @@ def test_gdn_bwd_workspace_is_one_record_per_chunk(B, S, H, Dk, Dv):
     assert L.load().kda_gdn_chunk_bwd_workspace_size(ctypes.byref(a), ctypes.byref(n)) == L.KDA_OK
     dk, dv = up(Dk, 16), up(Dv, 32)
     assert n.value == B * H * -(-S // 64) * 4 * (256 + 12288 + 64 * (dk + 2 * dv) + 2 * dk * dv)
+
+
+Z = torch.zeros
+
+
+@pytest.mark.parametrize("call,error,text", [
+    (lambda: K.qk_norm(Z(2, 2, 2), Z(2, 2, 2)), ValueError, "q must be a CUDA tensor"),
+    (lambda: K.qk_norm(None, Z(2, 2, 2)), ValueError, "q must be a CUDA tensor"),
+    (lambda: K.qk_norm(Z(2, 2, 2), Z(2, 2, 2), norm="layer"), ValueError, "norm must be one of"),
+    (lambda: K.qk_norm_bwd(*[Z(2, 2, 2)] * 4), ValueError, "q must be a CUDA tensor"),
+    (lambda: K.gdn_decode_step(*[Z(2, 2, 2)] * 5, z=Z(2, 2)), ValueError, "q must be a CUDA tensor"),
+    (lambda: K.gdn_chunk_bwd(*[Z(1, 1, 1, 1)] * 5), ValueError, "q must be a CUDA tensor"),
+    (lambda: K.quant_fp8(Z(4, 4)), ValueError, "x must be a CUDA tensor"),
+    (lambda: K.norm_gate_fp8(Z(2, 2), Z(2, 2)), ValueError, "o must be a CUDA tensor"),
+    (lambda: K.out_proj_fp8(*[Z(2, 2)] * 4), ValueError, "x8 must be a CUDA tensor"),
+    (lambda: K.out_proj_fp8(*[Z(2, 2)] * 4, out_dtype=torch.half), TypeError, "out_dtype"),
+])
+def test_python_calls_without_device_tensors_are_refused(call, error, text):
+    n0 = L.load().kda_launch_count()
+    with pytest.raises(error, match=text):
+        call()
+    assert L.load().kda_launch_count() == n0
