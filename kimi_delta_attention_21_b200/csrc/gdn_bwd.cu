@@ -39,9 +39,8 @@ namespace {
 constexpr int C = 64;       // tokens per chunk
 constexpr int LD = 136;     // pitch of [64 or 128][D] tiles in shared memory: 8 mod 32
 constexpr int LC = 72;      // pitch of [64][64] tiles
-constexpr int NT_P = 512;   // threads of the per-chunk kernels
+constexpr int NT_P = 512;   // threads of the gradient kernel
 constexpr int NT_C = 512;   // threads of the chain kernel
-constexpr int LP = 130;     // pitch of split [64][128] tiles: 2 mod 8 pairs
 constexpr int VS = 32;      // value columns per chain CTA
 constexpr int LS = 34;      // chain pitch of the split [Dk][32] state: 2 mod 8 pairs (read in pairs of k)
 constexpr int LO = 36;      // and of plain [.][32] ones
@@ -173,20 +172,23 @@ __device__ __forceinline__ void store_pair(float *row, int c, int D, bool in, bo
     }
 }
 
-// ---------------------------------------------------------------- per chunk: P, M, T, W, U
+// ---------------------------------------------------------------- per chunk: P, M, T, W, U, M^T dO, Q^T (e^G dO)
+// bf16 inputs: two CTAs of 8 warps on an SM, so that one's products run through the other's loads and inverse.  That
+// needs 106 KB a CTA: M gives its place to T once M^T dO is formed, Q to V.  fp32 ones: one CTA of 16 warps.
+template <typename T> constexpr int prep_nt() { return sizeof(T) == 2 ? 256 : 512; }
 template <typename T> constexpr size_t prep_smem() {
-    return sizeof(double) * C + sizeof(float) * (4 * C * LC + 2 * C) + 4 * sizeof(T) * C * LD +
-           (sizeof(T) == 2 ? sizeof(float2) * C * LP : 0);
+    return sizeof(double) * C + sizeof(float) * (3 * C * LC + 2 * C) + 3 * sizeof(T) * C * LD;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant__ GbArgs p) {
+__global__ void __launch_bounds__(prep_nt<T>(), 512 / prep_nt<T>()) gb_prep_kernel(const __grid_constant__ GbArgs p) {
     constexpr bool EX = sizeof(T) == 2;
+    constexpr int NT = prep_nt<T>(), NW = NT / 32;
     extern __shared__ __align__(16) uint8_t gb_sm[];
     double *sG = reinterpret_cast<double *>(gb_sm);
-    float *sA = reinterpret_cast<float *>(sG + C), *sT = sA + C * LC, *sY = sT + C * LC, *sM = sY + C * LC;
-    float *sb = sM + C * LC, *seG = sb + C;
-    T *sK = reinterpret_cast<T *>(seG + C), *sQ = sK + C * LD, *sV = sQ + C * LD, *sO = sV + C * LD;
+    float *sA = reinterpret_cast<float *>(sG + C), *sM = sA + C * LC, *sT = sM, *sY = sM + C * LC;
+    float *sb = sY + C * LC, *seG = sb + C;
+    T *sK = reinterpret_cast<T *>(seG + C), *sQ = sK + C * LD, *sV = sQ, *sO = sQ + C * LD;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t bh = blockIdx.x / p.Nc;
     const int n = (int)(blockIdx.x - bh * p.Nc);
@@ -197,11 +199,10 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
     if (!in_bounds(rec, (size_t)R.size * 4, p.ws, p.ws_bytes, p.bounds)) return;
 
     const int64_t rk = (int64_t)p.H * p.Dk, rv = (int64_t)p.H * p.Dv;
-    stage_rows<T, NT_P>(sK, (const T *)p.k + u.row0 * p.Dk, rk, u.len, p.Dk, Dkp, p.wide_k);
-    stage_rows<T, NT_P>(sQ, (const T *)p.q + u.row0 * p.Dk, rk, u.len, p.Dk, Dkp, p.wide_k);
+    stage_rows<T, NT>(sK, (const T *)p.k + u.row0 * p.Dk, rk, u.len, p.Dk, Dkp, p.wide_k);
+    stage_rows<T, NT>(sQ, (const T *)p.q + u.row0 * p.Dk, rk, u.len, p.Dk, Dkp, p.wide_k);
     cp_async_commit_group();
-    stage_rows<T, NT_P>(sV, (const T *)p.v + u.row0 * p.Dv, rv, u.len, p.Dv, Dvp, p.wide_v);
-    stage_rows<T, NT_P>(sO, (const T *)p.dO + u.row0 * p.Dv, rv, u.len, p.Dv, Dvp, p.wide_v);
+    stage_rows<T, NT>(sO, (const T *)p.dO + u.row0 * p.Dv, rv, u.len, p.Dv, Dvp, p.wide_v);
     cp_async_commit_group();
     if (warp == 0) {  // the cumulative log-decay: two tokens per lane, a scan over the warp
         double g[2];
@@ -239,18 +240,18 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
             rec[R.eD + r] = d;
         }
     }
-    for (int i = tid; i < C * LC; i += NT_P) sT[i] = 0.f;
     cp_async_wait<1>();  // k and q
     __syncthreads();
-    // P and M: warp (32 rows, 8 columns); tiles above the diagonal are zeros
+    // P and M: warp (32 rows, 8 or 16 columns); tiles above the diagonal are zeros
     {
-        const int r0 = 32 * (warp & 1), c0 = 8 * (warp >> 1);
-        float kk[2][1][4] = {}, qk[2][1][4] = {};
+        constexpr int NC = 16 / NW;
+        const int r0 = 32 * (warp & 1), c0 = 8 * NC * (warp >> 1);
+        float kk[2][NC][4] = {}, qk[2][NC][4] = {};
         if (c0 < r0 + 32) {
-            tf32::tile<2, 1, false, false, EX, EX>(kk, sK + r0 * LD, LD, sK + c0 * LD, LD, Dkp);
-            tf32::tile<2, 1, false, false, EX, EX>(qk, sQ + r0 * LD, LD, sK + c0 * LD, LD, Dkp);
+            tf32::tile<2, NC, false, false, EX, EX>(kk, sK + r0 * LD, LD, sK + c0 * LD, LD, Dkp);
+            tf32::tile<2, NC, false, false, EX, EX>(qk, sQ + r0 * LD, LD, sK + c0 * LD, LD, Dkp);
         }
-        tf32::each<2, 1>([&](int i, int j, int e, int r, int c) {
+        tf32::each<2, NC>([&](int i, int j, int e, int r, int c) {
             r += r0;
             c += c0;
             const float x = c <= r ? expf((float)(sG[r] - sG[c])) : 0.f;
@@ -264,7 +265,36 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
             }
         });
     }
+    cp_async_wait<0>();  // dO
     __syncthreads();
+    // 32 rows and 16 or 32 columns of a [64][D] result per warp
+    constexpr int NC = 32 / NW;
+    const int r0 = 32 * (warp & 1), c0 = 8 * NC * (warp >> 1);
+    auto put = [&](float *dst, int pitch, const float (&acc)[2][NC][4]) {
+        tf32::each<2, NC>([&](int i, int j, int e, int r, int c) {
+            if (!(e & 1) && c0 + c < pitch)
+                *reinterpret_cast<float2 *>(dst + (r0 + r) * pitch + c0 + c) = make_float2(acc[i][j][e], acc[i][j][e + 1]);
+        });
+    };
+    if (c0 < Dvp) {  // M^T dO: what dV' has of the chunk itself
+        float o[2][NC][4] = {};
+        tf32::tile<2, NC, true, true, false, EX>(o, sM + r0 + r0 * LC, LC, sO + c0 + r0 * LD, LD, C - r0);
+        put(rec + R.dV, Dvp, o);
+    }
+    // Q^T (e^G dO): what dS has of the chunk itself, 32 x 32 of [Dk][Dv] at a time
+    for (int t = warp; t < 16; t += NW) {
+        const int m0 = 32 * (t & 3), n0 = 32 * (t >> 2);
+        if (m0 >= Dkp || n0 >= Dvp) continue;
+        float h[2][4][4] = {};
+        tf32::tile<2, 4, true, true, EX, false, 1, 2, true>(h, sQ + m0, LD, sO + n0, LD, C, seG);
+        tf32::each<2, 4>([&](int i, int j, int e, int r, int c) {
+            if (!(e & 1) && m0 + r < Dkp)
+                *reinterpret_cast<float2 *>(rec + R.dS + (m0 + r) * Dvp + n0 + c) = make_float2(h[i][j][e], h[i][j][e + 1]);
+        });
+    }
+    __syncthreads();  // M and Q have been read
+    stage_rows<T, NT>(sV, (const T *)p.v + u.row0 * p.Dv, rv, u.len, p.Dv, Dvp, p.wide_v);
+    cp_async_commit_group();
     // T = (I + A)^{-1}: the four diagonal blocks of 16 by forward substitution (a thread per column) ...
     if (warp < 4 && lane < 16) {
         const float *a = sA + 16 * warp * (LC + 1);
@@ -279,47 +309,58 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
 #pragma unroll
         for (int r = 0; r < 16; ++r) sT[(16 * warp + r) * LC + 16 * warp + lane] = x[r];
     }
+    for (int i = tid; i < C * C; i += NT) {  // (the blocks above them are zeros)
+        const int r = i >> 6, c = i & 63;
+        if ((r >> 4) < (c >> 4)) sT[r * LC + c] = 0.f;
+    }
     __syncthreads();
     // ... then T21 = -T22 (A21 T11), blocks of 16 and of 32
-    {
-        const int b0 = 32 * (tid >> 8), r = (tid & 255) >> 4, c = tid & 15;
+#pragma unroll
+    for (int i = tid; i < 512; i += NT) {
+        const int b0 = 32 * (i >> 8), r = (i & 255) >> 4, c = i & 15;
         float s = 0.f;
 #pragma unroll
         for (int m = 0; m < 16; ++m) s = fmaf(sA[(b0 + 16 + r) * LC + b0 + m], sT[(b0 + m) * LC + b0 + c], s);
         sY[(b0 + r) * LC + c] = s;
-        __syncthreads();
-        s = 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = tid; i < 512; i += NT) {
+        const int b0 = 32 * (i >> 8), r = (i & 255) >> 4, c = i & 15;
+        float s = 0.f;
 #pragma unroll
         for (int m = 0; m < 16; ++m) s = fmaf(-sT[(b0 + 16 + r) * LC + b0 + 16 + m], sY[(b0 + m) * LC + c], s);
         sT[(b0 + 16 + r) * LC + b0 + c] = s;
     }
     __syncthreads();
     {
-        float s[2] = {0.f, 0.f};
-        const int c = tid & 31, r = tid >> 5;
+        constexpr int RW = 32 / NW;  // rows per thread
+        float s[RW] = {};
+        const int c = lane, r = warp;
 #pragma unroll 8
         for (int m = 0; m < 32; ++m) {
             const float t = sT[m * LC + c];
-            s[0] = fmaf(sA[(32 + r) * LC + m], t, s[0]);
-            s[1] = fmaf(sA[(48 + r) * LC + m], t, s[1]);
+#pragma unroll
+            for (int e = 0; e < RW; ++e) s[e] = fmaf(sA[(32 + r + NW * e) * LC + m], t, s[e]);
         }
-        sY[r * LC + c] = s[0];
-        sY[(16 + r) * LC + c] = s[1];
+#pragma unroll
+        for (int e = 0; e < RW; ++e) sY[(r + NW * e) * LC + c] = s[e];
         __syncthreads();
-        s[0] = s[1] = 0.f;
+#pragma unroll
+        for (int e = 0; e < RW; ++e) s[e] = 0.f;
 #pragma unroll 8
         for (int m = 0; m < 32; ++m) {
             const float y = sY[m * LC + c];
-            s[0] = fmaf(-sT[(32 + r) * LC + 32 + m], y, s[0]);
-            s[1] = fmaf(-sT[(48 + r) * LC + 32 + m], y, s[1]);
+#pragma unroll
+            for (int e = 0; e < RW; ++e) s[e] = fmaf(-sT[(32 + r + NW * e) * LC + 32 + m], y, s[e]);
         }
-        sT[(32 + r) * LC + c] = s[0];
-        sT[(48 + r) * LC + c] = s[1];
+#pragma unroll
+        for (int e = 0; e < RW; ++e) sT[(32 + r + NW * e) * LC + c] = s[e];
     }
-    cp_async_wait<0>();  // v and dO (made visible by the next barrier)
+    cp_async_wait<0>();  // v (made visible by the next barrier but one)
     __syncthreads();
     // T out; T Diag(beta e^G) over A, T Diag(beta) over the scratch: the scales of Bk's and Bv's rows
-    for (int i = tid; i < C * C; i += NT_P) {
+    for (int i = tid; i < C * C; i += NT) {
         const int r = i >> 6, c = i & 63;
         const float t = sT[r * LC + c], tb = t * sb[c];
         rec[R.T + i] = t;
@@ -327,49 +368,16 @@ __global__ void __launch_bounds__(NT_P, 1) gb_prep_kernel(const __grid_constant_
         sY[r * LC + c] = tb;
     }
     __syncthreads();
-    const int r0 = 32 * (warp & 1), c0 = 16 * (warp >> 1);
-    auto put = [&](float *dst, int pitch, const float (&acc)[2][2][4]) {
-        tf32::each<2, 2>([&](int i, int j, int e, int r, int c) {
-            if (!(e & 1))
-                *reinterpret_cast<float2 *>(dst + (r0 + r) * pitch + c0 + c) = make_float2(acc[i][j][e], acc[i][j][e + 1]);
-        });
-    };
     if (c0 < Dkp) {
-        float acc[2][2][4] = {};
-        tf32::tile<2, 2, false, true, false, EX>(acc, sA + r0 * LC, LC, sK + c0, LD, r0 + 32);
+        float acc[2][NC][4] = {};
+        tf32::tile<2, NC, false, true, false, EX>(acc, sA + r0 * LC, LC, sK + c0, LD, r0 + 32);
         put(rec + R.W, Dkp, acc);
     }
     if (c0 < Dvp) {
-        float acc[2][2][4] = {}, o[2][2][4] = {};
-        tf32::tile<2, 2, false, true, false, EX>(acc, sY + r0 * LC, LC, sV + c0, LD, r0 + 32);
+        float acc[2][NC][4] = {};
+        tf32::tile<2, NC, false, true, false, EX>(acc, sY + r0 * LC, LC, sV + c0, LD, r0 + 32);
         put(rec + R.V, Dvp, acc);
-        // M^T dO: what dV' has of the chunk itself
-        tf32::tile<2, 2, true, true, false, EX>(o, sM + r0 + r0 * LC, LC, sO + c0 + r0 * LD, LD, C - r0);
-        put(rec + R.dV, Dvp, o);
     }
-    // Q^T (e^G dO): what dS has of the chunk itself.  32 x 32 of [Dk][Dv] per warp, e^G on the rows of the exact side
-    // (fp32 dO: on dO, in place)
-    const int m0 = 32 * (warp & 3), n0 = 32 * (warp >> 2);
-    float h[2][4][4] = {};
-    if constexpr (EX) {
-        float2 *sgO = reinterpret_cast<float2 *>(sO + C * LD);  // e^G dO, split, 128 columns
-        for (int i = tid; i < C * 128; i += NT_P) {
-            const int r = i >> 7, c = i & 127;
-            if (c < Dvp) sgO[r * LP + c] = tf32::split2(seG[r] * load_elem(sO, r * LD + c));
-        }
-        __syncthreads();
-        if (m0 < Dkp && n0 < Dvp) tf32::tile<2, 4, true, true, EX, false>(h, sQ + m0, LD, sgO + n0, LP, C);
-    } else {
-        __syncthreads();  // M^T dO has read dO
-        for (int i = tid; i < C * 128; i += NT_P) sO[(i >> 7) * LD + (i & 127)] *= seG[i >> 7];
-        __syncthreads();
-        if (m0 < Dkp && n0 < Dvp) tf32::tile<2, 4, true, true, EX, false>(h, sQ + m0, LD, sO + n0, LD, C);
-    }
-    if (n0 < Dvp)
-        tf32::each<2, 4>([&](int i, int j, int e, int r, int c) {
-            if (!(e & 1) && m0 + r < Dkp)
-                *reinterpret_cast<float2 *>(rec + R.dS + (m0 + r) * Dvp + n0 + c) = make_float2(h[i][j][e], h[i][j][e + 1]);
-        });
 }
 
 // ---------------------------------------------------------------- the state and its gradient through the chunks
@@ -928,7 +936,7 @@ kda_status_t gb_launch(GbArgs p, int64_t nbh, cudaStream_t st) {
     p.wide_v = p.Dv * (int)sizeof(T) % 16 == 0 && aligned_to(p.v, 16) && aligned_to(p.dO, 16);
     p.pair_k = p.Dk % 2 == 0 && aligned_to(p.dq, 8) && aligned_to(p.dk, 8);
     p.pair_v = p.Dv % 2 == 0 && aligned_to(p.dv, 8);
-    gb_prep_kernel<T><<<(unsigned)units, NT_P, prep_smem<T>(), st>>>(p);
+    gb_prep_kernel<T><<<(unsigned)units, prep_nt<T>(), prep_smem<T>(), st>>>(p);
     KDA_TRY(check_launch("gb_prep_kernel"));
     chain<<<(unsigned)jobs, NT_C, chain_smem<T>(), st>>>(p);
     KDA_TRY(check_launch("gb_chain_kernel"));

@@ -69,14 +69,15 @@ __device__ __forceinline__ void ldsm_trans(uint32_t (&r)[4], uint32_t addr) {
 // 2 mod 8 pairs where k comes in pairs, 4 mod 16 where it does not.
 // The lo terms have accumulators of their own, so that the tensor core, which truncates as it adds, does so once per
 // step of 8 on the large sums; CROSS = 2 keeps the two kinds apart (shorter dependent chains where a warp has few
-// tiles).
-template <int MT, int NT, bool AT, bool BT, bool AEX, bool BEX, int CROSS = 1, int UNROLL = 2, typename TA,
-          typename TB>
+// tiles).  KS: B's rows k are multiplied by ks[k] as they are read.
+template <int MT, int NT, bool AT, bool BT, bool AEX, bool BEX, int CROSS = 1, int UNROLL = 2, bool KS = false,
+          typename TA, typename TB>
 __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int lda, const TB *B, int ldb,
-                                     int K) {
+                                     int K, const float *ks = nullptr) {
     constexpr bool A16 = sizeof(TA) == 2 && AT, B16 = sizeof(TB) == 2 && BT;
     constexpr bool PAIR = !(AT && BT) || A16 || B16;
     static_assert(sizeof(TB) != 8 || BT, "split operands are read by k");
+    static_assert(!KS || (BT && !BEX && sizeof(TB) != 8), "a scaled operand is read by k, and is not exact");
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float cross[CROSS][MT][NT][4] = {};
     uint32_t arow = 0, brow = 0;  // this lane's row for ldmatrix: k = lane % 8, of block lane / 8
@@ -87,6 +88,11 @@ __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int l
     for (int k = 0; k < K; k += 8) {
         const int ka = PAIR ? k + 2 * t : k + t, kb = PAIR ? ka + 1 : ka + 4;
         uint32_t ah[MT][4], al[MT][4], bh[NT][2], bl[NT][2];
+        float sc[2] = {1.f, 1.f};
+        if constexpr (KS) {
+            sc[0] = ks[ka];
+            sc[1] = ks[kb];
+        }
         if constexpr (A16) {
             uint32_t r[2 * MT];
             ldsm_trans(r, arow);
@@ -127,6 +133,10 @@ __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int l
             for (int j = 0; j < NT; ++j) {
                 bh[j][0] = r[j] << 16;
                 bh[j][1] = r[j] & 0xffff0000u;
+                if constexpr (KS) {
+                    split(__uint_as_float(bh[j][0]) * sc[0], bh[j][0], bl[j][0]);
+                    split(__uint_as_float(bh[j][1]) * sc[1], bh[j][1], bl[j][1]);
+                }
             }
         } else {
 #pragma unroll
@@ -140,8 +150,8 @@ __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int l
                 } else {
                     float x[2];
                     if (BT) {
-                        x[0] = load_elem(B, ka * ldb + 8 * j + g);
-                        x[1] = load_elem(B, kb * ldb + 8 * j + g);
+                        x[0] = sc[0] * load_elem(B, ka * ldb + 8 * j + g);
+                        x[1] = sc[1] * load_elem(B, kb * ldb + 8 * j + g);
                     } else {
                         load2(B + (8 * j + g) * ldb + ka, x[0], x[1]);
                     }
