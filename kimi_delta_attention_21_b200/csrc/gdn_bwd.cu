@@ -172,6 +172,11 @@ __device__ __forceinline__ void store_pair(float *row, int c, int D, bool in, bo
     }
 }
 
+// A warp's 32 rows of a 64-row result; its columns are tile warp / 2.  Triangular operands give the two halves of the
+// rows sums of different lengths: the four warps of an SM sub-partition (equal warp % 4), which share a tensor core, get
+// both (the gradient kernel 335 -> 323 us on prefill_4k).
+__device__ __forceinline__ int row_half(int warp) { return 32 * ((warp ^ (warp >> 2)) & 1); }
+
 // ---------------------------------------------------------------- per chunk: P, M, T, W, U, M^T dO, Q^T (e^G dO)
 // bf16 inputs: two CTAs of 8 warps on an SM, so that one's products run through the other's loads and inverse.  That
 // needs 106 KB a CTA: M gives its place to T once M^T dO is formed, Q to V.  fp32 ones: one CTA of 16 warps.
@@ -245,7 +250,7 @@ __global__ void __launch_bounds__(prep_nt<T>(), 512 / prep_nt<T>()) gb_prep_kern
     // P and M: warp (32 rows, 8 or 16 columns); tiles above the diagonal are zeros
     {
         constexpr int NC = 16 / NW;
-        const int r0 = 32 * (warp & 1), c0 = 8 * NC * (warp >> 1);
+        const int r0 = row_half(warp), c0 = 8 * NC * (warp >> 1);
         float kk[2][NC][4] = {}, qk[2][NC][4] = {};
         if (c0 < r0 + 32) {
             tf32::tile<2, NC, false, false, EX, EX>(kk, sK + r0 * LD, LD, sK + c0 * LD, LD, Dkp);
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(prep_nt<T>(), 512 / prep_nt<T>()) gb_prep_kern
     __syncthreads();
     // 32 rows and 16 or 32 columns of a [64][D] result per warp
     constexpr int NC = 32 / NW;
-    const int r0 = 32 * (warp & 1), c0 = 8 * NC * (warp >> 1);
+    const int r0 = row_half(warp), c0 = 8 * NC * (warp >> 1);
     auto put = [&](float *dst, int pitch, const float (&acc)[2][NC][4]) {
         tf32::each<2, NC>([&](int i, int j, int e, int r, int c) {
             if (!(e & 1) && c0 + c < pitch)
@@ -709,7 +714,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
     }
 
     // every warp: 32 rows from r0; 16 columns from c0 of [64][D] results, 8 from c1 of [64][64] ones
-    const int r0 = 32 * (warp & 1), c0 = 16 * (warp >> 1), c1 = 8 * (warp >> 1);
+    const int r0 = row_half(warp), ct = warp >> 1, c0 = 16 * ct, c1 = 8 * ct;
     const bool inK = c0 < Dkp, inV = c0 < Dvp, tri = c1 < r0 + 32;  // tri: the tile reaches below the diagonal
     float dq[2][2][4] = {}, dk[2][2][4] = {}, X[2][1][4] = {};
     float late[2][2] = {}, early[2][2] = {}, db[2][2] = {};  // row sums of this lane's rows 16 i + g + 8 half
@@ -726,12 +731,12 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
             if (inK) {
                 tf32::tile<2, 2, false, false, EX, false, 1, 4>(dq, q.dO + r0 * LQ, LQ, q.S + c0 * LQ, LQ, 32);
                 tf32::tile<2, 2, false, false, false, false, 1, 4>(w, q.dV + r0 * LQ, LQ, q.S + c0 * LQ, LQ, 32);
-                tf32::tile<2, 2, false, false, false, false, 1, 4>(dk, q.V + r0 * LQ, LQ, q.dS + c0 * LQ, LQ, 32);
             }
             if (tri) {
                 tf32::tile<2, 1, false, false, EX, false, 1, 4>(m, q.dO + r0 * LQ, LQ, q.V + c1 * LQ, LQ, 32);
                 tf32::tile<2, 1, false, false, false, EX, 1, 4>(d, q.dV + r0 * LQ, LQ, q.v + c1 * LQ, LQ, 32);
             }
+            if (inK) tf32::tile<2, 2, false, false, false, false, 1, 4>(dk, q.V + r0 * LQ, LQ, q.dS + c0 * LQ, LQ, 32);
             for (int r = tid >> 3, c = (tid & 7) * 4; r < Dkp; r += NT_P / 8) {
                 const float4 x = *reinterpret_cast<const float4 *>(q.S + r * LQ + c);
                 const float4 y = *reinterpret_cast<const float4 *>(q.dS + r * LQ + c);
@@ -858,7 +863,7 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
             for (int k = 0; k < 3; ++k) {
                 s[k] += __shfl_xor_sync(0xffffffffu, s[k], 1);
                 s[k] += __shfl_xor_sync(0xffffffffu, s[k], 2);
-                if (t4 == 0) part[(k * 8 + (warp >> 1)) * C + r0 + 16 * i + 8 * hh + g] = s[k];
+                if (t4 == 0) part[(k * 8 + ct) * C + r0 + 16 * i + 8 * hh + g] = s[k];
             }
         }
     tf32::each<2, 1>([&](int i, int j, int e, int r, int c) { sX[(r0 + r) * LC + c1 + c] = X[i][j][e]; });
