@@ -538,7 +538,7 @@ kda_status_t kda_gdn_decode_step(const kda_gdn_decode_args *args);
  * csrc/mma_tf32.cuh); any g_min.  Outputs are fully written.  The workspace holds
  * one record per (b, h, chunk of 64 tokens): 4 (256 + 12288 + 64 (Dk + 2 Dv) + 2 Dk Dv)
  * bytes with D_k rounded up to a multiple of 16 and D_v to one of 32 (273 KiB at 128).
- * Errors: as kda_chunk_bwd; UNSUPPORTED if B*H*max(chunks, 8) exceeds 2^31 - 1.
+ * Errors: as kda_chunk_bwd; UNSUPPORTED if B*H*max(chunks, 16) exceeds 2^31 - 1.
  */
 kda_status_t kda_gdn_chunk_bwd_workspace_size(const kda_recurrent_bwd_args *args, size_t *bytes);
 

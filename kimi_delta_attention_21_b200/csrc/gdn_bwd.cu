@@ -40,10 +40,10 @@ constexpr int C = 64;       // tokens per chunk
 constexpr int LD = 136;     // pitch of [64 or 128][D] tiles in shared memory: 8 mod 32
 constexpr int LC = 72;      // pitch of [64][64] tiles
 constexpr int NT_P = 512;   // threads of the gradient kernel
-constexpr int NT_C = 512;   // threads of the chain kernel
-constexpr int VS = 32;      // value columns per chain CTA
-constexpr int LS = 34;      // chain pitch of the split [Dk][32] state: 2 mod 8 pairs (read in pairs of k)
-constexpr int LO = 36;      // and of plain [.][32] ones
+constexpr int NT_C = 256;   // threads of the chain kernel
+constexpr int VS = 16;      // value columns per chain CTA
+constexpr int LO = 20;      // chain pitch of [.][16] tiles read in pairs of k, and
+constexpr int LV = 24;      // of those read by single k: rows (pairs of rows) 8 banks apart
 
 __host__ __device__ inline int pad16(int x) { return (x + 15) & ~15; }
 __host__ __device__ inline int pad32(int x) { return (x + 31) & ~31; }
@@ -386,39 +386,36 @@ __global__ void __launch_bounds__(prep_nt<T>(), 512 / prep_nt<T>()) gb_prep_kern
 }
 
 // ---------------------------------------------------------------- the state and its gradient through the chunks
-// What a step reads of its chunk: e^G and e^D, W, K, U or M^T dO, and backwards Q^T (e^G dO).  Two sets: the next
-// chunk's arrive while this one's are used (fp32 keys leave room for one set of K only).
+// What a step reads of its chunk: e^G and e^D, W, K, U or M^T dO, and backwards Q^T (e^G dO).  A step is two products,
+// one with W and one with K; each of the two is replaced by the next chunk's while the other is used.
 template <typename T> struct Stage {
-    static constexpr int KEYS = sizeof(T) == 2 ? 2 : 1;
-    float *e, *W, *U, *H;
+    float *e, *U, *W, *H;  // e and U: two sets
     T *K;
-    __device__ Stage(float *base, int set) {
-        e = base + set * 2 * C;
-        W = base + 4 * C + set * C * LD;
-        U = base + 4 * C + 2 * C * LD + set * C * LO;
-        H = base + 4 * C + 2 * C * LD + 2 * C * LO + set * 128 * LO;
-        K = reinterpret_cast<T *>(base + FLOATS) + (KEYS == 2 ? set * C * LD : 0);
+    float *sY, *sV, *sS;  // the other half of a sum, V' and S (or their gradients)
+    __device__ explicit Stage(float *base) {
+        e = base;
+        U = e + 4 * C;
+        W = U + 2 * C * LO;
+        H = W + C * LD;
+        sY = H + 128 * LO;
+        sV = sY + C * LO;
+        sS = sV + C * LV;
+        K = reinterpret_cast<T *>(sS + 128 * LO);
     }
-    static constexpr int FLOATS = 4 * C + 2 * C * LD + 2 * C * LO + 2 * 128 * LO;
-    static constexpr size_t BYTES = FLOATS * sizeof(float) + KEYS * sizeof(T) * C * LD;
+    static constexpr int FLOATS = 4 * C + 2 * C * LO + C * LD + 128 * LO + C * LO + C * LV + 128 * LO;
 };
-template <typename T> constexpr size_t chain_smem() {
-    // the two sets, the other half of a sum, V' and S (or their gradients) split
-    return Stage<T>::BYTES + sizeof(float) * (C * LO + 2 * C * 36 + 2 * 128 * LS);
-}
+template <typename T> constexpr size_t chain_smem() { return Stage<T>::FLOATS * sizeof(float) + sizeof(T) * C * LD; }
 
-// 16 warps: [64][32] results as 4 x 2 tiles of 16 x 16, the sum over k shared by two groups of warps; [Dk][32] ones
-// as 8 x 2 tiles.  The operands that several warps read as B are kept split in shared memory.  The state, or its
-// gradient, stays in the accumulators of the warps that own it.  Products have accumulators of their own: the tensor
-// core truncates as it adds, the state is rounded once a chunk.
+// 8 warps: [64][16] results as 4 tiles of 16 x 16, the sum over k shared by two groups of warps; [Dk][16] ones as 8
+// tiles.  The state, or its gradient, stays in the accumulators of the warps that own it.  Products have accumulators of
+// their own: the tensor core truncates as it adds, the state is rounded once a chunk.
 struct Chain {
     const float *rec0;  // the records of this (b, h)
     Rec R;
     int Dkp, Dvp, j0;
     int64_t row0, rk;   // token rows of the (b, h)
-    int m0, n0;         // this warp's part of a [Dk][32] result
-    int r0, c0, half;   // this warp's part of a [64][32] result, and its half of the sum over the key channels:
-    int kh, kn;         // kn of them from kh
+    int m0, r0, half;   // this warp's rows of a [Dk][16] and of a [64][16] result; its half of the sum over the key
+    int kh, kn;         // channels: kn of them from kh
 };
 
 __device__ __forceinline__ Chain chain_of(const GbArgs &p, int64_t bh, int j0) {
@@ -432,100 +429,85 @@ __device__ __forceinline__ Chain chain_of(const GbArgs &p, int64_t bh, int j0) {
     const int64_t b = bh / p.H;
     c.row0 = b * p.S * p.H + (bh - b * p.H);
     c.rk = (int64_t)p.H * p.Dk;
-    c.m0 = 16 * (warp & 7);
-    c.n0 = 16 * (warp >> 3);
+    c.m0 = 16 * warp;
     c.r0 = 16 * (warp & 3);
-    c.c0 = 16 * ((warp >> 2) & 1);
-    c.half = warp >> 3;
+    c.half = warp >> 2;
     const int mid = (c.Dkp / 2 + 7) & ~7;
     c.kh = c.half ? mid : 0;
     c.kn = c.half ? c.Dkp - mid : mid;
     return c;
 }
 
-template <typename T>
-__device__ __forceinline__ void stage_keys(const GbArgs &p, const Chain &c, T *sK, int n) {
+// NT of the CTA's threads, t of them.
+template <int NT, typename T>
+__device__ __forceinline__ void stage_keys(const GbArgs &p, const Chain &c, T *sK, int n, int t) {
     const int64_t t0 = (int64_t)n * C;
-    stage_rows<T, NT_C / 2>(sK, (const T *)p.k + (c.row0 + t0 * p.H) * p.Dk, c.rk, (int)min((int64_t)C, p.S - t0), p.Dk, c.Dkp,
-                            p.wide_k, threadIdx.x & (NT_C / 2 - 1));
-}
-
-// Two neighbouring values, split, as one 16-byte store (an even column).
-__device__ __forceinline__ void put_split(float2 *dst, float x, float y) {
-    const float2 a = tf32::split2(x), b = tf32::split2(y);
-    *reinterpret_cast<float4 *>(dst) = make_float4(a.x, a.y, b.x, b.y);
+    stage_rows<T, NT>(sK, (const T *)p.k + (c.row0 + t0 * p.H) * p.Dk, c.rk, (int)min((int64_t)C, p.S - t0), p.Dk, c.Dkp,
+                      p.wide_k, t);
 }
 
 // V' = U - W S,  S <- gamma S + K^T (e^D V').  FULL: D_k pads to 128.
 template <typename T, bool FULL>
 __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j0, float *sm) {
     constexpr bool EX = sizeof(T) == 2;
-    float *sY = sm + Stage<T>::BYTES / sizeof(float);
-    constexpr int LV = EX ? 34 : 36;  // K comes in pairs of k (2 mod 8 pairs) where it comes through ldmatrix
-    float2 *sVp = reinterpret_cast<float2 *>(sY + C * LO), *sS = sVp + C * 36;
+    constexpr int HT = NT_C / 2, lv = EX ? LO : LV;  // V' is read in pairs of k where K comes through ldmatrix
+    const Stage<T> g(sm);
     const Chain q = chain_of(p, bh, j0);
     const Rec &R = q.R;
-    const int m0 = q.m0, n0 = q.n0, r0 = q.r0, c0 = q.c0, Dkp = FULL ? 128 : q.Dkp, Dvp = q.Dvp;
+    const int m0 = q.m0, r0 = q.r0, Dkp = FULL ? 128 : q.Dkp, Dvp = q.Dvp;
     const bool own = FULL || m0 < Dkp, first = !q.half;
-    const int ht = threadIdx.x & (NT_C / 2 - 1);
-    auto stage = [&](const float *rec, int n) {  // by the second group of warps
-        const Stage<T> g(sm, n & 1);
-        stage_block<NT_C / 2, 32>(g.e, 2 * C, rec + R.eG, 2 * C, 1, 2 * C, ht);
-        stage_block<NT_C / 2, 32>(g.W, LD, rec + R.W, Dkp, C, Dkp, ht);
-        stage_block<NT_C / 2, 8>(g.U, LO, rec + R.V + j0, Dvp, C, VS, ht);
-        if (EX) stage_keys<T>(p, q, g.K, n);
-        cp_async_commit_group();
+    const int ht = threadIdx.x & (HT - 1);
+    auto stage = [&](const float *rec, int n) {  // W, U, e: by the second group of warps
+        stage_block<HT, 32>(g.e + (n & 1) * 2 * C, 2 * C, rec + R.eG, 2 * C, 1, 2 * C, ht);
+        stage_block<HT, 32>(g.W, LD, rec + R.W, Dkp, C, Dkp, ht);
+        stage_block<HT, 4>(g.U + (n & 1) * C * LO, LO, rec + R.V + j0, Dvp, C, VS, ht);
     };
     float S[1][2][4] = {};
     tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
         r += m0;
-        c += n0;
         if (r < p.Dk && j0 + c < p.Dv && p.S0) S[i][j][e] = p.S0[(bh * p.Dk + r) * p.Dv + j0 + c];
-        if (own) sS[r * LS + c] = tf32::split2(S[i][j][e]);
+        if (own) g.sS[r * LO + c] = S[i][j][e];
     });
     float *rec = const_cast<float *>(q.rec0);
     if (!first) stage(rec, 0);
+    cp_async_commit_group();
     for (int n = 0; n < p.Nc; ++n, rec += R.size) {
-        const Stage<T> g(sm, n & 1);
-        cp_async_wait<0>();  // this chunk's set
-        __syncthreads();
-        if (!EX && !first) {
-            stage_keys<T>(p, q, g.K, n);
-            cp_async_commit_group();
-        }
+        const float *e_ = g.e + (n & 1) * 2 * C, *U = g.U + (n & 1) * C * LO;
+        cp_async_wait<0>();  // W
+        __syncthreads();     // and S; the last chunk's K is read
+        stage_keys<NT_C>(p, q, g.K, n, threadIdx.x);
+        cp_async_commit_group();
         if (own)  // the state entering the chunk
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 if (!(e & 1))
-                    *reinterpret_cast<float2 *>(rec + R.S + (m0 + r) * Dvp + j0 + n0 + c) =
-                        make_float2(S[i][j][e], S[i][j][e + 1]);
+                    *reinterpret_cast<float2 *>(rec + R.S + (m0 + r) * Dvp + j0 + c) = make_float2(S[i][j][e], S[i][j][e + 1]);
             });
         float v[1][2][4] = {};
-        tf32::tile<1, 2, false, true, false, false, 2, 8>(v, g.W + r0 * LD + q.kh, LD, sS + c0 + q.kh * LS, LS,
-                                                             FULL ? C : q.kn);
-        if (!first)
-            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { sY[(r0 + r) * LO + c0 + c] = v[i][j][e]; });
-        if (!EX) cp_async_wait<0>();
-        __syncthreads();  // the other half of the sum
+        tf32::tile<1, 2, false, true, false, false, 1, 8>(v, g.W + r0 * LD + q.kh, LD, g.sS + q.kh * LO, LO, FULL ? C : q.kn);
+        if (!first) tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { g.sY[(r0 + r) * LO + c] = v[i][j][e]; });
+        __syncthreads();  // the other half of the sum; W is read
         if (first)
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 r += r0;
-                c += c0;
-                v[i][j][e] = g.U[r * LO + c] - (v[i][j][e] + sY[r * LO + c]);
+                v[i][j][e] = U[r * LO + c] - (v[i][j][e] + g.sY[r * LO + c]);
                 if (e & 1) {
-                    put_split(sVp + r * LV + c - 1, g.e[C + r] * v[i][j][e - 1], g.e[C + r] * v[i][j][e]);  // e^D V'
+                    *reinterpret_cast<float2 *>(g.sV + r * lv + c - 1) =  // e^D V'
+                        make_float2(e_[C + r] * v[i][j][e - 1], e_[C + r] * v[i][j][e]);
                     *reinterpret_cast<float2 *>(rec + R.V + r * Dvp + j0 + c - 1) = make_float2(v[i][j][e - 1], v[i][j][e]);
                 }
             });
-        else if (n + 1 < p.Nc)  // (the set was last read two steps ago)
+        else if (n + 1 < p.Nc)
             stage(rec + R.size, n + 1);
+        cp_async_commit_group();
+        cp_async_wait<1>();  // K
         __syncthreads();
         if (own) {
-            const float gamma = g.e[C - 1];
+            const float gamma = e_[C - 1];
             float add[1][2][4] = {};
-            tf32::tile<1, 2, true, true, EX, false, 2, 8>(add, g.K + m0, LD, sVp + n0, LV, C);
+            tf32::tile<1, 2, true, true, EX, false, 1, 8>(add, g.K + m0, LD, g.sV, lv, C);
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 S[i][j][e] = fmaf(gamma, S[i][j][e], add[i][j][e]);
-                if (e & 1) put_split(sS + (m0 + r) * LS + n0 + c - 1, S[i][j][e - 1], S[i][j][e]);
+                if (e & 1) *reinterpret_cast<float2 *>(g.sS + (m0 + r) * LO + c - 1) = make_float2(S[i][j][e - 1], S[i][j][e]);
             });
         }
     }
@@ -536,94 +518,84 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
 template <typename T, bool FULL>
 __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int j0, float *sm) {
     constexpr bool EX = sizeof(T) == 2;
-    float *sY = sm + Stage<T>::BYTES / sizeof(float);
-    constexpr int LV = 36;  // W is read by single k: 4 mod 16 pairs
-    float2 *sdV = reinterpret_cast<float2 *>(sY + C * LO), *sS = sdV + C * 36;
+    constexpr int HT = NT_C / 2;
+    const Stage<T> g(sm);
     const Chain q = chain_of(p, bh, j0);
     const Rec &R = q.R;
-    const int m0 = q.m0, n0 = q.n0, r0 = q.r0, c0 = q.c0, Dkp = FULL ? 128 : q.Dkp, Dvp = q.Dvp;
+    const int m0 = q.m0, r0 = q.r0, Dkp = FULL ? 128 : q.Dkp, Dvp = q.Dvp;
     const bool own = FULL || m0 < Dkp, first = !q.half;
-    const int ht = threadIdx.x & (NT_C / 2 - 1);
-    auto stage = [&](const float *rec, int n) {  // by the second group of warps
-        const Stage<T> g(sm, n & 1);
-        stage_block<NT_C / 2, 32>(g.e, 2 * C, rec + R.eG, 2 * C, 1, 2 * C, ht);
-        stage_block<NT_C / 2, 32>(g.W, LD, rec + R.W, Dkp, C, Dkp, ht);
-        stage_block<NT_C / 2, 8>(g.U, LO, rec + R.dV + j0, Dvp, C, VS, ht);
-        stage_block<NT_C / 2, 8>(g.H, LO, rec + R.dS + j0, Dvp, Dkp, VS, ht);
-        if (EX) stage_keys<T>(p, q, g.K, n);
-        cp_async_commit_group();
+    const int ht = threadIdx.x & (HT - 1);
+    auto stage = [&](const float *rec, int n) {  // K, M^T dO, e: by the second group of warps
+        stage_block<HT, 32>(g.e + (n & 1) * 2 * C, 2 * C, rec + R.eG, 2 * C, 1, 2 * C, ht);
+        stage_keys<HT>(p, q, g.K, n, ht);
+        stage_block<HT, 4>(g.U + (n & 1) * C * LO, LO, rec + R.dV + j0, Dvp, C, VS, ht);
     };
     float dS[1][2][4] = {};
     tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
         r += m0;
-        c += n0;
         if (r < p.Dk && j0 + c < p.Dv && p.dST) dS[i][j][e] = p.dST[(bh * p.Dk + r) * p.Dv + j0 + c];
-        if (own) sS[r * LS + c] = tf32::split2(dS[i][j][e]);
+        if (own) g.sS[r * LO + c] = dS[i][j][e];
     });
     float *rec = const_cast<float *>(q.rec0) + (int64_t)(p.Nc - 1) * R.size;
-    if (!first) {
-        if (!EX) stage_keys<T>(p, q, Stage<T>(sm, 0).K, p.Nc - 1);
-        stage(rec, p.Nc - 1);
-    }
+    if (!first) stage(rec, p.Nc - 1);
+    cp_async_commit_group();
     for (int n = p.Nc - 1; n >= 0; --n, rec -= R.size) {
-        const Stage<T> g(sm, n & 1);
-        cp_async_wait<0>();  // this chunk's set
-        __syncthreads();
-        if (own)  // the gradient of the state leaving the chunk
-            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
-                if (!(e & 1))
-                    *reinterpret_cast<float2 *>(rec + R.dS + (m0 + r) * Dvp + j0 + n0 + c) =
-                        make_float2(dS[i][j][e], dS[i][j][e + 1]);
-            });
+        const float *e_ = g.e + (n & 1) * 2 * C, *U = g.U + (n & 1) * C * LO;
+        cp_async_wait<0>();  // K
+        __syncthreads();     // and dS; the last chunk's W and H are read
+        stage_block<NT_C, 32>(g.W, LD, rec + R.W, Dkp, C, Dkp);
+        stage_block<NT_C, 4>(g.H, LO, rec + R.dS + j0, Dvp, Dkp, VS);
+        cp_async_commit_group();
         float x[1][2][4] = {};
-        tf32::tile<1, 2, false, true, EX, false, 2, 8>(x, g.K + r0 * LD + q.kh, LD, sS + c0 + q.kh * LS, LS,
-                                                          FULL ? C : q.kn);
-        if (!first)
-            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { sY[(r0 + r) * LO + c0 + c] = x[i][j][e]; });
+        tf32::tile<1, 2, false, true, EX, false, 1, 8>(x, g.K + r0 * LD + q.kh, LD, g.sS + q.kh * LO, LO, FULL ? C : q.kn);
+        if (!first) tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { g.sY[(r0 + r) * LO + c] = x[i][j][e]; });
         __syncthreads();  // the other half of the sum; K is read
         if (first)
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 r += r0;
-                c += c0;
-                x[i][j][e] = fmaf(g.e[C + r], x[i][j][e] + sY[r * LO + c], g.U[r * LO + c]);
+                x[i][j][e] = fmaf(e_[C + r], x[i][j][e] + g.sY[r * LO + c], U[r * LO + c]);
                 if (e & 1) {
-                    put_split(sdV + r * LV + c - 1, -x[i][j][e - 1], -x[i][j][e]);
+                    *reinterpret_cast<float2 *>(g.sV + r * LV + c - 1) = make_float2(-x[i][j][e - 1], -x[i][j][e]);
                     *reinterpret_cast<float2 *>(rec + R.dV + r * Dvp + j0 + c - 1) = make_float2(x[i][j][e - 1], x[i][j][e]);
                 }
             });
-        else if (n > 0) {  // (the set was last read two steps ago, a single K just now)
-            if (!EX) stage_keys<T>(p, q, g.K, n - 1);
+        else if (n > 0)
             stage(rec - R.size, n - 1);
-        }
+        cp_async_commit_group();
+        cp_async_wait<1>();  // W and H
         __syncthreads();
         if (own) {
-            const float gamma = g.e[C - 1];
+            tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {  // the gradient of the state leaving the chunk
+                if (!(e & 1))
+                    *reinterpret_cast<float2 *>(rec + R.dS + (m0 + r) * Dvp + j0 + c) = make_float2(dS[i][j][e], dS[i][j][e + 1]);
+            });
+            const float gamma = e_[C - 1];
             float sub[1][2][4] = {};
-            tf32::tile<1, 2, true, true, false, false, 2, 8>(sub, g.W + m0, LD, sdV + n0, LV, C);
+            tf32::tile<1, 2, true, true, false, false, 1, 8>(sub, g.W + m0, LD, g.sV, LV, C);
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
-                dS[i][j][e] = fmaf(gamma, dS[i][j][e], g.H[(m0 + r) * LO + n0 + c] + sub[i][j][e]);
-                if (e & 1) put_split(sS + (m0 + r) * LS + n0 + c - 1, dS[i][j][e - 1], dS[i][j][e]);
+                dS[i][j][e] = fmaf(gamma, dS[i][j][e], g.H[(m0 + r) * LO + c] + sub[i][j][e]);
+                if (e & 1) *reinterpret_cast<float2 *>(g.sS + (m0 + r) * LO + c - 1) = make_float2(dS[i][j][e - 1], dS[i][j][e]);
             });
         }
     }
     if (p.dS0 && in_bounds(p.dS0 + bh * p.Dk * p.Dv, (size_t)p.Dk * p.Dv * 4, p.dS0, p.ns_bytes, p.bounds))
         tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
             r += m0;
-            c += n0;
             if (r < p.Dk && j0 + c < p.Dv) p.dS0[(bh * p.Dk + r) * p.Dv + j0 + c] = dS[i][j][e];
         });
 }
 
 template <typename T, bool FULL>
-__global__ void __launch_bounds__(NT_C, 1) gb_chain_kernel(const __grid_constant__ GbArgs p) {
+__global__ void __launch_bounds__(NT_C, 2) gb_chain_kernel(const __grid_constant__ GbArgs p) {
     extern __shared__ __align__(16) uint8_t gb_sm[];
-    const int64_t job = blockIdx.x >> 1, bh = job / p.nslice;
+    // the backward ones first: they take longer, and an SM then holds one of each (16 heads: 228 us, alternating 244)
+    const int64_t half = gridDim.x >> 1, job = blockIdx.x < half ? blockIdx.x : blockIdx.x - half, bh = job / p.nslice;
     const int j0 = (int)(job - bh * p.nslice) * VS;
     const Rec R = make_rec(p.Dk, p.Dv);
     if (!in_bounds(p.ws + bh * p.Nc * R.size, (size_t)p.Nc * R.size * 4, p.ws, p.ws_bytes, p.bounds)) return;
     float *sm = reinterpret_cast<float *>(gb_sm);
-    if (blockIdx.x & 1) chain_forward<T, FULL>(p, bh, j0, sm);
-    else chain_backward<T, FULL>(p, bh, j0, sm);
+    if (blockIdx.x < half) chain_backward<T, FULL>(p, bh, j0, sm);
+    else chain_forward<T, FULL>(p, bh, j0, sm);
 }
 
 // ---------------------------------------------------------------- per chunk: the gradients
@@ -958,10 +930,10 @@ kda_status_t gb_validate(const kda_recurrent_bwd_args *a) {
                     a->H, a->D_k, a->D_v);
     if (a->D_k > 128 || a->D_v > 128)
         return fail(KDA_ERR_UNSUPPORTED, "D_k and D_v must be <= 128 (got %d, %d)", a->D_k, a->D_v);
-    // one CTA per (b, h, chunk), and two per (b, h, 32 value columns)
-    const int64_t nc = a->S / C + (a->S % C != 0), most = nc > 8 ? nc : 8;
+    // one CTA per (b, h, chunk), and two per (b, h, 16 value columns)
+    const int64_t nc = a->S / C + (a->S % C != 0), most = nc > 16 ? nc : 16;
     if (a->B > 0 && (a->B > 0x7fffffffLL / a->H || a->B * a->H > 0x7fffffffLL / most))
-        return fail(KDA_ERR_UNSUPPORTED, "gdn backward: B*H*max(chunks, 8) exceeds 2^31 - 1");
+        return fail(KDA_ERR_UNSUPPORTED, "gdn backward: B*H*max(chunks, 16) exceeds 2^31 - 1");
     return KDA_OK;
 }
 
