@@ -56,6 +56,15 @@ def test_quantises(K, N, Kd, rows, dtype):
     assert torch.equal(x8.float(), (x.float() / s).to(E4M3).float())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N,Kd,off", [(37, 1001, 0), (9, 130, 0), (64, 256, 1), (5000, 264, 0)])
+def test_quantises_rows_of_any_alignment(K, N, Kd, off, dtype):
+    x = randn(gen(Kd), N * Kd + off, dtype=dtype)[off:].view(N, Kd)
+    x8, sc = K.quant_fp8(x)
+    check_quantised(x, x8, sc, 1, 0.0)
+    assert torch.equal(x8.float(), (x.float() / spread(sc, 1, N, Kd)).to(E4M3).float())
+
+
 def test_blocks_of_zeros_and_non_finite(K):
     x = torch.zeros(4, 300, device="cuda")
     x[1, 5], x[1, 6] = float("nan"), 2.0
