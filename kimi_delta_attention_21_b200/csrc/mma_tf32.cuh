@@ -4,7 +4,8 @@
 // A tf32 operand has 11 significant bits.  An fp32 value x is split into hi = x rounded to tf32 and
 // lo = x - hi (exact), and a product becomes hi hi' + hi lo' + lo hi': what is left out is below 2^-21 of
 // the product.  An operand that tf32 holds exactly (bf16 values) has no lo, and its products are one (both
-// exact) or two instructions.  Accumulation is fp32.
+// exact) or two instructions.  Accumulation is fp32.  Measured: 8 clocks an instruction on a sub-partition (288 TFLOP/s
+// on 148 SMs at 1.9 GHz), 9 to 12 in the loops below, where splitting and the reads from shared memory take issue slots.
 #pragma once
 
 #include "kda_internal.cuh"

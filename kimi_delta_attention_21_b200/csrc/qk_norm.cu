@@ -8,7 +8,10 @@
 //   dx = r (h - x r^2 s sum(h x)).
 // r is recomputed from x, so the backward needs nothing kept from the forward.
 //
-// Both are bound by HBM: a row is read once and written once, every intermediate stays in registers.
+// Both are bound by HBM: a row is read once and written once, every intermediate stays in registers.  Measured (bf16,
+// heads of 128): forward, 4096 tokens x 32 heads, 12 us (10 at the copy rate); backward, 16384 tokens x 64 heads with
+// fp32 gradients, 195 us (164): rows in flight do not bound it (a shared-memory ring of any depth: 241 us), but the
+// row's two sums, and the angles of a token, which cost as much as three rows.
 // A group of G lanes holds one row, 16 bytes of input per lane and register vector, so that a warp's
 // loads are whole rows; the pairs of a half-split rotation are 16-byte vectors apart and meet by a
 // shuffle.  A group takes `hc` heads of one token in turn: the token's cosines and sines are computed
@@ -112,6 +115,21 @@ template <int VEC, int G, int NV, int ROT>
 __device__ __forceinline__ void qn_phases(const QnArgs &p, int64_t pos, int lane, float (&cs)[NV][VEC],
                                           float (&sn)[NV][VEC]) {
     const int half = p.R >> 1;
+    if (ROT == ROT_HALF && NV == 1 && p.R == G * VEC) {  // lanes j and j + G / 2 have the same angles: each makes half
+        const bool second = lane >= G / 2;               // of them (backward of 16384 tokens: 198 -> 195 us)
+        const int j0 = (lane & (G / 2 - 1)) * VEC + (second ? VEC / 2 : 0);
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) {
+            float c, s;
+            qn_angle(pos, p.inv[j0 + e], c, s);
+            const float oc = __shfl_xor_sync(0xffffffffu, c, G / 2), os = __shfl_xor_sync(0xffffffffu, s, G / 2);
+            cs[0][e] = second ? oc : c;
+            sn[0][e] = second ? os : -s;
+            cs[0][e + VEC / 2] = second ? c : oc;
+            sn[0][e + VEC / 2] = second ? s : -os;
+        }
+        return;
+    }
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll

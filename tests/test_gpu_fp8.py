@@ -105,6 +105,36 @@ def test_norm_gate_writes_stay_inside(K):
         assert torch.equal(g8.t, x8.view(torch.uint8)) and torch.equal(gs.t, sc)
 
 
+def test_quantiser_and_projection_writes_stay_inside(K):
+    lib, st = K.load_library(), torch.cuda.current_stream().cuda_stream
+    for N, Kd, rows in ((5, 264, 1), (7, 130, 1), (131, 264, 128), (131, 130, 128)):
+        x = randn(gen(Kd), N, Kd, dtype=BF16)
+        g8, gs = Guarded((N, Kd), torch.uint8), Guarded((-(-N // rows), -(-Kd // 128)), F32)
+        assert lib.kda_quant_fp8(x.data_ptr(), 1, N, Kd, rows, g8.t.data_ptr(), gs.t.data_ptr(), st) == 0
+        g8.check("x8")
+        gs.check("scales")
+    for N, Kd, M in ((5, 256, 67), (300, 512, 2000), (2600, 256, 2048), (9, 130, 70)):
+        x, xs, w, ws = operands(N, Kd, M)
+        y = Guarded((N, M), BF16)
+        assert lib.kda_out_proj_fp8(x.data_ptr(), xs.data_ptr(), w.data_ptr(), ws.data_ptr(), N, Kd, M, y.t.data_ptr(), 1,
+                                    st) == 0
+        y.check("y")
+        assert torch.equal(y.t, K.out_proj_fp8(x, xs, w, ws))
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quotients_at_extreme_scales(K, rows):
+    """Scales from the smallest normal value to the largest: the value is the nearest to IEEE's quotient at all of them."""
+    e = torch.arange(-140, 127, device="cuda", dtype=F32)
+    top = torch.exp2(e).repeat_interleave(rows)
+    x = torch.rand((top.numel(), 128), generator=gen(7), device="cuda") * 2 - 1
+    x[::rows, 0] = 1.0
+    x = x * top[:, None]
+    x8, sc = K.quant_fp8(x, rows)
+    s = spread(sc, rows, *x.shape)
+    assert torch.equal(x8.float(), (x / s).to(E4M3).float())
+
+
 def operands(N, Kd, M, seed=0):
     """e4m3 operands whose scales differ from block to block by powers of ten."""
     g = gen(seed)
