@@ -290,24 +290,24 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_vec_kernel(const T *__restr
     }
 }
 
-// D_v a multiple of the vector that is no power of two: heads straddle the blocks.  A CTA per token keeps the token's
-// vectors in registers (K <= 256 NG8_V vectors): their sums of squares meet in shared memory, a thread per head adds
-// them up, then the blocks (128 / VEC neighbouring lanes) are quantised.
+// D_v a multiple of the vector that is no power of two: heads straddle the blocks.  A CTA of NT threads per token keeps
+// the token's vectors in registers (K <= NT NG8_V vectors): their sums of squares meet in shared memory, a thread per
+// head adds them up, then the blocks (128 / VEC neighbouring lanes) are quantised.
 constexpr int NG8_V = 4;
-template <typename T>
-__global__ void __launch_bounds__(256) norm_gate_fp8_row_kernel(const T *__restrict__ o, const T *__restrict__ gate, int H,
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) norm_gate_fp8_row_kernel(const T *__restrict__ o, const T *__restrict__ gate, int H,
                                                                 int Dv, float eps, uint8_t *__restrict__ out,
                                                                 float *__restrict__ scales) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
     constexpr int VEC = Q8Vec<T>::N, G = 128 / VEC;
-    __shared__ float s_ss[256 * NG8_V], s_inv[256 * NG8_V];  // per vector; per head (a head has one vector at least)
+    __shared__ float s_ss[NT * NG8_V], s_inv[NT * NG8_V];  // per vector; per head (a head has one vector at least)
     const int K = H * Dv, nv = K / VEC, per = Dv / VEC, nb = (K + 127) / 128;
     const int64_t base = (int64_t)blockIdx.x * K;
     uint4 ov[NG8_V], gv[NG8_V];
 #pragma unroll
     for (int u = 0; u < NG8_V; ++u) {
-        const int i = threadIdx.x + 256 * u;
+        const int i = threadIdx.x + NT * u;
         ov[u] = gv[u] = make_uint4(0, 0, 0, 0);
         if (i < nv) {
             ov[u] = __ldcs(reinterpret_cast<const uint4 *>(o + base + i * VEC));
@@ -320,10 +320,10 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_row_kernel(const T *__restr
         Q8Vec<T>::unpack(ov[u], f);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) ss = fmaf(f[e], f[e], ss);
-        s_ss[threadIdx.x + 256 * u] = ss;
+        s_ss[threadIdx.x + NT * u] = ss;
     }
     __syncthreads();
-    for (int h = threadIdx.x; h < H; h += 256) {
+    for (int h = threadIdx.x; h < H; h += NT) {
         float ss = 0.f;
         for (int i = 0; i < per; ++i) ss += s_ss[h * per + i];
         s_inv[h] = rsqrtf(fmaf(ss, 1.0f / (float)Dv, eps));
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_row_kernel(const T *__restr
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < NG8_V; ++u) {
-        const int i = threadIdx.x + 256 * u;
+        const int i = threadIdx.x + NT * u;
         if (i - (int)(threadIdx.x & 31) >= nv) break;  // (the whole warp)
         const bool in = i < nv;
         const float inv = in ? s_inv[i / per] : 0.f;
@@ -344,12 +344,10 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_row_kernel(const T *__restr
             amax = fmaxf(amax, fabsf(f[e]));
         }
         const float s = q8_scale(group_max<G>(amax)), r = 1.0f / s;
-        uint32_t w[VEC / 4];
 #pragma unroll
-        for (int e = 0; e < VEC; e += 4) w[e / 4] = q8_pack4(f[e] * r, f[e + 1] * r, f[e + 2] * r, f[e + 3] * r);
+        for (int e = 0; e < VEC; ++e) f[e] *= r;
         if (in) {
-            if (VEC == 8) *reinterpret_cast<uint2 *>(out + base + i * VEC) = make_uint2(w[0], w[VEC / 4 - 1]);
-            else *reinterpret_cast<uint32_t *>(out + base + i * VEC) = w[0];
+            put8<VEC>(out + base + i * VEC, f);
             if (i % G == 0) scales[(int64_t)blockIdx.x * nb + i / G] = s;
         }
     }
@@ -406,9 +404,15 @@ cudaError_t ng8_launch(const void *o, const void *gl, int64_t N, int H, int Dv, 
             return launch_pdl(K % 128 ? norm_gate_fp8_vec_kernel<T, false> : norm_gate_fp8_vec_kernel<T, true>, dim3((unsigned)ctas), dim3(256), 0, st, (const T *)o,
                               (const T *)gl, N, K, nb, Dv / VEC, 1.0f / (float)Dv, eps, (uint8_t *)x8, scales);
     }
-    if (Dv % VEC == 0 && K / VEC <= 256 * NG8_V && aligned_to(o, 16) && aligned_to(gl, 16) && aligned_to(x8, VEC))
-        return launch_pdl(norm_gate_fp8_row_kernel<T>, dim3((unsigned)N), dim3(256), 0, st, (const T *)o, (const T *)gl, H, Dv,
-                          eps, (uint8_t *)x8, scales);
+    if (Dv % VEC == 0 && K / VEC <= 256 * NG8_V && aligned_to(o, 16) && aligned_to(gl, 16) && aligned_to(x8, VEC)) {
+        // the fewest threads that hold the token: 9109 tokens x 4 heads of 80 take 37 us with 256, 12 us with 64
+        const int nv = K / VEC, nt = nv <= 64 * NG8_V ? 64 : nv <= 128 * NG8_V ? 128 : 256;
+        const auto kernel = nt == 64    ? norm_gate_fp8_row_kernel<T, 64>
+                            : nt == 128 ? norm_gate_fp8_row_kernel<T, 128>
+                                        : norm_gate_fp8_row_kernel<T, 256>;
+        return launch_pdl(kernel, dim3((unsigned)N), dim3(nt), 0, st, (const T *)o, (const T *)gl, H, Dv, eps,
+                          (uint8_t *)x8, scales);
+    }
     return launch_pdl(norm_gate_fp8_kernel<T>, dim3((unsigned)N), dim3(256), (size_t)H * 4, st, (const T *)o,
                       (const T *)gl, H, Dv, eps, (uint8_t *)x8, scales);
 }
