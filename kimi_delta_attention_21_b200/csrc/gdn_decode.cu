@@ -8,7 +8,7 @@
 // (sequence, head): lane l of warp w owns the key rows w, w + 8, ... and four value columns, so that a
 // warp reads whole rows; the sums over key rows are partial sums of 8 warps joined in shared memory, one
 // barrier each (the buffers alternate, so the next token's sums need no second one).
-// Measured (bf16, D = 128, 32 heads): 256 sequences 183 us, 5.9 TB/s (90% of a copy's rate; a plain in-place
+// Measured (bf16, D = 128, 32 heads): 256 sequences 181 us, 6.0 TB/s (91% of a copy's rate; a plain in-place
 // update of as many bytes takes 159 us); with three CTAs on an SM instead of two it spills (233 us), with plain
 // stores instead of streaming ones 218 us.  One sequence: 5 us, the call's own time.
 #include "host_check.cuh"
@@ -41,7 +41,7 @@ template <typename T, bool VEC, bool FULL>
 __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constant__ GdArgs p) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
-    __shared__ float s_q[2][GD_MAXD], s_k[2][GD_MAXD];
+    __shared__ __align__(16) float s_q[2][GD_MAXD], s_k[2][GD_MAXD];
     __shared__ __align__(16) float s_red[2][2][GD_NW][GD_MAXD];
     const int Dk = FULL ? GD_MAXD : p.Dk, Dv = FULL ? GD_MAXD : p.Dv;
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31;
@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
         return;
     }
     float *S = p.state + (slot * p.H + h) * (int64_t)Dk * Dv;
+    auto row = [&](int i) { return w + GD_NW * i; };
     auto col = [&](int j) { return VEC ? 4 * l + j : l + 32 * j; };
     const int64_t tok0 = b * p.T * p.H + h;  // (token, head) index of token 0; p.H further for each token
     auto fetch = [&](int t) {                // this thread's element of token t's q (threads < 128) or k
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
     float s[GD_RPW][4];
 #pragma unroll
     for (int i = 0; i < GD_RPW; ++i) {
-        const int c = w + GD_NW * i;
+        const int c = row(i);
         if (VEC) {
             const float4 t = FULL || (c < Dk && 4 * l < Dv) ? __ldcs(reinterpret_cast<const float4 *>(S + c * Dv + 4 * l))
                                                             : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
     for (int t = 0; t < p.T; ++t) {
         const int64_t th = tok0 + (int64_t)t * p.H;
         const int buf = t & 1;
-        (tid < 128 ? s_q : s_k)[buf][tid & 127] = pre;
+        (tid < 128 ? s_q : s_k)[buf][GD_RPW * (tid & 7) + ((tid & 127) >> 3)] = pre;  // a warp's rows side by side
         float v[4], gt[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -116,45 +117,55 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
         const float a = expf(p.log_decay ? clamp_log_decay(now.log_decay, p.g_min) : log_alpha_of((float)now.z, p.g_min));
         if (t + 1 < p.T) pre = fetch(t + 1);
         __syncthreads();  // q and k of token t
+        // q . k first, in every warp, although one needs it: behind the products it costs T = 1 11% (203 us, so 181)
         float qk = 0.f, pp[4] = {0.f, 0.f, 0.f, 0.f}, qs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 4; ++j) qk = fmaf(s_q[buf][l + 32 * j], s_k[buf][l + 32 * j], qk);
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) qk += __shfl_xor_sync(0xffffffffu, qk, m);
 #pragma unroll
-        for (int i = 0; i < GD_RPW; ++i) {
-            const int c = w + GD_NW * i;
-            const float kc = s_k[buf][c], qc = s_q[buf][c];
+        for (int ii = 0; ii < GD_RPW; ii += 4) {
+            const float4 k4 = *reinterpret_cast<const float4 *>(&s_k[buf][GD_RPW * w + ii]);
+            const float4 q4 = *reinterpret_cast<const float4 *>(&s_q[buf][GD_RPW * w + ii]);
+            const float kc[4] = {k4.x, k4.y, k4.z, k4.w}, qc[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s[i][j] *= a;
-                pp[j] = fmaf(kc, s[i][j], pp[j]);
-                qs[j] = fmaf(qc, s[i][j], qs[j]);
-            }
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[ii + i][j] *= a;
+                    pp[j] = fmaf(kc[i], s[ii + i][j], pp[j]);
+                    qs[j] = fmaf(qc[i], s[ii + i][j], qs[j]);
+                }
         }
         *reinterpret_cast<float4 *>(&s_red[buf][0][w][4 * l]) = make_float4(pp[0], pp[1], pp[2], pp[3]);
         *reinterpret_cast<float4 *>(&s_red[buf][1][w][4 * l]) = make_float4(qs[0], qs[1], qs[2], qs[3]);
         __syncthreads();  // the partial sums
-        float r[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
+        float r[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < GD_NW; ++u) {
             const float4 x = *reinterpret_cast<const float4 *>(&s_red[buf][0][u][4 * l]);
-            const float4 y = *reinterpret_cast<const float4 *>(&s_red[buf][1][u][4 * l]);
             r[0] += x.x; r[1] += x.y; r[2] += x.z; r[3] += x.w;
-            o[0] += y.x; o[1] += y.y; o[2] += y.z; o[3] += y.w;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            r[j] = bt * (v[j] - r[j]);
-            o[j] = fmaf(qk, r[j], o[j]);
-        }
+        for (int j = 0; j < 4; ++j) r[j] = bt * (v[j] - r[j]);
 #pragma unroll
-        for (int i = 0; i < GD_RPW; ++i) {
-            const float kc = s_k[buf][w + GD_NW * i];
+        for (int ii = 0; ii < GD_RPW; ii += 4) {
+            const float4 k4 = *reinterpret_cast<const float4 *>(&s_k[buf][GD_RPW * w + ii]);
+            const float kc[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = fmaf(kc, r[j], s[i][j]);
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[ii + i][j] = fmaf(kc[i], r[j], s[ii + i][j]);
         }
-        if (w == (t & 7)) {
+        if (w == (t & 7)) {  // one warp has the outputs of this token, another those of the next
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < GD_NW; ++u) {
+                const float4 y = *reinterpret_cast<const float4 *>(&s_red[buf][1][u][4 * l]);
+                o[0] += y.x; o[1] += y.y; o[2] += y.z; o[3] += y.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = fmaf(qk, r[j], o[j]);
             if (p.gate) {
                 float ss = 0.f;
 #pragma unroll
@@ -174,7 +185,7 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
     if (!in_bounds(S, (size_t)Dk * Dv * 4, p.state, p.state_bytes, p.bounds)) return;
 #pragma unroll
     for (int i = 0; i < GD_RPW; ++i) {
-        const int c = w + GD_NW * i;
+        const int c = row(i);
         if (VEC) {
             if (FULL || (c < Dk && 4 * l < Dv))
                 __stcs(reinterpret_cast<float4 *>(S + c * Dv + 4 * l), make_float4(s[i][0], s[i][1], s[i][2], s[i][3]));
