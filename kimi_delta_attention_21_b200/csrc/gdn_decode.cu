@@ -19,7 +19,7 @@ namespace kda {
 
 namespace {
 
-constexpr int GD_NW = 8, GD_RPW = 16, GD_MAXD = 128;
+constexpr int GD_NW = 8, GD_MAXD = 128;
 
 struct GdArgs {
     int64_t slots_n;
@@ -37,8 +37,10 @@ struct GdArgs {
 
 // VEC: D_v is a multiple of 4 and the state 16-byte aligned; lane l owns columns 4l .. 4l + 3.  Otherwise the columns
 // l, l + 32, l + 64, l + 96.  FULL: D_k = D_v = 128 besides, nothing to mask.
-template <typename T, bool VEC, bool FULL>
-__global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constant__ GdArgs p) {
+// RPW: rows per warp, D_k <= 8 RPW; the fewer, the more CTAs on an SM (4096 sequences x 16 heads of 16: 756 us with 16
+// rows, 323 us with 4).
+template <typename T, bool VEC, bool FULL, int RPW>
+__global__ void __launch_bounds__(256, RPW == 16 ? 2 : RPW == 8 ? 3 : 4) gdn_decode_kernel(const __grid_constant__ GdArgs p) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
     __shared__ __align__(16) float s_q[2][GD_MAXD], s_k[2][GD_MAXD];
@@ -82,9 +84,9 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
     };
     float pre = fetch(0);  // ahead of the state: behind it they would wait for all of it (203 -> 183 us at 256 x 32)
     Token now = token(0);
-    float s[GD_RPW][4];
+    float s[RPW][4];
 #pragma unroll
-    for (int i = 0; i < GD_RPW; ++i) {
+    for (int i = 0; i < RPW; ++i) {
         const int c = row(i);
         if (VEC) {
             const float4 t = FULL || (c < Dk && 4 * l < Dv) ? __ldcs(reinterpret_cast<const float4 *>(S + c * Dv + 4 * l))
@@ -106,7 +108,8 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
     for (int t = 0; t < p.T; ++t) {
         const int64_t th = tok0 + (int64_t)t * p.H;
         const int buf = t & 1;
-        (tid < 128 ? s_q : s_k)[buf][GD_RPW * (tid & 7) + ((tid & 127) >> 3)] = pre;  // a warp's rows side by side
+        if (RPW == 16 || (tid & 127) < GD_NW * RPW)  // a warp's rows side by side
+            (tid < 128 ? s_q : s_k)[buf][RPW * (tid & 7) + ((tid & 127) >> 3)] = pre;
         float v[4], gt[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -120,13 +123,13 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
         // q . k first, in every warp, although one needs it: behind the products it costs T = 1 11% (203 us, so 181)
         float qk = 0.f, pp[4] = {0.f, 0.f, 0.f, 0.f}, qs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) qk = fmaf(s_q[buf][l + 32 * j], s_k[buf][l + 32 * j], qk);
+        for (int j = 0; j < RPW / 4; ++j) qk = fmaf(s_q[buf][l + 32 * j], s_k[buf][l + 32 * j], qk);
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) qk += __shfl_xor_sync(0xffffffffu, qk, m);
 #pragma unroll
-        for (int ii = 0; ii < GD_RPW; ii += 4) {
-            const float4 k4 = *reinterpret_cast<const float4 *>(&s_k[buf][GD_RPW * w + ii]);
-            const float4 q4 = *reinterpret_cast<const float4 *>(&s_q[buf][GD_RPW * w + ii]);
+        for (int ii = 0; ii < RPW; ii += 4) {
+            const float4 k4 = *reinterpret_cast<const float4 *>(&s_k[buf][RPW * w + ii]);
+            const float4 q4 = *reinterpret_cast<const float4 *>(&s_q[buf][RPW * w + ii]);
             const float kc[4] = {k4.x, k4.y, k4.z, k4.w}, qc[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -149,8 +152,8 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
 #pragma unroll
         for (int j = 0; j < 4; ++j) r[j] = bt * (v[j] - r[j]);
 #pragma unroll
-        for (int ii = 0; ii < GD_RPW; ii += 4) {
-            const float4 k4 = *reinterpret_cast<const float4 *>(&s_k[buf][GD_RPW * w + ii]);
+        for (int ii = 0; ii < RPW; ii += 4) {
+            const float4 k4 = *reinterpret_cast<const float4 *>(&s_k[buf][RPW * w + ii]);
             const float kc[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(256, 2) gdn_decode_kernel(const __grid_constan
     }
     if (!in_bounds(S, (size_t)Dk * Dv * 4, p.state, p.state_bytes, p.bounds)) return;
 #pragma unroll
-    for (int i = 0; i < GD_RPW; ++i) {
+    for (int i = 0; i < RPW; ++i) {
         const int c = row(i);
         if (VEC) {
             if (FULL || (c < Dk && 4 * l < Dv))
@@ -201,10 +204,11 @@ template <typename T>
 cudaError_t gd_launch(const kda_gdn_decode_args &a, const GdArgs &p, cudaStream_t st) {
     const dim3 grid((unsigned)(a.B * a.H));
     const bool vec = a.D_v % 4 == 0 && aligned_to(a.state, 16);
-    if (vec && a.D_k == GD_MAXD && a.D_v == GD_MAXD)
-        return launch_pdl(gdn_decode_kernel<T, true, true>, grid, dim3(256), 0, st, p);
-    if (vec) return launch_pdl(gdn_decode_kernel<T, true, false>, grid, dim3(256), 0, st, p);
-    return launch_pdl(gdn_decode_kernel<T, false, false>, grid, dim3(256), 0, st, p);
+    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, st, p); };
+    if (vec && a.D_k == GD_MAXD && a.D_v == GD_MAXD) return go(gdn_decode_kernel<T, true, true, 16>);
+    if (a.D_k <= 4 * GD_NW) return go(vec ? gdn_decode_kernel<T, true, false, 4> : gdn_decode_kernel<T, false, false, 4>);
+    if (a.D_k <= 8 * GD_NW) return go(vec ? gdn_decode_kernel<T, true, false, 8> : gdn_decode_kernel<T, false, false, 8>);
+    return go(vec ? gdn_decode_kernel<T, true, false, 16> : gdn_decode_kernel<T, false, false, 16>);
 }
 
 }  // namespace

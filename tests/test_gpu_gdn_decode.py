@@ -118,6 +118,12 @@ def test_slots_padding_and_bad_slots(K, T, D, dtype):
     assert int(status) == 0
 
 
+@pytest.mark.parametrize("Dk,Dv", [(32, 32), (33, 128), (16, 15), (64, 128), (65, 20), (8, 4), (31, 96), (63, 31)])
+@pytest.mark.parametrize("T,dtype", [(1, BF16), (5, F32)])
+def test_matches_the_recurrence_for_few_key_channels(K, T, Dk, Dv, dtype):
+    test_matches_the_recurrence(K, 9, T, 3, Dk, Dv, dtype, "z", -5.0, True)
+
+
 def test_tokens_at_once_equal_tokens_one_by_one(K):
     d, state0 = make(4, 6, 3, 128, 128, BF16, 4, "z", -3.0, True, seed=8)
     all_at_once, one = state0.clone(), state0.clone()
