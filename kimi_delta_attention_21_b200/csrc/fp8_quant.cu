@@ -4,8 +4,8 @@
 // The scale maps the block's largest magnitude to e4m3's largest, so nothing saturates.
 //
 // All are bound by HBM: each input is read once, the values leave as 1 byte each.  Measured: norm and gate, 8192 rows x
-// 32 heads of 128 in bf16, 38 us (26 at the copy rate); 65536 x 4096 values 146 us
-// (123), a 4096 x 4096 weight 13 us.
+// 32 heads of 128 in bf16, 40 us (26 at the copy rate; what it issues takes the SMs longer than the bytes); 65536 x 4096
+// values 146 us (123), a 4096 x 4096 weight 13 us.
 #include <cuda_fp8.h>
 
 #include "host_check.cuh"
@@ -35,8 +35,8 @@ __device__ __forceinline__ float group_max(float v) {
     for (int m = G / 2; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
     return v;
 }
-template <int G>
-__device__ __forceinline__ float group_sum(float v) {
+template <int G, typename AT>
+__device__ __forceinline__ AT group_sum(AT v) {
 #pragma unroll
     for (int m = G / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
     return v;
@@ -229,21 +229,31 @@ __global__ void __launch_bounds__(256) quant_tiles_kernel(const T *__restrict__ 
 }
 
 // ---------------------------------------------------------------- norm, gate and quantisation
-// sigmoid by the fast exponential and quotient: off by (2 + 1.2 |x|) units in the last place of fp32
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// sigmoid to 8 half-steps of fp32 for every x, without a division: with e = exp(-|x|) (4) and d = 1 + e (1), in [1, 2], it
+// is 1 / d (2), or e / d for a negative x (1).  (8192 x 32 heads of 128: 40 us; with 1 / (1 + exp(-x)) by division 61 us.)
+__device__ __forceinline__ float ng8_sigmoid(float x) {
+    const float e = expf(-fabsf(x));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return x < 0.f ? e * r : r;
+}
+
+// 1 / rms of a head from its sum of squares (fp32 inputs: an fp64 sum), inv_dv = 1 / D_v
+template <typename AT>
+__device__ __forceinline__ float ng8_inv(AT ss, AT inv_dv, float eps) { return rsqrtf((float)(ss * inv_dv + (AT)eps)); }
 
 // D_v = 8 (fp32: 4) .. 128, a power of two: a block of 128 channels holds whole heads.  A group of 128 / VEC
 // lanes per block, 16 bytes of o and of the gate per lane; `hl` lanes share a head's norm.  Four blocks per group
-// are in flight together.  2 * es + 1 bytes per channel pass HBM; about 30 instructions per channel would take the
-// SMs as long, which is why the sigmoid is the fast one and the division by the scale a product with its inverse.
+// are in flight together.
 // FLAT: K is a multiple of 128, so that the blocks follow one another without gaps (no division per block).
 template <typename T, bool FLAT>
 __global__ void __launch_bounds__(256) norm_gate_fp8_vec_kernel(const T *__restrict__ o, const T *__restrict__ gate,
-                                                                int64_t N, int K, int nb, int hl, float inv_dv,
-                                                                float eps, uint8_t *__restrict__ out,
-                                                                float *__restrict__ scales) {
+                                                                int64_t N, int K, int nb, int hl,
+                                                                typename AccT<T>::type inv_dv, float eps,
+                                                                uint8_t *__restrict__ out, float *__restrict__ scales) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
+    using AT = typename AccT<T>::type;
     constexpr int VEC = Q8Vec<T>::N, G = 128 / VEC, PER = 256 / G, U = 4;
     const int lane = threadIdx.x & (G - 1);
     const int64_t units = N * nb, u0 = (int64_t)blockIdx.x * (PER * U) + threadIdx.x / G;
@@ -270,19 +280,19 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_vec_kernel(const T *__restr
         float f[VEC], t[VEC];
         Q8Vec<T>::unpack(ov[u], f);
         Q8Vec<T>::unpack(gv[u], t);
-        float ss = 0.f, amax = 0.f;
+        AT ss = 0;
+        float amax = 0.f;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) ss = fmaf(f[e], f[e], ss);
+        for (int e = 0; e < VEC; ++e) ss += (AT)f[e] * (AT)f[e];
         for (int m = hl >> 1; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-        const float inv = rsqrtf(fmaf(ss, inv_dv, eps));
+        const float inv = in[u] ? ng8_inv(ss, inv_dv, eps) : 0.f;  // (infinite for an absent row with eps = 0)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            f[e] = in[u] ? f[e] * inv * sigmoid_fast(t[e]) : 0.f;  // (an absent row with eps = 0 would be NaN)
+            f[e] = f[e] * inv * ng8_sigmoid(t[e]);
             amax = fmaxf(amax, fabsf(f[e]));
         }
         const float s = q8_scale(group_max<G>(amax)), r = 1.0f / s;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) f[e] *= r;
+        divide<VEC>(f, s, r);
         if (in[u]) {
             put8<VEC>(out + at[u], f);
             if (lane == 0) scales[u0 + u * PER] = s;
@@ -300,8 +310,10 @@ __global__ void __launch_bounds__(NT) norm_gate_fp8_row_kernel(const T *__restri
                                                                 float *__restrict__ scales) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
+    using AT = typename AccT<T>::type;
     constexpr int VEC = Q8Vec<T>::N, G = 128 / VEC;
-    __shared__ float s_ss[NT * NG8_V], s_inv[NT * NG8_V];  // per vector; per head (a head has one vector at least)
+    __shared__ AT s_ss[NT * NG8_V];
+    __shared__ float s_inv[NT * NG8_V];  // per vector; per head (a head has one vector at least)
     const int K = H * Dv, nv = K / VEC, per = Dv / VEC, nb = (K + 127) / 128;
     const int64_t base = (int64_t)blockIdx.x * K;
     uint4 ov[NG8_V], gv[NG8_V];
@@ -316,17 +328,18 @@ __global__ void __launch_bounds__(NT) norm_gate_fp8_row_kernel(const T *__restri
     }
 #pragma unroll
     for (int u = 0; u < NG8_V; ++u) {
-        float f[VEC], ss = 0.f;
+        float f[VEC];
+        AT ss = 0;
         Q8Vec<T>::unpack(ov[u], f);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) ss = fmaf(f[e], f[e], ss);
+        for (int e = 0; e < VEC; ++e) ss += (AT)f[e] * (AT)f[e];
         s_ss[threadIdx.x + NT * u] = ss;
     }
     __syncthreads();
     for (int h = threadIdx.x; h < H; h += NT) {
-        float ss = 0.f;
+        AT ss = 0;
         for (int i = 0; i < per; ++i) ss += s_ss[h * per + i];
-        s_inv[h] = rsqrtf(fmaf(ss, 1.0f / (float)Dv, eps));
+        s_inv[h] = ng8_inv(ss, AT(1) / (AT)Dv, eps);
     }
     __syncthreads();
 #pragma unroll
@@ -340,12 +353,11 @@ __global__ void __launch_bounds__(NT) norm_gate_fp8_row_kernel(const T *__restri
         Q8Vec<T>::unpack(gv[u], t);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            f[e] = in ? f[e] * inv * sigmoid_fast(t[e]) : 0.f;
+            f[e] = f[e] * inv * ng8_sigmoid(t[e]);
             amax = fmaxf(amax, fabsf(f[e]));
         }
         const float s = q8_scale(group_max<G>(amax)), r = 1.0f / s;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) f[e] *= r;
+        divide<VEC>(f, s, r);
         if (in) {
             put8<VEC>(out + base + i * VEC, f);
             if (i % G == 0) scales[(int64_t)blockIdx.x * nb + i / G] = s;
@@ -360,18 +372,19 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_kernel(const T *__restrict_
                                                             float *__restrict__ scales) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
+    using AT = typename AccT<T>::type;
     extern __shared__ float s_inv[];
     const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int K = H * Dv, nb = (K + 127) / 128;
     const int64_t base = (int64_t)blockIdx.x * K;
     for (int h = w; h < H; h += 8) {
-        float ss = 0.f;
+        AT ss = 0;
         for (int j = l; j < Dv; j += 32) {
-            const float v = load_elem(o, base + (int64_t)h * Dv + j);
-            ss = fmaf(v, v, ss);
+            const AT v = load_elem(o, base + (int64_t)h * Dv + j);
+            ss += v * v;
         }
         ss = group_sum<32>(ss);
-        if (l == 0) s_inv[h] = 1.0f / sqrtf(ss / (float)Dv + eps);
+        if (l == 0) s_inv[h] = ng8_inv(ss, AT(1) / (AT)Dv, eps);
     }
     __syncthreads();
     for (int u = w; u < nb; u += 8) {
@@ -379,14 +392,14 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_kernel(const T *__restrict_
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = 128 * u + l + 32 * j;
-            f[j] = c < K ? load_elem(o, base + c) * s_inv[c / Dv] * sigmoid_fast(load_elem(gate, base + c)) : 0.f;
+            f[j] = c < K ? load_elem(o, base + c) * s_inv[c / Dv] * ng8_sigmoid(load_elem(gate, base + c)) : 0.f;
             amax = fmaxf(amax, fabsf(f[j]));
         }
-        const float s = q8_scale(group_max<32>(amax)), r = 1.0f / s;
+        const float s = q8_scale(group_max<32>(amax));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = 128 * u + l + 32 * j;
-            if (c < K) out[base + c] = q8_one(f[j] * r);
+            if (c < K) out[base + c] = q8_one(f[j] / s);
         }
         if (l == 0) scales[(int64_t)blockIdx.x * nb + u] = s;
     }
@@ -402,7 +415,7 @@ cudaError_t ng8_launch(const void *o, const void *gl, int64_t N, int H, int Dv, 
         const int64_t ctas = (N * nb + 8 * VEC - 1) / (8 * VEC);  // 256 threads: 2 VEC groups of four blocks
         if (ctas <= 0x7fffffffLL)
             return launch_pdl(K % 128 ? norm_gate_fp8_vec_kernel<T, false> : norm_gate_fp8_vec_kernel<T, true>, dim3((unsigned)ctas), dim3(256), 0, st, (const T *)o,
-                              (const T *)gl, N, K, nb, Dv / VEC, 1.0f / (float)Dv, eps, (uint8_t *)x8, scales);
+                              (const T *)gl, N, K, nb, Dv / VEC, typename AccT<T>::type(1) / Dv, eps, (uint8_t *)x8, scales);
     }
     if (Dv % VEC == 0 && K / VEC <= 256 * NG8_V && aligned_to(o, 16) && aligned_to(gl, 16) && aligned_to(x8, VEC)) {
         // the fewest threads that hold the token: 9109 tokens x 4 heads of 80 take 37 us with 256, 12 us with 64
