@@ -418,10 +418,13 @@ PyObject *gdn_chunk_bwd(PyObject *const *a) {
 int64_t blocks128(int64_t n) { return (n + 127) / 128; }
 
 PyObject *quant_fp8(PyObject *const *a) {  // x, block_rows
+    // the scales are sized by what the library gets: 32 bits, which 2^32 + 1 would leave as 1
+    const long wide = integer(a[1]);
+    const int32_t rows_per = (int32_t)wide;
+    if (rows_per != wide) refuse(PyExc_ValueError, "block_rows must be 1 or 128 (got " + std::to_string(wide) + ")");
     const at::Tensor &x = first(a[0], "x");
     const int device = x.get_device();
     const kda_dtype_t code = dtype_code(x, "x");
-    const long rows_per = integer(a[1]);
     if (x.dim() < 1 || (rows_per != 1 && x.dim() != 2))
         refuse(PyExc_ValueError, x.dim() < 1 ? "x must have at least one dimension" : "blocks of several rows need a matrix");
     const void *px = need(a[0], "x", device, x.scalar_type(), x.sizes());
@@ -432,7 +435,7 @@ PyObject *quant_fp8(PyObject *const *a) {  // x, block_rows
     const at::Tensor x8 = make(x.sizes(), at::kFloat8_e4m3fn, device), sc = make(shape, at::kFloat, device);
     void *st = stream_of(device);
     const kda_status_t s = call(device, [&] {
-        return F.quant_fp8(px, code, n, K, (int32_t)rows_per, x8.data_ptr(), (float *)sc.data_ptr(), st);
+        return F.quant_fp8(px, code, n, K, rows_per, x8.data_ptr(), (float *)sc.data_ptr(), st);
     });
     return s == KDA_OK ? tuple_of({x8, sc}) : PyLong_FromLong(s);
 }
