@@ -80,9 +80,12 @@ kda_status_t kda_device_timeouts(uint32_t *count, int reset);
  * found outside their buffer and skipped, on the current device, since the
  * last reset; reset != 0 clears it.  *checked_build (if not NULL) is set to 1
  * in a checked build, 0 otherwise (where the count stays 0).  The checks cover
- * every global write through an offset the library computes: workspace
- * records, segment maps and entering states, checkpoints and stashes, final
- * states and staged outputs.  Synchronous. */
+ * workspace records, segment maps and entering states, checkpoints and stashes,
+ * final states, staged outputs, and every output and workspace of the norms of
+ * queries and keys, the gated delta rule's decode step and gradients and the
+ * e4m3 path, but for stores through a TMA map, which clips them.  Not covered:
+ * what kda_gate, kda_norm_gate, kda_decode_step, the SIMT engine and the bf16
+ * and fp32 projections store.  Synchronous. */
 kda_status_t kda_device_bounds_errors(uint32_t *count, int reset, int *checked_build);
 
 /* Self-test of the bounded-wait path the tensor-core kernels use: launches a

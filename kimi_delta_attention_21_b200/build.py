@@ -5,10 +5,10 @@
 Each csrc/*.cu compiles to _build/<name>.o in parallel, then links into
 kimi_delta_attention_21_b200/libkda.so.  Objects are rebuilt when their source
 or any header changed.  --checked builds the bounds-checked variant
-(-DKDA_CHECKED) from _build_checked/ into libkda_checked.so: every global write
-through an offset the library computes is tested against its buffer and, if it
-would leave it, skipped and counted (kda_device_bounds_errors).  The binding
-loads it when KDA_LIBRARY names it.
+(-DKDA_CHECKED) from _build_checked/ into libkda_checked.so: the global writes
+that kda.h lists at kda_device_bounds_errors are tested against their buffers
+and, if they would leave them, skipped and counted.  The binding loads it when
+KDA_LIBRARY names it.
 
 csrc_py/marshal.cpp, the argument marshalling of the operators whose calls take
 microseconds, compiles with g++ against torch's headers into _marshal.so (the

@@ -3,6 +3,7 @@
 #include <stdarg.h>
 #include <atomic>
 #include <stdio.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include "host_check.cuh"
@@ -37,6 +38,16 @@ kda_status_t check_launch(const char *what) {
     if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
     return KDA_OK;
 }
+
+#ifdef KDA_CHECKED
+size_t checked_size(size_t n) {
+    static const size_t shrink = [] {
+        const char *s = getenv("KDA_CHECKED_SHRINK");
+        return s ? (size_t)strtoull(s, nullptr, 10) : (size_t)0;
+    }();
+    return n > shrink ? n - shrink : 0;
+}
+#endif
 
 // gdn: the scalar-decay (Gated DeltaNet) entry points, whose z / log_decay are (B, S, H).
 static kda_status_t chunk_validate(const kda_chunk_args *a, int *chunk_out, bool *use_tc, bool gdn) {

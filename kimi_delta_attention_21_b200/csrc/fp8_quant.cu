@@ -16,6 +16,15 @@ namespace kda {
 
 namespace {
 
+// What the checked build holds the stores against: bytes of the values and of the scales, and the counter.
+struct Q8Size {
+    size_t v, s;
+    unsigned int *bounds;
+};
+__device__ __forceinline__ void put_scale(float *scales, int64_t i, float s, const Q8Size &z) {
+    if (in_bounds(scales + i, 4, scales, z.s, z.bounds)) scales[i] = s;
+}
+
 constexpr float E4M3_MAX = 448.f, SCALE_MIN = 1.17549435e-38f;  // the smallest normal fp32 value
 
 // An infinite or NaN element makes the scale infinite or leaves it (fmaxf ignores NaN): the block then holds
@@ -81,9 +90,11 @@ __device__ __forceinline__ void divide(float (&f)[VEC], float s, float r) {
     }
 }
 
-// VEC (4 or 8) values as e4m3
+// VEC (4 or 8) values as e4m3, from the at-th of the output on
 template <int VEC>
-__device__ __forceinline__ void put8(uint8_t *out, const float (&f)[VEC]) {
+__device__ __forceinline__ void put8(uint8_t *base, int64_t at, const float (&f)[VEC], const Q8Size &z) {
+    uint8_t *out = base + at;
+    if (!in_bounds(out, VEC, base, z.v, z.bounds)) return;
     uint32_t w[VEC / 4];
 #pragma unroll
     for (int e = 0; e < VEC; e += 4) w[e / 4] = q8_pack4(f[e], f[e + 1], f[e + 2], f[e + 3]);
@@ -91,11 +102,16 @@ __device__ __forceinline__ void put8(uint8_t *out, const float (&f)[VEC]) {
     else *reinterpret_cast<uint32_t *>(out) = w[0];
 }
 
+__device__ __forceinline__ void put1(uint8_t *out, int64_t at, float f, const Q8Size &z) {
+    if (in_bounds(out + at, 1, out, z.v, z.bounds)) out[at] = q8_one(f);
+}
+
 // Rows of whole 16-byte vectors: 128 / VEC lanes per block, four blocks of each lane group in flight together.
 // FLAT: whole blocks, that follow one another without gaps (no division per block).
 template <typename T, bool FLAT>
 __global__ void __launch_bounds__(256) quant_rows_vec_kernel(const T *__restrict__ x, int64_t rows, int64_t cols,
-                                                             uint8_t *__restrict__ out, float *__restrict__ scales) {
+                                                             uint8_t *__restrict__ out, float *__restrict__ scales,
+                                                             const Q8Size z) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
     constexpr int VEC = Q8Vec<T>::N, G = 128 / VEC, PER = 256 / G, U = 4;
@@ -128,8 +144,8 @@ __global__ void __launch_bounds__(256) quant_rows_vec_kernel(const T *__restrict
         const float s = q8_scale(group_max<G>(amax)), r = 1.0f / s;
         divide<VEC>(f, s, r);
         if (in[u]) {
-            put8<VEC>(out + at[u], f);
-            if (lane == 0) scales[b0 + u * PER] = s;
+            put8<VEC>(out, at[u], f, z);
+            if (lane == 0) put_scale(scales, b0 + u * PER, s, z);
         }
     }
 }
@@ -137,7 +153,8 @@ __global__ void __launch_bounds__(256) quant_rows_vec_kernel(const T *__restrict
 // Any others: a warp per block, lane l holds channels l + 32 j.
 template <typename T>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const T *__restrict__ x, int64_t rows, int64_t cols,
-                                                         uint8_t *__restrict__ out, float *__restrict__ scales) {
+                                                         uint8_t *__restrict__ out, float *__restrict__ scales,
+                                                         const Q8Size z) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
     const int l = threadIdx.x & 31;
@@ -154,8 +171,8 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T *__restrict__ x
         const float s = q8_scale(group_max<32>(amax));
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (c0 + l + 32 * j < cols) out[r * cols + c0 + l + 32 * j] = q8_one(f[j] / s);
-        if (l == 0) scales[u] = s;
+            if (c0 + l + 32 * j < cols) put1(out, r * cols + c0 + l + 32 * j, f[j] / s, z);
+        if (l == 0) put_scale(scales, u, s, z);
     }
 }
 
@@ -163,7 +180,8 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T *__restrict__ x
 // Rows of whole 16-byte vectors: a CTA holds its block in registers from its largest magnitude to its values.
 template <typename T>
 __global__ void __launch_bounds__(256) quant_tiles_vec_kernel(const T *__restrict__ x, int64_t rows, int64_t cols,
-                                                              uint8_t *__restrict__ out, float *__restrict__ scales) {
+                                                              uint8_t *__restrict__ out, float *__restrict__ scales,
+                                                              const Q8Size z) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
     constexpr int VEC = Q8Vec<T>::N, G = 128 / VEC, PER = 256 / G, U = 128 / PER;
@@ -194,15 +212,16 @@ __global__ void __launch_bounds__(256) quant_tiles_vec_kernel(const T *__restric
     for (int u = 0; u < U; ++u) {
         Q8Vec<T>::unpack(v[u], f);
         divide<VEC>(f, s, r);
-        if (r0 + u * PER < rows && c < cols) put8<VEC>(out + (r0 + u * PER) * cols + c, f);
+        if (r0 + u * PER < rows && c < cols) put8<VEC>(out, (r0 + u * PER) * cols + c, f, z);
     }
-    if (tid == 0) scales[blockIdx.x] = s;
+    if (tid == 0) put_scale(scales, blockIdx.x, s, z);
 }
 
 // Any others: the largest magnitude of the block, then its values (the second read comes from L1/L2).
 template <typename T>
 __global__ void __launch_bounds__(256) quant_tiles_kernel(const T *__restrict__ x, int64_t rows, int64_t cols,
-                                                          uint8_t *__restrict__ out, float *__restrict__ scales) {
+                                                          uint8_t *__restrict__ out, float *__restrict__ scales,
+                                                          const Q8Size z) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
     __shared__ float s_max[8];
@@ -224,8 +243,8 @@ __global__ void __launch_bounds__(256) quant_tiles_kernel(const T *__restrict__ 
     const float s = q8_scale(amax);
 #pragma unroll 8
     for (int r = tid >> 7; r < h; r += 2)
-        if (in) out[(r0 + r) * cols + c0 + c] = q8_one(load_elem(src, (int64_t)r * cols) / s);
-    if (tid == 0) scales[blockIdx.x] = s;
+        if (in) put1(out, (r0 + r) * cols + c0 + c, load_elem(src, (int64_t)r * cols) / s, z);
+    if (tid == 0) put_scale(scales, blockIdx.x, s, z);
 }
 
 // ---------------------------------------------------------------- norm, gate and quantisation
@@ -250,7 +269,8 @@ template <typename T, bool FLAT>
 __global__ void __launch_bounds__(256) norm_gate_fp8_vec_kernel(const T *__restrict__ o, const T *__restrict__ gate,
                                                                 int64_t N, int K, int nb, int hl,
                                                                 typename AccT<T>::type inv_dv, float eps,
-                                                                uint8_t *__restrict__ out, float *__restrict__ scales) {
+                                                                uint8_t *__restrict__ out, float *__restrict__ scales,
+                                                                const Q8Size z) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
     using AT = typename AccT<T>::type;
@@ -294,8 +314,8 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_vec_kernel(const T *__restr
         const float s = q8_scale(group_max<G>(amax)), r = 1.0f / s;
         divide<VEC>(f, s, r);
         if (in[u]) {
-            put8<VEC>(out + at[u], f);
-            if (lane == 0) scales[u0 + u * PER] = s;
+            put8<VEC>(out, at[u], f, z);
+            if (lane == 0) put_scale(scales, u0 + u * PER, s, z);
         }
     }
 }
@@ -307,7 +327,7 @@ constexpr int NG8_V = 4;
 template <typename T, int NT>
 __global__ void __launch_bounds__(NT) norm_gate_fp8_row_kernel(const T *__restrict__ o, const T *__restrict__ gate, int H,
                                                                 int Dv, float eps, uint8_t *__restrict__ out,
-                                                                float *__restrict__ scales) {
+                                                                float *__restrict__ scales, const Q8Size z) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
     using AT = typename AccT<T>::type;
@@ -359,8 +379,8 @@ __global__ void __launch_bounds__(NT) norm_gate_fp8_row_kernel(const T *__restri
         const float s = q8_scale(group_max<G>(amax)), r = 1.0f / s;
         divide<VEC>(f, s, r);
         if (in) {
-            put8<VEC>(out + base + i * VEC, f);
-            if (i % G == 0) scales[(int64_t)blockIdx.x * nb + i / G] = s;
+            put8<VEC>(out, base + i * VEC, f, z);
+            if (i % G == 0) put_scale(scales, (int64_t)blockIdx.x * nb + i / G, s, z);
         }
     }
 }
@@ -369,7 +389,7 @@ __global__ void __launch_bounds__(NT) norm_gate_fp8_row_kernel(const T *__restri
 template <typename T>
 __global__ void __launch_bounds__(256) norm_gate_fp8_kernel(const T *__restrict__ o, const T *__restrict__ gate, int H,
                                                             int Dv, float eps, uint8_t *__restrict__ out,
-                                                            float *__restrict__ scales) {
+                                                            float *__restrict__ scales, const Q8Size z) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
     using AT = typename AccT<T>::type;
@@ -399,9 +419,9 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_kernel(const T *__restrict_
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = 128 * u + l + 32 * j;
-            if (c < K) out[base + c] = q8_one(f[j] / s);
+            if (c < K) put1(out, base + c, f[j] / s, z);
         }
-        if (l == 0) scales[(int64_t)blockIdx.x * nb + u] = s;
+        if (l == 0) put_scale(scales, (int64_t)blockIdx.x * nb + u, s, z);
     }
 }
 
@@ -410,12 +430,14 @@ cudaError_t ng8_launch(const void *o, const void *gl, int64_t N, int H, int Dv, 
                        cudaStream_t st) {
     constexpr int VEC = Q8Vec<T>::N;
     const int K = H * Dv, nb = (K + 127) / 128;
+    const Q8Size z = {checked_size((size_t)N * K), checked_size((size_t)N * nb * 4), checked_counter()};
     // whole 16-byte vectors of one head per lane, whole heads per block, aligned rows
     if (Dv >= VEC && Dv <= 128 && (Dv & (Dv - 1)) == 0 && aligned_to(o, 16) && aligned_to(gl, 16) && aligned_to(x8, VEC)) {
         const int64_t ctas = (N * nb + 8 * VEC - 1) / (8 * VEC);  // 256 threads: 2 VEC groups of four blocks
         if (ctas <= 0x7fffffffLL)
-            return launch_pdl(K % 128 ? norm_gate_fp8_vec_kernel<T, false> : norm_gate_fp8_vec_kernel<T, true>, dim3((unsigned)ctas), dim3(256), 0, st, (const T *)o,
-                              (const T *)gl, N, K, nb, Dv / VEC, typename AccT<T>::type(1) / Dv, eps, (uint8_t *)x8, scales);
+            return launch_pdl(K % 128 ? norm_gate_fp8_vec_kernel<T, false> : norm_gate_fp8_vec_kernel<T, true>,
+                              dim3((unsigned)ctas), dim3(256), 0, st, (const T *)o, (const T *)gl, N, K, nb, Dv / VEC,
+                              typename AccT<T>::type(1) / Dv, eps, (uint8_t *)x8, scales, z);
     }
     if (Dv % VEC == 0 && K / VEC <= 256 * NG8_V && aligned_to(o, 16) && aligned_to(gl, 16) && aligned_to(x8, VEC)) {
         // the fewest threads that hold the token: 9109 tokens x 4 heads of 80 take 37 us with 256, 12 us with 64
@@ -424,19 +446,20 @@ cudaError_t ng8_launch(const void *o, const void *gl, int64_t N, int H, int Dv, 
                             : nt == 128 ? norm_gate_fp8_row_kernel<T, 128>
                                         : norm_gate_fp8_row_kernel<T, 256>;
         return launch_pdl(kernel, dim3((unsigned)N), dim3(nt), 0, st, (const T *)o, (const T *)gl, H, Dv, eps,
-                          (uint8_t *)x8, scales);
+                          (uint8_t *)x8, scales, z);
     }
     return launch_pdl(norm_gate_fp8_kernel<T>, dim3((unsigned)N), dim3(256), (size_t)H * 4, st, (const T *)o,
-                      (const T *)gl, H, Dv, eps, (uint8_t *)x8, scales);
+                      (const T *)gl, H, Dv, eps, (uint8_t *)x8, scales, z);
 }
 
 template <typename T>
 cudaError_t launch_quant(const void *x, int64_t rows, int64_t cols, int block_rows, int64_t units, uint8_t *y,
                          float *scales, cudaStream_t st) {
     constexpr int VEC = Q8Vec<T>::N, PER = 256 / (128 / VEC) * 4;
+    const Q8Size z = {checked_size((size_t)rows * cols), checked_size((size_t)units * 4), checked_counter()};
     auto go = [&](auto kernel, int64_t ctas) {
         return launch_pdl(kernel, dim3((unsigned)(ctas < 0x7fffffffLL ? ctas : 0x7fffffffLL)), dim3(256), 0, st,
-                          (const T *)x, rows, cols, y, scales);
+                          (const T *)x, rows, cols, y, scales, z);
     };
     const bool vec = cols % VEC == 0 && aligned_to(x, 16) && aligned_to(y, VEC);
     if (block_rows != 1) return go(vec ? quant_tiles_vec_kernel<T> : quant_tiles_kernel<T>, units);

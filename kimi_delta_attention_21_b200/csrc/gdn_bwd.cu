@@ -97,7 +97,7 @@ struct GbArgs {
     const float *S0, *dST;
     float *dq, *dk, *dv, *dbeta, *dz, *dS0;
     float *ws;
-    size_t ws_bytes, ns_bytes;
+    size_t ws_bytes, ns_bytes, nk_bytes, nv_bytes, nb_bytes;  // ns: dS0; nk: dq, dk; nv: dv; nb: dbeta, dz
     unsigned int *bounds;
 };
 
@@ -167,9 +167,12 @@ __device__ __forceinline__ float2 row_pair(const T *row, int c, int D, bool in, 
     return v;
 }
 
-// Columns c (even) and c + 1 of an output row.
-__device__ __forceinline__ void store_pair(float *row, int c, int D, bool in, bool pair, float x, float y) {
+// Columns c (even) and c + 1 of the row at `at` of an output of `bytes`.
+__device__ __forceinline__ void store_pair(float *out, size_t bytes, unsigned int *errors, int64_t at, int c, int D, bool in,
+                                           bool pair, float x, float y) {
     if (!in || c >= D) return;
+    float *row = out + at;
+    if (!in_bounds(row + c, c + 1 < D ? 8 : 4, out, bytes, errors)) return;
     if (pair) {
         *reinterpret_cast<float2 *>(row + c) = make_float2(x, y);
     } else {
@@ -784,8 +787,8 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
             r += r0;
             c += c0;
             db[i][e >> 1] = fmaf(a[i][j][e], e & 1 ? vv[i][j][e >> 1].y : vv[i][j][e >> 1].x, db[i][e >> 1]);
-            store_pair(p.dv + (u.row0 + (int64_t)r * p.H) * Dv, c - (e & 1), Dv, r < len && (e & 1), p.pair_v,
-                       sb[r] * a[i][j][e & 2], sb[r] * a[i][j][e | 1]);
+            store_pair(p.dv, p.nv_bytes, p.bounds, (u.row0 + (int64_t)r * p.H) * Dv, c - (e & 1), Dv, r < len && (e & 1),
+                       p.pair_v, sb[r] * a[i][j][e & 2], sb[r] * a[i][j][e | 1]);
         });
     }
     {
@@ -826,8 +829,9 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
             r += r0;
             c += c0;
             const int64_t row = (u.row0 + (int64_t)r * p.H) * Dk;
-            store_pair(p.dq + row, c - (e & 1), Dk, r < len && (e & 1), p.pair_k, dq[i][j][e & 2], dq[i][j][e | 1]);
-            store_pair(p.dk + row, c - (e & 1), Dk, r < len && (e & 1), p.pair_k, dk[i][j][e & 2], dk[i][j][e | 1]);
+            const bool in = r < len && (e & 1);
+            store_pair(p.dq, p.nk_bytes, p.bounds, row, c - (e & 1), Dk, in, p.pair_k, dq[i][j][e & 2], dq[i][j][e | 1]);
+            store_pair(p.dk, p.nk_bytes, p.bounds, row, c - (e & 1), Dk, in, p.pair_k, dk[i][j][e & 2], dk[i][j][e | 1]);
         });
     }
     // the sums over rows and pairs, in the places of T^T dT and dV', which are read
@@ -891,7 +895,8 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
         if (part) return;
         if (t < len) {
             const int64_t at = u.row0 + (int64_t)t * p.H;
-            p.dbeta[at] = sums[2 * C + t];
+            if (in_bounds(p.dbeta + at, 4, p.dbeta, p.nb_bytes, p.bounds)) p.dbeta[at] = sums[2 * C + t];
+            if (!in_bounds(p.dz + at, 4, p.dz, p.nb_bytes, p.bounds)) return;
             if (p.log_decay) {  // a clamped input has no gradient
                 const float x = p.log_decay[at];
                 p.dz[at] = (x >= p.g_min && x <= 0.f) ? dg : 0.f;
@@ -981,15 +986,19 @@ kda_status_t kda_gdn_chunk_bwd(const kda_recurrent_bwd_args *a) {
     p.dST = a->d_final_state;
     p.dq = a->dq; p.dk = a->dk; p.dv = a->dv; p.dbeta = a->dbeta; p.dz = a->dz; p.dS0 = a->d_initial_state;
     p.ws = reinterpret_cast<float *>(a->workspace);
-    p.ws_bytes = need;
-    p.ns_bytes = (size_t)nbh * a->D_k * a->D_v * 4;
+    const size_t ns = (size_t)nbh * a->D_k * a->D_v * 4, nb = (size_t)nbh * a->S * 4;
+    p.ws_bytes = checked_size(need);
+    p.ns_bytes = checked_size(ns);
+    p.nk_bytes = checked_size(nb * a->D_k);
+    p.nv_bytes = checked_size(nb * a->D_v);
+    p.nb_bytes = checked_size(nb);
     p.bounds = device_bounds_counter();
     if (a->S == 0) {  // no token: the state's gradient passes through
         if (a->d_initial_state) {
             const cudaError_t e = a->d_final_state
-                                      ? cudaMemcpyAsync(a->d_initial_state, a->d_final_state, p.ns_bytes,
+                                      ? cudaMemcpyAsync(a->d_initial_state, a->d_final_state, ns,
                                                         cudaMemcpyDeviceToDevice, st)
-                                      : cudaMemsetAsync(a->d_initial_state, 0, p.ns_bytes, st);
+                                      : cudaMemsetAsync(a->d_initial_state, 0, ns, st);
             if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "gdn backward: %s", cudaGetErrorString(e));
         }
         return KDA_OK;

@@ -31,7 +31,7 @@ struct GdArgs {
     const int32_t *slots;
     void *o;
     int32_t *status;
-    size_t state_bytes;
+    size_t state_bytes, o_bytes;
     unsigned int *bounds;
 };
 
@@ -181,7 +181,9 @@ __global__ void __launch_bounds__(256, RPW == 16 ? 2 : RPW == 8 ? 3 : 4) gdn_dec
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (FULL || col(j) < Dv) store_elem((T *)p.o, th * Dv + col(j), o[j]);
+                if ((FULL || col(j) < Dv) &&
+                    in_bounds((const T *)p.o + th * Dv + col(j), sizeof(T), p.o, p.o_bytes, p.bounds))
+                    store_elem((T *)p.o, th * Dv + col(j), o[j]);
         }
         if (t + 1 < p.T) now = token(t + 1);  // here, not above: its registers beside the sums cost 8% of eight tokens
     }
@@ -255,9 +257,10 @@ extern "C" kda_status_t kda_gdn_decode_step(const kda_gdn_decode_args *a) {
     KDA_TRY(check_no_overlap(Buf{a->state, ns, "state"}, ins, nin));
     KDA_TRY(check_no_overlap(Buf{a->o, nv, "o"}, ins, nin));
     if (overlap(a->o, nv, a->state, ns)) return fail(KDA_ERR_INVALID_ARG, "o overlaps state");
-    const GdArgs p = {a->num_slots, a->T,     a->H,     a->D_k,       a->D_v, a->q,      a->k,
-                      a->v,         a->z,     a->beta,  a->gate_logits, a->log_decay, a->g_min, a->eps,
-                      a->state,     a->slots, a->o,     a->dev_status, ns,     device_bounds_counter()};
+    const GdArgs p = {a->num_slots, a->T,  a->H,    a->D_k,         a->D_v,       a->q,     a->k,
+                      a->v,         a->z,  a->beta, a->gate_logits, a->log_decay, a->g_min, a->eps,
+                      a->state,     a->slots, a->o, a->dev_status,  checked_size(ns), checked_size(nv),
+                      device_bounds_counter()};
     cudaStream_t st = (cudaStream_t)a->stream;
     const cudaError_t e = a->dtype == KDA_F32 ? gd_launch<float>(*a, p, st) : gd_launch<__nv_bfloat16>(*a, p, st);
     if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "gdn_decode_kernel: %s", cudaGetErrorString(e));

@@ -47,11 +47,13 @@ __device__ __forceinline__ float log_alpha_of(float z, float g_min) {
 }
 
 // ----------------------------------------------------------------- checked builds
-// A build with -DKDA_CHECKED tests every global write through an offset the library computes itself
-// (workspace records, segment maps and entering states, checkpoints and stashes, final states, staged
-// outputs) against the buffer it has to land in: a write that would leave its buffer is skipped and
-// counted in a device counter (kda_device_bounds_errors), never trapped.  Other builds compile the
-// test away.
+// A build with -DKDA_CHECKED tests global writes through an offset the library computes itself against the
+// buffer they have to land in: workspace records, segment maps and entering states, checkpoints and stashes,
+// final states, staged outputs, and every output and workspace of the operators in qk_norm.cu, gdn_decode.cu,
+// gdn_bwd.cu, fp8_quant.cu and proj_fp8.cu but those that a TMA map clips.  (Not tested: the elements that
+// gate.cu, norm_gate.cu, decode.cu, chunk_simt.cu and the bf16 and SIMT projections store.)  A write that would
+// leave its buffer is skipped and counted in a device counter (kda_device_bounds_errors), never trapped.  Other
+// builds compile the test away.
 #ifdef KDA_CHECKED
 __device__ __forceinline__ bool in_bounds(const void *p, size_t n, const void *base, size_t size,
                                           unsigned int *errors) {
@@ -66,6 +68,17 @@ __device__ __forceinline__ constexpr bool in_bounds(const void *, size_t, const 
 }
 #endif
 unsigned int *device_bounds_counter();  // device address of the counter (host)
+
+// The size of a buffer as the device checks get it.  In a checked build the environment variable KDA_CHECKED_SHRINK
+// (bytes) makes every such size smaller, so that a test can see a kernel's last writes skipped and counted: all of them
+// stay inside the buffers.
+#ifdef KDA_CHECKED
+size_t checked_size(size_t n);
+inline unsigned int *checked_counter() { return device_bounds_counter(); }
+#else
+inline size_t checked_size(size_t n) { return n; }
+inline unsigned int *checked_counter() { return nullptr; }  // (nothing counts)
+#endif
 
 // ----------------------------------------------------------------- asynchronous global -> shared copies
 // One fp32 element by cp.async (4-byte aligned addresses); with fill == false the destination gets

@@ -54,6 +54,12 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void 
                  : "memory");
 }
 
+// What the checked build holds the stores to y against.
+struct YSize {
+    size_t n;
+    unsigned int *bounds;
+};
+
 // Address of a shared-memory object of this CTA in the cluster's CTA `rank`.
 __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
     uint32_t a;
@@ -145,7 +151,7 @@ template <typename OT>
 __global__ void __launch_bounds__(PF_NT, 1)
 proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmY, const float *__restrict__ xs, const float *__restrict__ ws,
-                int M, int N, int K, OT *__restrict__ y, int tma_y, unsigned int *timeouts) {
+                int M, int N, int K, OT *__restrict__ y, int tma_y, const YSize yz, unsigned int *timeouts) {
     pdl_trigger();
     pdl_wait();
     constexpr int ST = Tile::STAGES, NB = Tile::BUFS, BN = Tile::BN, HC = BN / 2;  // HC: columns per epilogue warp
@@ -294,7 +300,8 @@ proj_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                         for (int i = 0; i < PER; i += 32) {
                             const int j = lane + i;
-                            if (c0 + c + j < N) dst[j] = buf[r * PER + (((j / E) ^ (r & 7)) * E + j % E)];
+                            if (c0 + c + j < N && in_bounds(dst + j, sizeof(OT), y, yz.n, yz.bounds))
+                                dst[j] = buf[r * PER + (((j / E) ^ (r & 7)) * E + j % E)];
                         }
                     }
                     __syncwarp();
@@ -325,7 +332,7 @@ template <typename OT>
 __global__ void __launch_bounds__(PF_NT, 1)
 proj_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const float *__restrict__ xs, const float *__restrict__ ws, int M, int N, int K, int parts,
-                      OT *__restrict__ y, int vec_y, unsigned int *timeouts) {
+                      OT *__restrict__ y, int vec_y, const YSize yz, unsigned int *timeouts) {
     pdl_trigger();
     pdl_wait();
     constexpr int ST = Split::STAGES, NB = Split::BUFS, BN = Split::BN, HC = BN / 2, LY = Split::LY;
@@ -437,8 +444,8 @@ proj_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             const float f[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (col + i < N) store_elem(dst, i, f[i]);
-        } else {
+                if (col + i < N && in_bounds(dst + i, sizeof(OT), y, yz.n, yz.bounds)) store_elem(dst, i, f[i]);
+        } else if (in_bounds(dst, 4 * sizeof(OT), y, yz.n, yz.bounds)) {
             if (sizeof(OT) == 4) {
                 *reinterpret_cast<float4 *>(dst) = t;
             } else {
@@ -456,7 +463,7 @@ proj_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
 template <typename OT>
 __global__ void __launch_bounds__(256) proj_fp8_simt_kernel(const uint8_t *__restrict__ x, const float *__restrict__ xs,
                                                             const uint8_t *__restrict__ w, const float *__restrict__ ws,
-                                                            int64_t M, int N, int K, OT *__restrict__ y) {
+                                                            int64_t M, int N, int K, OT *__restrict__ y, const YSize yz) {
     pdl_trigger();
     pdl_wait();
     __shared__ float sX[16][65], sW[16][65];
@@ -501,7 +508,8 @@ __global__ void __launch_bounds__(256) proj_fp8_simt_kernel(const uint8_t *__res
         for (int j = 0; j < 4; ++j) {
             const int64_t r = m0 + ty + 16 * i;
             const int c = n0 + tx + 16 * j;
-            if (r < M && c < N) store_elem(y, r * N + c, acc[i][j]);
+            if (r < M && c < N && in_bounds(y + r * N + c, sizeof(OT), y, yz.n, yz.bounds))
+                store_elem(y, r * N + c, acc[i][j]);
         }
 }
 
@@ -545,11 +553,12 @@ kda_status_t map_bytes(CUtensorMap *m, const void *base, int64_t rows, int K, ui
 template <typename OT>
 kda_status_t launch_proj_fp8(const P8Args &a, cudaStream_t st) {
     // whole 16-byte vectors in the rows of x and W, and aligned bases: what the TMA maps ask for
+    const YSize yz = {checked_size((size_t)a.N * a.M * sizeof(OT)), checked_counter()};
     const bool tc = a.K % 16 == 0 && aligned_to(a.x, 16) && aligned_to(a.w, 16);
     if (!tc) {
         const int64_t ctas = ((a.N + 63) / 64) * ((a.M + 63) / 64);
         const cudaError_t e = launch_pdl(proj_fp8_simt_kernel<OT>, dim3((unsigned)ctas), dim3(256), 0, st,
-                                         (const uint8_t *)a.x, a.xs, (const uint8_t *)a.w, a.ws, a.N, a.M, a.K, (OT *)a.y);
+                                         (const uint8_t *)a.x, a.xs, (const uint8_t *)a.w, a.ws, a.N, a.M, a.K, (OT *)a.y, yz);
         if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "proj_fp8_simt_kernel: %s", cudaGetErrorString(e));
         return check_launch("proj_fp8_simt_kernel");
     }
@@ -567,7 +576,8 @@ kda_status_t launch_proj_fp8(const P8Args &a, cudaStream_t st) {
         while (parts < 8 && tiles * parts * 2 <= sms && KB >= 8 * parts) parts *= 2;
         const cudaError_t e = launch_cluster(proj_fp8_split_kernel<OT>, (unsigned)(tiles * parts), (unsigned)parts, Split::SMEM,
                                              st, ta, tb, a.xs, a.ws, (int)a.N, a.M, a.K, parts, (OT *)a.y,
-                                             (int)(a.M % 4 == 0 && aligned_to(a.y, 4 * sizeof(OT))), device_timeout_counter());
+                                             (int)(a.M % 4 == 0 && aligned_to(a.y, 4 * sizeof(OT))), yz,
+                                             device_timeout_counter());
         if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "proj_fp8_split_kernel: %s", cudaGetErrorString(e));
         return check_launch("proj_fp8_split_kernel");
     }
@@ -582,7 +592,8 @@ kda_status_t launch_proj_fp8(const P8Args &a, cudaStream_t st) {
     const int64_t big = ((a.N + PM - 1) / PM) * ((a.M + Tile::BN - 1) / Tile::BN);
     cudaFuncSetAttribute(proj_fp8_kernel<OT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tile::SMEM);
     const cudaError_t e = launch_pdl(proj_fp8_kernel<OT>, dim3((unsigned)(big < sms ? big : sms)), dim3(PF_NT), Tile::SMEM, st,
-                                     ta, tb, ty, a.xs, a.ws, (int)a.N, a.M, a.K, (OT *)a.y, tma_y, device_timeout_counter());
+                                     ta, tb, ty, a.xs, a.ws, (int)a.N, a.M, a.K, (OT *)a.y, tma_y, yz,
+                                     device_timeout_counter());
     if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "proj_fp8_kernel: %s", cudaGetErrorString(e));
     return check_launch("proj_fp8_kernel");
 }

@@ -38,6 +38,7 @@ struct QnSide {       // queries, or keys
     void *y;          // forward: out; backward: dx
     const void *dy;
     float *dw;
+    size_t y_bytes;
 };
 
 struct QnArgs {
@@ -48,7 +49,15 @@ struct QnArgs {
     const int64_t *pos;
     const float *inv;
     float *partial;   // [gridDim.x][2][D] weight gradients of each CTA
+    size_t partial_bytes, dw_bytes;
+    unsigned int *bounds;
 };
+
+// A store that the checked build tests (n bytes at `at`, into y or the partial sums).
+template <typename V>
+__device__ __forceinline__ void qn_put(const QnArgs &p, void *base, size_t bytes, V *at, const V &v) {
+    if (in_bounds(at, sizeof(V), base, bytes, p.bounds)) *at = v;
+}
 
 // cos and sin of pos * f
 __device__ __forceinline__ void qn_angle(int64_t pos, float f, float &c, float &s) {
@@ -243,8 +252,9 @@ __global__ void __launch_bounds__(QN_NT) qk_norm_kernel(const __grid_constant__ 
 #pragma unroll
                     for (int v = 0; v < NV; ++v)
                         if (in[v])
-                            *reinterpret_cast<uint4 *>(y + (int64_t)(h0 + i + u) * p.D + (lane + G * v) * VEC) =
-                                QnVec<T>::pack(f[v]);
+                            qn_put(p, s.y, s.y_bytes,
+                                   reinterpret_cast<uint4 *>(y + (int64_t)(h0 + i + u) * p.D + (lane + G * v) * VEC),
+                                   QnVec<T>::pack(f[v]));
             }
         }
     }
@@ -334,8 +344,10 @@ __global__ void __launch_bounds__(QN_NT) qk_norm_bwd_kernel(const __grid_constan
 #pragma unroll
                     for (int v = 0; v < NV; ++v)
                         if (in[v])
-                            *reinterpret_cast<uint4 *>((T *)s.y + row + (int64_t)(h0 + i + u) * p.D +
-                                                       (lane + G * v) * VEC) = QnVec<T>::pack(f[v]);
+                            qn_put(p, s.y, s.y_bytes,
+                                   reinterpret_cast<uint4 *>((T *)s.y + row + (int64_t)(h0 + i + u) * p.D +
+                                                             (lane + G * v) * VEC),
+                                   QnVec<T>::pack(f[v]));
             }
         }
     }
@@ -348,7 +360,7 @@ __global__ void __launch_bounds__(QN_NT) qk_norm_bwd_kernel(const __grid_constan
     for (int c = threadIdx.x; c < p.D; c += QN_NT) {
         float t = 0.f;
         for (int i = 0; i < PER; ++i) t += s_dw[i][c];
-        p.partial[((int64_t)blockIdx.x * 2 + blockIdx.y) * p.D + c] = t;
+        qn_put(p, p.partial, p.partial_bytes, p.partial + ((int64_t)blockIdx.x * 2 + blockIdx.y) * p.D + c, t);
     }
 }
 
@@ -369,7 +381,7 @@ __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const __grid_constant_
     if (ry == 0 && c < p.D) {
         t = 0.f;
         for (int i = 0; i < 32; ++i) t += red[i][cx];
-        dw[c] = t;
+        qn_put(p, dw, p.dw_bytes, dw + c, t);
     }
 }
 
@@ -461,7 +473,8 @@ __global__ void __launch_bounds__(QN_NT) qk_norm_generic_kernel(const __grid_con
 #pragma unroll
             for (int j = 0; j < QN_J; ++j) {
                 const int c = lane + 32 * j;
-                if (c < p.D) store_elem((T *)s.y, row + c, f[j]);
+                if (c < p.D && in_bounds((const T *)s.y + row + c, sizeof(T), s.y, s.y_bytes, p.bounds))
+                    store_elem((T *)s.y, row + c, f[j]);
             }
         }
     }
@@ -473,7 +486,7 @@ __global__ void __launch_bounds__(QN_NT) qk_norm_generic_kernel(const __grid_con
     for (int c = threadIdx.x; c < p.D; c += QN_NT) {
         float t = 0.f;
         for (int i = 0; i < NW; ++i) t += buf[i][c];
-        p.partial[((int64_t)blockIdx.x * 2 + blockIdx.y) * p.D + c] = t;
+        qn_put(p, p.partial, p.partial_bytes, p.partial + ((int64_t)blockIdx.x * 2 + blockIdx.y) * p.D + c, t);
     }
 }
 
@@ -508,8 +521,8 @@ void qn_items(QnSide &s, int64_t tokens, int lanes, int sms) {
 
 QnArgs qn_args(const kda_qk_norm_args &a) {
     QnArgs p = {};
-    p.side[0] = {a.q, a.q_stride_b, a.q_stride_s, a.H_q, 0, 0, a.q_weight, a.q_out, nullptr, nullptr};
-    p.side[1] = {a.k, a.k_stride_b, a.k_stride_s, a.H_k, 0, 0, a.k_weight, a.k_out, nullptr, nullptr};
+    p.side[0] = {a.q, a.q_stride_b, a.q_stride_s, a.H_q, 0, 0, a.q_weight, a.q_out, nullptr, nullptr, 0};
+    p.side[1] = {a.k, a.k_stride_b, a.k_stride_s, a.H_k, 0, 0, a.k_weight, a.k_out, nullptr, nullptr, 0};
     p.tokens = a.B * a.S;
     p.S = a.S;
     p.D = a.D;
@@ -518,6 +531,10 @@ QnArgs qn_args(const kda_qk_norm_args &a) {
     p.eps = a.eps;
     p.pos = a.positions;
     p.inv = a.inv_freq;
+    const size_t rows = (size_t)p.tokens * a.D * esize(a.dtype);
+    p.side[0].y_bytes = checked_size(rows * a.H_q);
+    p.side[1].y_bytes = checked_size(rows * a.H_k);
+    p.bounds = checked_counter();
     return p;
 }
 
@@ -707,6 +724,8 @@ kda_status_t kda_qk_norm_bwd(const kda_qk_norm_bwd_args *a) {
     p.side[0].dw = a->dq_weight;
     p.side[1].dw = a->dk_weight;
     p.partial = (float *)a->workspace;
+    p.partial_bytes = checked_size(need);
+    p.dw_bytes = checked_size((size_t)f.D * 4);
     const void *ptrs[] = {f.q, f.k, a->dq, a->dk, a->dq_out, a->dk_out};
     const bool vec = qn_vector(f, ptrs, 6);
     unsigned ctas = 0;
