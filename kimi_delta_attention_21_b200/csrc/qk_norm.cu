@@ -161,14 +161,15 @@ __device__ __forceinline__ void qn_phases(const QnArgs &p, int64_t pos, int lane
         }
 }
 
-// The partners of this lane's channels (half-split: the vector R/2 channels away).
+// The partners of this lane's channels (half-split: the vector R/2 channels away); zero past R, where an infinite or NaN
+// neighbour times a sine of zero would be NaN.
 template <int VEC, int G, int NV, int ROT>
 __device__ __forceinline__ void qn_partner(const QnArgs &p, int lane, const float (&y)[NV][VEC], float (&o)[NV][VEC]) {
     if (ROT == ROT_INTERLEAVED) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[v][e] = y[v][e ^ 1];
+            for (int e = 0; e < VEC; ++e) o[v][e] = (lane + G * v) * VEC + e < p.R ? y[v][e ^ 1] : 0.f;
         return;
     }
     const int d = (p.R >> 1) / VEC;
@@ -183,7 +184,7 @@ __device__ __forceinline__ void qn_partner(const QnArgs &p, int lane, const floa
                 const float t1 = __shfl_sync(0xffffffffu, y[NV - 1][e], src, G);
                 t = other >= G ? t1 : t;
             }
-            o[v][e] = t;
+            o[v][e] = j < 2 * d ? t : 0.f;
         }
     }
 }
