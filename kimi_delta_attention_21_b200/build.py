@@ -12,13 +12,18 @@ KDA_LIBRARY names it.
 
 csrc_py/marshal.cpp, the argument marshalling of the operators whose calls take
 microseconds, compiles with g++ against torch's headers into _marshal.so (the
-library itself knows nothing of torch).
+library itself knows nothing of torch).  For a user of the C library alone,
+`python kimi_delta_attention_21_b200/build.py` needs neither: without torch, its
+headers or g++ it builds the library, says that the extension was left out and
+why, and the Python calls that need it fail with an ImportError.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 
@@ -30,6 +35,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 BUILD_CHECKED = os.path.join(ROOT, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libkda_checked.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC,
@@ -61,15 +67,31 @@ def _compile(src, ptxas_verbose, build_dir=BUILD, extra=()):
     return obj, r.stderr
 
 
-def build_marshal() -> str:
-    """Compile csrc_py/marshal.cpp into the importable _marshal.so."""
-    src, so = os.path.join(PKG, "csrc_py", "marshal.cpp"), os.path.join(PKG, "_marshal.so")
+def _torch_root():
+    """The installed torch package's directory, or None."""
+    try:
+        spec = importlib.util.find_spec("torch")
+    except (ImportError, ValueError):
+        spec = None
+    return os.path.dirname(os.path.abspath(spec.origin)) if spec and spec.origin else None
+
+
+def build_marshal() -> str | None:
+    """Compile csrc_py/marshal.cpp into the importable _marshal.so; None, and a line that says so, where there is nothing
+    to compile it with."""
+    src, so = os.path.join(PKG, "csrc_py", "marshal.cpp"), MARSHAL
     if not _stale(so, [src] + glob.glob(os.path.join(INCLUDE, "*.h"))):
         return so
     import sysconfig
+    root = _torch_root()
+    headers = [os.path.join(root or "", "include", "ATen", "ATen.h"), os.path.join(sysconfig.get_paths()["include"], "Python.h")]
+    lacking = ("torch" if root is None else "g++" if shutil.which("g++") is None else
+               next((h for h in headers if not os.path.exists(h)), None))
+    if lacking:
+        sys.stderr.write(f"{os.path.basename(so)} was not built: {lacking} is missing (only Python calls need it)\n")
+        return None
 
     import torch
-    root = os.path.dirname(os.path.abspath(torch.__file__))
     system = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
               os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
     tmp = so + f".tmp{os.getpid()}"
