@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(prep_nt<T>(), 512 / prep_nt<T>()) gb_prep_kern
         const int m0 = 32 * (t & 3), n0 = 32 * (t >> 2);
         if (m0 >= Dkp || n0 >= Dvp) continue;
         float h[2][4][4] = {};
-        tf32::tile<2, 4, true, true, EX, false, 1, 2, true>(h, sQ + m0, LD, sO + n0, LD, C, seG);
+        tf32::tile<2, 4, true, true, EX, false, 2, true>(h, sQ + m0, LD, sO + n0, LD, C, seG);
         tf32::each<2, 4>([&](int i, int j, int e, int r, int c) {
             if (!(e & 1) && m0 + r < Dkp)
                 *reinterpret_cast<float2 *>(rec + R.dS + (m0 + r) * Dvp + n0 + c) = make_float2(h[i][j][e], h[i][j][e + 1]);
@@ -492,7 +492,7 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
                     *reinterpret_cast<float2 *>(rec + R.S + (m0 + r) * Dvp + j0 + c) = make_float2(S[i][j][e], S[i][j][e + 1]);
             });
         float v[1][2][4] = {};
-        tf32::tile<1, 2, false, true, false, false, 1, 8>(v, g.W + r0 * LD + q.kh, LD, g.sS + q.kh * LO, LO, FULL ? C : q.kn);
+        tf32::tile<1, 2, false, true, false, false, 8>(v, g.W + r0 * LD + q.kh, LD, g.sS + q.kh * LO, LO, FULL ? C : q.kn);
         if (!first) tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { g.sY[(r0 + r) * LO + c] = v[i][j][e]; });
         __syncthreads();  // the other half of the sum; W is read
         if (first)
@@ -513,7 +513,7 @@ __device__ __forceinline__ void chain_forward(const GbArgs &p, int64_t bh, int j
         if (own) {
             const float gamma = e_[C - 1];
             float add[1][2][4] = {};
-            tf32::tile<1, 2, true, true, EX, false, 1, 8>(add, g.K + m0, LD, g.sV, lv, C);
+            tf32::tile<1, 2, true, true, EX, false, 8>(add, g.K + m0, LD, g.sV, lv, C);
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 S[i][j][e] = fmaf(gamma, S[i][j][e], add[i][j][e]);
                 if (e & 1) *reinterpret_cast<float2 *>(g.sS + (m0 + r) * LO + c - 1) = make_float2(S[i][j][e - 1], S[i][j][e]);
@@ -556,7 +556,7 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
         stage_block<NT_C, 4>(g.H, LO, rec + R.dS + j0, Dvp, Dkp, VS);
         cp_async_commit_group();
         float x[1][2][4] = {};
-        tf32::tile<1, 2, false, true, EX, false, 1, 8>(x, g.K + r0 * LD + q.kh, LD, g.sS + q.kh * LO, LO, FULL ? C : q.kn);
+        tf32::tile<1, 2, false, true, EX, false, 8>(x, g.K + r0 * LD + q.kh, LD, g.sS + q.kh * LO, LO, FULL ? C : q.kn);
         if (!first) tf32::each<1, 2>([&](int i, int j, int e, int r, int c) { g.sY[(r0 + r) * LO + c] = x[i][j][e]; });
         __syncthreads();  // the other half of the sum; K is read
         if (first)
@@ -580,7 +580,7 @@ __device__ __forceinline__ void chain_backward(const GbArgs &p, int64_t bh, int 
             });
             const float gamma = e_[C - 1];
             float sub[1][2][4] = {};
-            tf32::tile<1, 2, true, true, false, false, 1, 8>(sub, g.W + m0, LD, g.sV, LV, C);
+            tf32::tile<1, 2, true, true, false, false, 8>(sub, g.W + m0, LD, g.sV, LV, C);
             tf32::each<1, 2>([&](int i, int j, int e, int r, int c) {
                 dS[i][j][e] = fmaf(gamma, dS[i][j][e], g.H[(m0 + r) * LO + c] + sub[i][j][e]);
                 if (e & 1) *reinterpret_cast<float2 *>(g.sS + (m0 + r) * LO + c - 1) = make_float2(dS[i][j][e - 1], dS[i][j][e]);
@@ -710,14 +710,14 @@ __global__ void __launch_bounds__(NT_P, 1) gb_grad_kernel(const __grid_constant_
             if (Piece<T>::SETS == 2 && i + 1 < np) stage(i + 1);
             const Piece<T> q(area, i);
             if (inK) {
-                tf32::tile<2, 2, false, false, EX, false, 1, 4>(dq, q.dO + r0 * LQ, LQ, q.S + c0 * LQ, LQ, 32);
-                tf32::tile<2, 2, false, false, false, false, 1, 4>(w, q.dV + r0 * LQ, LQ, q.S + c0 * LQ, LQ, 32);
+                tf32::tile<2, 2, false, false, EX, false, 4>(dq, q.dO + r0 * LQ, LQ, q.S + c0 * LQ, LQ, 32);
+                tf32::tile<2, 2, false, false, false, false, 4>(w, q.dV + r0 * LQ, LQ, q.S + c0 * LQ, LQ, 32);
             }
             if (tri) {
-                tf32::tile<2, 1, false, false, EX, false, 1, 4>(m, q.dO + r0 * LQ, LQ, q.V + c1 * LQ, LQ, 32);
-                tf32::tile<2, 1, false, false, false, EX, 1, 4>(d, q.dV + r0 * LQ, LQ, q.v + c1 * LQ, LQ, 32);
+                tf32::tile<2, 1, false, false, EX, false, 4>(m, q.dO + r0 * LQ, LQ, q.V + c1 * LQ, LQ, 32);
+                tf32::tile<2, 1, false, false, false, EX, 4>(d, q.dV + r0 * LQ, LQ, q.v + c1 * LQ, LQ, 32);
             }
-            if (inK) tf32::tile<2, 2, false, false, false, false, 1, 4>(dk, q.V + r0 * LQ, LQ, q.dS + c0 * LQ, LQ, 32);
+            if (inK) tf32::tile<2, 2, false, false, false, false, 4>(dk, q.V + r0 * LQ, LQ, q.dS + c0 * LQ, LQ, 32);
             for (int r = tid >> 3, c = (tid & 7) * 4; r < Dkp; r += NT_P / 8) {
                 const float4 x = *reinterpret_cast<const float4 *>(q.S + r * LQ + c);
                 const float4 y = *reinterpret_cast<const float4 *>(q.dS + r * LQ + c);

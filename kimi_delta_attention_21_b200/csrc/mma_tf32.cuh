@@ -37,13 +37,6 @@ __device__ __forceinline__ void load2(const __nv_bfloat16 *p, float &x, float &y
     y = __uint_as_float(t & 0xffff0000u);
 }
 
-// (hi, lo) of a value, as operands kept split in shared memory hold them
-__device__ __forceinline__ float2 split2(float x) {
-    uint32_t hi, lo;
-    split(x, hi, lo);
-    return make_float2(__uint_as_float(hi), __uint_as_float(lo));
-}
-
 // Neighbouring bf16 rows k = 2t, 2t + 1 of column g of an 8 x 8 block, packed into one register per block; each lane
 // gives the address of a row of 16 bytes (lanes 8b .. 8b + 7: block b).
 __device__ __forceinline__ void ldsm_trans(uint32_t (&r)[1], uint32_t addr) {
@@ -62,25 +55,20 @@ __device__ __forceinline__ void ldsm_trans(uint32_t (&r)[4], uint32_t addr) {
 // acc += A B^T over k < K (a multiple of 8; UNROLL steps of 8 at a time), for a warp's MT x 16 rows and NT x 8 columns:
 // acc[i][j] holds (16i + g, 8j + 2t), (.., + 1), (16i + g + 8, ..), (.., + 1) with g = lane / 4, t = lane % 4.
 //   A(m, k) = A[m * lda + k], or A[k * lda + m] with AT;  B(n, k) = B[n * ldb + k], or B[k * ldb + n] with BT.
-// Operands are fp32, bf16 (exact; read by k they come through ldmatrix, from rows on 16-byte boundaries) or, B read
-// by k, kept split (float2: hi, lo).  AEX / BEX: tf32 holds the operand exactly.  The order of k within an
-// instruction is free, as long as A and B share it: unless both are fp32 and read by k, a lane takes neighbouring k
-// (one load where the operand is contiguous in k).
-// Pitches of 8 mod 32 floats make the reads free of bank conflicts (fp32 read by k in pairs: two-way); for a split B,
-// 2 mod 8 pairs where k comes in pairs, 4 mod 16 where it does not.
+// Operands are fp32 or bf16 (exact; read by k they come through ldmatrix, from rows on 16-byte boundaries).  AEX / BEX:
+// tf32 holds the operand exactly.  The order of k within an instruction is free, as long as A and B share it: unless
+// both are fp32 and read by k, a lane takes neighbouring k (one load where the operand is contiguous in k).
+// Pitches of 8 mod 32 floats make the reads free of bank conflicts (fp32 read by k in pairs: two-way).
 // The lo terms have accumulators of their own, so that the tensor core, which truncates as it adds, does so once per
-// step of 8 on the large sums; CROSS = 2 keeps the two kinds apart (shorter dependent chains where a warp has few
-// tiles).  KS: B's rows k are multiplied by ks[k] as they are read.
-template <int MT, int NT, bool AT, bool BT, bool AEX, bool BEX, int CROSS = 1, int UNROLL = 2, bool KS = false,
-          typename TA, typename TB>
+// step of 8 on the large sums.  KS: B's rows k are multiplied by ks[k] as they are read.
+template <int MT, int NT, bool AT, bool BT, bool AEX, bool BEX, int UNROLL = 2, bool KS = false, typename TA, typename TB>
 __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int lda, const TB *B, int ldb,
                                      int K, const float *ks = nullptr) {
     constexpr bool A16 = sizeof(TA) == 2 && AT, B16 = sizeof(TB) == 2 && BT;
     constexpr bool PAIR = !(AT && BT) || A16 || B16;
-    static_assert(sizeof(TB) != 8 || BT, "split operands are read by k");
-    static_assert(!KS || (BT && !BEX && sizeof(TB) != 8), "a scaled operand is read by k, and is not exact");
+    static_assert(!KS || (BT && !BEX), "a scaled operand is read by k, and is not exact");
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float cross[CROSS][MT][NT][4] = {};
+    float cross[MT][NT][4] = {};
     uint32_t arow = 0, brow = 0;  // this lane's row for ldmatrix: k = lane % 8, of block lane / 8
     if constexpr (A16)
         arow = (uint32_t)__cvta_generic_to_shared(A + (lane & 7) * lda + ((lane >> 3) & (2 * MT - 1)) * 8);
@@ -142,25 +130,17 @@ __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int l
         } else {
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                if constexpr (sizeof(TB) == 8) {
-                    const float2 u = B[ka * ldb + 8 * j + g], v = B[kb * ldb + 8 * j + g];
-                    bh[j][0] = __float_as_uint(u.x);
-                    bl[j][0] = __float_as_uint(u.y);
-                    bh[j][1] = __float_as_uint(v.x);
-                    bl[j][1] = __float_as_uint(v.y);
+                float x[2];
+                if (BT) {
+                    x[0] = sc[0] * load_elem(B, ka * ldb + 8 * j + g);
+                    x[1] = sc[1] * load_elem(B, kb * ldb + 8 * j + g);
                 } else {
-                    float x[2];
-                    if (BT) {
-                        x[0] = sc[0] * load_elem(B, ka * ldb + 8 * j + g);
-                        x[1] = sc[1] * load_elem(B, kb * ldb + 8 * j + g);
-                    } else {
-                        load2(B + (8 * j + g) * ldb + ka, x[0], x[1]);
-                    }
+                    load2(B + (8 * j + g) * ldb + ka, x[0], x[1]);
+                }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (BEX) bh[j][e] = __float_as_uint(x[e]);
-                        else split(x[e], bh[j][e], bl[j][e]);
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    if (BEX) bh[j][e] = __float_as_uint(x[e]);
+                    else split(x[e], bh[j][e], bl[j][e]);
                 }
             }
         }
@@ -168,8 +148,8 @@ __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int l
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                if (!BEX) mma(cross[0][i][j], ah[i], bl[j]);
-                if (!AEX) mma(cross[CROSS - 1][i][j], al[i], bh[j]);
+                if (!BEX) mma(cross[i][j], ah[i], bl[j]);
+                if (!AEX) mma(cross[i][j], al[i], bh[j]);
             }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -182,8 +162,7 @@ __device__ __forceinline__ void tile(float (&acc)[MT][NT][4], const TA *A, int l
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] += CROSS == 2 ? cross[0][i][j][e] + cross[CROSS - 1][i][j][e] : cross[0][i][j][e];
+                for (int e = 0; e < 4; ++e) acc[i][j][e] += cross[i][j][e];
     }
 }
 
