@@ -51,26 +51,6 @@ __device__ __forceinline__ AT group_sum(AT v) {
     return v;
 }
 
-template <typename T> struct Q8Vec;
-template <> struct Q8Vec<float> {
-    static constexpr int N = 4;
-    __device__ static void unpack(const uint4 &u, float (&f)[4]) {
-        f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-        f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
-    }
-};
-template <> struct Q8Vec<__nv_bfloat16> {
-    static constexpr int N = 8;
-    __device__ static void unpack(const uint4 &u, float (&f)[8]) {
-        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(v[i] << 16);
-            f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-        }
-    }
-};
-
 // ---------------------------------------------------------------- 1 x 128 blocks of a matrix
 // f / s, rounded to nearest, r = 1 / s: the product with r and one correction by the remainder f - q s, which an fma
 // gives exactly (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990), for
@@ -114,7 +94,7 @@ __global__ void __launch_bounds__(256) quant_rows_vec_kernel(const T *__restrict
                                                              const Q8Size z) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
-    constexpr int VEC = Q8Vec<T>::N, G = 128 / VEC, PER = 256 / G, U = 4;
+    constexpr int VEC = Vec16<T>::N, G = 128 / VEC, PER = 256 / G, U = 4;
     const int lane = threadIdx.x & (G - 1);
     const unsigned nb = (unsigned)((cols + 127) / 128), blocks = (unsigned)rows * nb;
     const unsigned b0 = blockIdx.x * (PER * U) + threadIdx.x / G;
@@ -138,7 +118,7 @@ __global__ void __launch_bounds__(256) quant_rows_vec_kernel(const T *__restrict
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         float f[VEC], amax = 0.f;
-        Q8Vec<T>::unpack(v[u], f);
+        Vec16<T>::unpack(v[u], f);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fabsf(f[e]));
         const float s = q8_scale(group_max<G>(amax)), r = 1.0f / s;
@@ -184,7 +164,7 @@ __global__ void __launch_bounds__(256) quant_tiles_vec_kernel(const T *__restric
                                                               const Q8Size z) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
-    constexpr int VEC = Q8Vec<T>::N, G = 128 / VEC, PER = 256 / G, U = 128 / PER;
+    constexpr int VEC = Vec16<T>::N, G = 128 / VEC, PER = 256 / G, U = 128 / PER;
     __shared__ float s_max[8];
     const int tid = threadIdx.x;
     const int64_t nb = (cols + 127) / 128, r0 = blockIdx.x / nb * 128 + tid / G;
@@ -197,7 +177,7 @@ __global__ void __launch_bounds__(256) quant_tiles_vec_kernel(const T *__restric
                                                : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        Q8Vec<T>::unpack(v[u], f);
+        Vec16<T>::unpack(v[u], f);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fabsf(f[e]));
     }
@@ -210,7 +190,7 @@ __global__ void __launch_bounds__(256) quant_tiles_vec_kernel(const T *__restric
     const float s = q8_scale(amax), r = 1.0f / s;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        Q8Vec<T>::unpack(v[u], f);
+        Vec16<T>::unpack(v[u], f);
         divide<VEC>(f, s, r);
         if (r0 + u * PER < rows && c < cols) put8<VEC>(out, (r0 + u * PER) * cols + c, f, z);
     }
@@ -274,7 +254,7 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_vec_kernel(const T *__restr
     sm100::pdl_trigger();
     sm100::pdl_wait();
     using AT = typename AccT<T>::type;
-    constexpr int VEC = Q8Vec<T>::N, G = 128 / VEC, PER = 256 / G, U = 4;
+    constexpr int VEC = Vec16<T>::N, G = 128 / VEC, PER = 256 / G, U = 4;
     const int lane = threadIdx.x & (G - 1);
     const int64_t units = N * nb, u0 = (int64_t)blockIdx.x * (PER * U) + threadIdx.x / G;
     uint4 ov[U], gv[U];
@@ -298,8 +278,8 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_vec_kernel(const T *__restr
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         float f[VEC], t[VEC];
-        Q8Vec<T>::unpack(ov[u], f);
-        Q8Vec<T>::unpack(gv[u], t);
+        Vec16<T>::unpack(ov[u], f);
+        Vec16<T>::unpack(gv[u], t);
         AT ss = 0;
         float amax = 0.f;
 #pragma unroll
@@ -331,7 +311,7 @@ __global__ void __launch_bounds__(NT) norm_gate_fp8_row_kernel(const T *__restri
     sm100::pdl_trigger();
     sm100::pdl_wait();
     using AT = typename AccT<T>::type;
-    constexpr int VEC = Q8Vec<T>::N, G = 128 / VEC;
+    constexpr int VEC = Vec16<T>::N, G = 128 / VEC;
     __shared__ AT s_ss[NT * NG8_V];
     __shared__ float s_inv[NT * NG8_V];  // per vector; per head (a head has one vector at least)
     const int K = H * Dv, nv = K / VEC, per = Dv / VEC, nb = (K + 127) / 128;
@@ -350,7 +330,7 @@ __global__ void __launch_bounds__(NT) norm_gate_fp8_row_kernel(const T *__restri
     for (int u = 0; u < NG8_V; ++u) {
         float f[VEC];
         AT ss = 0;
-        Q8Vec<T>::unpack(ov[u], f);
+        Vec16<T>::unpack(ov[u], f);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) ss += (AT)f[e] * (AT)f[e];
         s_ss[threadIdx.x + NT * u] = ss;
@@ -369,8 +349,8 @@ __global__ void __launch_bounds__(NT) norm_gate_fp8_row_kernel(const T *__restri
         const bool in = i < nv;
         const float inv = in ? s_inv[i / per] : 0.f;
         float f[VEC], t[VEC], amax = 0.f;
-        Q8Vec<T>::unpack(ov[u], f);
-        Q8Vec<T>::unpack(gv[u], t);
+        Vec16<T>::unpack(ov[u], f);
+        Vec16<T>::unpack(gv[u], t);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             f[e] = f[e] * inv * ng8_sigmoid(t[e]);
@@ -428,7 +408,7 @@ __global__ void __launch_bounds__(256) norm_gate_fp8_kernel(const T *__restrict_
 template <typename T>
 cudaError_t ng8_launch(const void *o, const void *gl, int64_t N, int H, int Dv, float eps, void *x8, float *scales,
                        cudaStream_t st) {
-    constexpr int VEC = Q8Vec<T>::N;
+    constexpr int VEC = Vec16<T>::N;
     const int K = H * Dv, nb = (K + 127) / 128;
     const Q8Size z = {checked_size((size_t)N * K), checked_size((size_t)N * nb * 4), checked_counter()};
     // whole 16-byte vectors of one head per lane, whole heads per block, aligned rows
@@ -455,7 +435,7 @@ cudaError_t ng8_launch(const void *o, const void *gl, int64_t N, int H, int Dv, 
 template <typename T>
 cudaError_t launch_quant(const void *x, int64_t rows, int64_t cols, int block_rows, int64_t units, uint8_t *y,
                          float *scales, cudaStream_t st) {
-    constexpr int VEC = Q8Vec<T>::N, PER = 256 / (128 / VEC) * 4;
+    constexpr int VEC = Vec16<T>::N, PER = 256 / (128 / VEC) * 4;
     const Q8Size z = {checked_size((size_t)rows * cols), checked_size((size_t)units * 4), checked_counter()};
     auto go = [&](auto kernel, int64_t ctas) {
         return launch_pdl(kernel, dim3((unsigned)(ctas < 0x7fffffffLL ? ctas : 0x7fffffffLL)), dim3(256), 0, st,

@@ -27,6 +27,39 @@ __device__ __forceinline__ void store_elem(__nv_bfloat16 *p, int64_t i, float v)
     p[i] = __float2bfloat16_rn(v);
 }
 
+// 16 bytes of elements as fp32 values, and back.
+template <typename T> struct Vec16;
+template <> struct Vec16<float> {
+    static constexpr int N = 4;
+    __device__ static void unpack(const uint4 &u, float (&f)[4]) {
+        f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
+        f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+    }
+    __device__ static uint4 pack(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+template <> struct Vec16<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ static void unpack(const uint4 &u, float (&f)[8]) {
+        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(v[i] << 16);
+            f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+        }
+    }
+    __device__ static uint4 pack(const float (&f)[8]) {
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            v[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        return make_uint4(v[0], v[1], v[2], v[3]);
+    }
+};
+
 // Accumulator type of the exact-fp32 kernels: fp32 inputs accumulate their
 // reductions in fp64 so that results stay within 1e-6 absolute / 1e-5 relative
 // of an fp64 evaluation; bf16 inputs accumulate in fp32.

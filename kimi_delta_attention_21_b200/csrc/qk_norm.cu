@@ -66,47 +66,15 @@ __device__ __forceinline__ void qn_angle(int64_t pos, float f, float &c, float &
     sincospif(2.0f * (float)t, &s, &c);
 }
 
-template <typename T> struct QnVec;
-template <> struct QnVec<float> {
-    static constexpr int N = 4;
-    __device__ static void unpack(const uint4 &u, float (&f)[4]) {
-        f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-        f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
-    }
-    __device__ static uint4 pack(const float (&f)[4]) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    }
-};
-template <> struct QnVec<__nv_bfloat16> {
-    static constexpr int N = 8;
-    __device__ static void unpack(const uint4 &u, float (&f)[8]) {
-        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(v[i] << 16);
-            f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-        }
-    }
-    __device__ static uint4 pack(const float (&f)[8]) {
-        uint32_t v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            v[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        return make_uint4(v[0], v[1], v[2], v[3]);
-    }
-};
-
 // VEC consecutive gradient values of type GT
 template <typename GT, int VEC>
 __device__ __forceinline__ void qn_load_grad(const GT *p, float (&f)[VEC]) {
-    constexpr int N = QnVec<GT>::N;
+    constexpr int N = Vec16<GT>::N;
     static_assert(VEC % N == 0, "whole 16-byte vectors");
 #pragma unroll
     for (int i = 0; i < VEC / N; ++i) {
         float t[N];
-        QnVec<GT>::unpack(*reinterpret_cast<const uint4 *>(p + N * i), t);
+        Vec16<GT>::unpack(*reinterpret_cast<const uint4 *>(p + N * i), t);
 #pragma unroll
         for (int e = 0; e < N; ++e) f[N * i + e] = t[e];
     }
@@ -194,7 +162,7 @@ template <typename T, int G, int NV, int ROT>
 __global__ void __launch_bounds__(QN_NT) qk_norm_kernel(const __grid_constant__ QnArgs p) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
-    constexpr int VEC = QnVec<T>::N, U = NV == 1 ? 4 : 2, PER = QN_NT / G;
+    constexpr int VEC = Vec16<T>::N, U = NV == 1 ? 4 : 2, PER = QN_NT / G;
     const QnSide &s = p.side[blockIdx.y];
     const int lane = threadIdx.x & (G - 1);
     const int64_t items = p.tokens * s.chunks;
@@ -233,7 +201,7 @@ __global__ void __launch_bounds__(QN_NT) qk_norm_kernel(const __grid_constant__ 
                 float ss = 0.f;
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    QnVec<T>::unpack(raw[u][v], f[v]);
+                    Vec16<T>::unpack(raw[u][v], f[v]);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) ss = fmaf(f[v][e], f[v][e], ss);
                 }
@@ -255,7 +223,7 @@ __global__ void __launch_bounds__(QN_NT) qk_norm_kernel(const __grid_constant__ 
                         if (in[v])
                             qn_put(p, s.y, s.y_bytes,
                                    reinterpret_cast<uint4 *>(y + (int64_t)(h0 + i + u) * p.D + (lane + G * v) * VEC),
-                                   QnVec<T>::pack(f[v]));
+                                   Vec16<T>::pack(f[v]));
             }
         }
     }
@@ -266,7 +234,7 @@ template <typename T, typename GT, int G, int NV, int ROT>
 __global__ void __launch_bounds__(QN_NT) qk_norm_bwd_kernel(const __grid_constant__ QnArgs p) {
     sm100::pdl_trigger();
     sm100::pdl_wait();
-    constexpr int VEC = QnVec<T>::N, U = NV == 1 ? 2 : 1, PER = QN_NT / G;
+    constexpr int VEC = Vec16<T>::N, U = NV == 1 ? 2 : 1, PER = QN_NT / G;
     __shared__ float s_dw[PER][G * NV * VEC];
     const QnSide &s = p.side[blockIdx.y];
     const int lane = threadIdx.x & (G - 1);
@@ -324,7 +292,7 @@ __global__ void __launch_bounds__(QN_NT) qk_norm_bwd_kernel(const __grid_constan
                 float ss = 0.f, hx = 0.f;
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    QnVec<T>::unpack(raw[u][v], f[v]);
+                    Vec16<T>::unpack(raw[u][v], f[v]);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
                         ss = fmaf(f[v][e], f[v][e], ss);
@@ -348,7 +316,7 @@ __global__ void __launch_bounds__(QN_NT) qk_norm_bwd_kernel(const __grid_constan
                             qn_put(p, s.y, s.y_bytes,
                                    reinterpret_cast<uint4 *>((T *)s.y + row + (int64_t)(h0 + i + u) * p.D +
                                                              (lane + G * v) * VEC),
-                                   QnVec<T>::pack(f[v]));
+                                   Vec16<T>::pack(f[v]));
             }
         }
     }
@@ -565,7 +533,7 @@ cudaError_t qn_launch_rot(const QnArgs &p, int rot, bool bwd, dim3 grid, cudaStr
 template <typename T, typename GT>
 kda_status_t qn_launch(const kda_qk_norm_args &a, QnArgs p, bool vector, bool bwd, unsigned max_ctas, unsigned *ctas,
                        cudaStream_t st) {
-    constexpr int VEC = QnVec<T>::N;
+    constexpr int VEC = Vec16<T>::N;
     const int rot = !a.rot_dim ? ROT_NONE : a.interleaved ? ROT_INTERLEAVED : ROT_HALF;
     const int sms = sm_count();
     cudaError_t e;
