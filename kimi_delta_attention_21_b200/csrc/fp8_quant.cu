@@ -237,9 +237,14 @@ __device__ __forceinline__ float ng8_sigmoid(float x) {
     return x < 0.f ? e * r : r;
 }
 
-// 1 / rms of a head from its sum of squares (fp32 inputs: an fp64 sum), inv_dv = 1 / D_v
-template <typename AT>
-__device__ __forceinline__ float ng8_inv(AT ss, AT inv_dv, float eps) { return rsqrtf((float)(ss * inv_dv + (AT)eps)); }
+// 1 / rms of a head from its sum of squares, inv_dv = 1 / D_v.  fp32 inputs: an fp64 sum, which holds the squares of any of
+// them; the root in fp64 too where the mean is not one of fp32's.
+__device__ __forceinline__ float ng8_inv(float ss, float inv_dv, float eps) { return rsqrtf(fmaf(ss, inv_dv, eps)); }
+__device__ __forceinline__ float ng8_inv(double ss, double inv_dv, float eps) {
+    const double m = fma(ss, inv_dv, (double)eps);
+    const float f = (float)m;
+    return f > 1e-37f && f < 1e38f ? rsqrtf(f) : (float)(1.0 / sqrt(m));
+}
 
 // D_v = 8 (fp32: 4) .. 128, a power of two: a block of 128 channels holds whole heads.  A group of 128 / VEC
 // lanes per block, 16 bytes of o and of the gate per lane; `hl` lanes share a head's norm.  Four blocks per group
