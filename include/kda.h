@@ -422,7 +422,9 @@ kda_status_t kda_out_norm_gate_proj_noalloc(const void *o, const void *gate_logi
  * and, with rot_dim = R > 0, the first R channels of y turned in pairs (a, b)
  * to (a cos t - b sin t, a sin t + b cos t), t = position * inv_freq[j]: pair j
  * is channels (j, j + R/2), or (2j, 2j + 1) with interleaved != 0.  The angle
- * is evaluated in fp64 (exact for positions within +-2^31).
+ * is a product in fp64, reduced there to a fraction of a turn and rounded to
+ * fp32: off by at most 3 * 2^-53 of itself and 2^-26 of a turn (1e-7 radians up
+ * to an angle of 2^25, 8e-7 at 2^31).
  *   q, k          token (b, s) at b * stride_b + s * stride_s elements, its H
  *                 heads of D channels contiguous there: views of the rows of a
  *                 fused projection need no copy.  Strides 0 .. 2^40.

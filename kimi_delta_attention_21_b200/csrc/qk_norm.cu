@@ -15,8 +15,9 @@
 // A group of G lanes holds one row, 16 bytes of input per lane and register vector, so that a warp's
 // loads are whole rows; the pairs of a half-split rotation are 16-byte vectors apart and meet by a
 // shuffle.  A group takes `hc` heads of one token in turn: the token's cosines and sines are computed
-// once for all of them (the sine of an exact angle: pos * f is one fp64 product, reduced to a fraction
-// of a turn in fp64 before the fp32 sine, so that far positions lose nothing).
+// once for all of them.  pos * f is an fp64 product, reduced to a fraction of a turn in fp64 before the fp32
+// sine: the roundings of pos * f, of 1 / 2 pi and of their product are 3 * 2^-53 of the angle (7e-7 radians at
+// 2^31), the fraction's in fp32 2^-26 of a turn.
 #include "host_check.cuh"
 #include "kda_internal.cuh"
 #include "sm100_ptx.cuh"
