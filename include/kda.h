@@ -468,7 +468,8 @@ kda_status_t kda_qk_norm_fwd(const kda_qk_norm_args *args);
  *                 recurrence's backward passes give it) or dtype
  *   dq, dk        dtype, contiguous, out
  *   dq_weight, dk_weight  (D) fp32 out, or NULL to skip: sums over all tokens
- *                 and heads, added in a fixed order (the same bits every run)
+ *                 and heads in fp32, added in a fixed order (the same bits every
+ *                 run)
  *   workspace     256-byte aligned; needed if a weight's gradient is asked for
  *                 (its size depends on the current device's SM count)
  * Without tokens the weights' gradients are zero.
@@ -494,9 +495,10 @@ kda_status_t kda_qk_norm_bwd(const kda_qk_norm_bwd_args *args);
 /*
  * kda_gdn_decode_step - the recurrent form of the gated delta rule (one scalar
  * decay per token and head, as kda_gdn_chunk_fwd): T new tokens of each of B
- * sequences, token by token, exact fp32, the states advanced IN PLACE.  T = 1
- * is a decode step; more tokens are drafted ones or short prompts.  The state
- * is read and written once per call, whatever T is.
+ * sequences, token by token in fp32 (sums too: kda_decode_step's are fp64 for
+ * fp32 inputs), the states advanced IN PLACE.  T = 1 is a decode step; more
+ * tokens are drafted ones or short prompts.  The state is read and written once
+ * per call, whatever T is.
  *   q, k          (B, T, H, D_k)  dtype;   v (B, T, H, D_v)  dtype
  *   z             (B, T, H)  dtype decay logits, alpha = exp(g_min * sigmoid(z)),
  *                 or log_decay (B, T, H) fp32 (clamped to [g_min, 0]) instead
@@ -506,7 +508,9 @@ kda_status_t kda_qk_norm_bwd(const kda_qk_norm_bwd_args *args);
  *                 A negative slot is a padded row: nothing of it is read or
  *                 written, its rows of o stay as they were.  A slot >= num_slots,
  *                 or one that an earlier sequence of the call has, is treated the
- *                 same way and sets *dev_status to KDA_ERR_INVALID_ARG.
+ *                 same way and sets *dev_status to KDA_ERR_INVALID_ARG.  The look
+ *                 for a slot given twice reads B^2 H / 2 slots (a quarter of the
+ *                 call's time at 16384 sequences x 4 heads of 16).
  *   gate_logits   (B, T, H, D_v)  dtype or NULL (as in kda_chunk_fwd), eps
  *   o             (B, T, H, D_v)  dtype, out
  *   dev_status    device int32 that the caller zeroes, or NULL
@@ -567,7 +571,7 @@ kda_status_t kda_quant_fp8(const void *x, kda_dtype_t dtype, int64_t rows, int64
 
 /*
  * kda_norm_gate_fp8 - kda_norm_gate with its result quantised as it is produced
- * (never rounded to dtype in between):
+ * (formed in fp32, fp32 inputs with fp64 sums, never rounded to dtype in between):
  *   o, gate_logits (N, H, D_v) dtype;  x8 (N, H * D_v) e4m3 out
  *   scales (N, ceil(H * D_v / 128)) fp32 out (with D_v = 128: one per head)
  * H and D_v <= 8192.

@@ -8,9 +8,12 @@
 // (sequence, head): lane l of warp w owns the key rows w, w + 8, ... and four value columns, so that a
 // warp reads whole rows; the sums over key rows are partial sums of 8 warps joined in shared memory, one
 // barrier each (the buffers alternate, so the next token's sums need no second one).
+// Sums are fp32 for fp32 inputs too (with fp64 ones, as the per-channel decode step has, four tokens of 33 sequences x 6
+// heads of 96 x 72 take 20 us instead of 11, one token of 256 x 32 heads of 128 in fp32 224 us instead of 173).
 // Measured (bf16, D = 128, 32 heads): 256 sequences 181 us, 6.0 TB/s (91% of a copy's rate; a plain in-place
-// update of as many bytes takes 159 us); with three CTAs on an SM instead of two it spills (233 us), with plain
-// stores instead of streaming ones 218 us.  One sequence: 5 us, the call's own time.
+// update of as many bytes takes 159 us); with three CTAs on an SM instead of two it spills 312 bytes a thread instead
+// of 20 (233 us), with plain stores instead of streaming ones 218 us.  One sequence: 5 us, the call's own time.
+// Every instance spills some (16 to 192 bytes).
 #include "host_check.cuh"
 #include "kda_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -38,7 +41,7 @@ struct GdArgs {
 // VEC: D_v is a multiple of 4 and the state 16-byte aligned; lane l owns columns 4l .. 4l + 3.  Otherwise the columns
 // l, l + 32, l + 64, l + 96.  FULL: D_k = D_v = 128 besides, nothing to mask.
 // RPW: rows per warp, D_k <= 8 RPW; the fewer, the more CTAs on an SM (4096 sequences x 16 heads of 16: 756 us with 16
-// rows, 323 us with 4).
+// rows, 333 us with 4, 397 us with slots; of 64: 650 us with 8, 781 us with slots).  Lanes past D_v / 4 columns are idle.
 template <typename T, bool VEC, bool FULL, int RPW>
 __global__ void __launch_bounds__(256, RPW == 16 ? 2 : RPW == 8 ? 3 : 4) gdn_decode_kernel(const __grid_constant__ GdArgs p) {
     sm100::pdl_trigger();
@@ -97,7 +100,10 @@ __global__ void __launch_bounds__(256, RPW == 16 ? 2 : RPW == 8 ? 3 : 4) gdn_dec
             for (int j = 0; j < 4; ++j) s[i][j] = (c < Dk && col(j) < Dv) ? S[c * Dv + col(j)] : 0.f;
         }
     }
-    if (p.slots) {  // a slot that an earlier sequence of the batch has: two CTAs would race on its state
+    // A slot that an earlier sequence of the batch has: two CTAs would race on its state.  Every CTA looks through the slots
+    // before its own, B^2 H / 2 reads of 4 bytes from the caches in all: 1024 sequences x 32 heads of 128 take 719 us instead
+    // of 674, 16384 x 4 of 16 472 instead of 333, 65536 x 1 of 16 838 instead of 333.
+    if (p.slots) {
         bool twice = false;
         for (int64_t e = tid; e < b; e += 256) twice |= p.slots[e] == (int32_t)slot;
         if (__syncthreads_or(twice)) {

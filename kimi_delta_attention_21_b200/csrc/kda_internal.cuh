@@ -60,9 +60,10 @@ template <> struct Vec16<__nv_bfloat16> {
     }
 };
 
-// Accumulator type of the exact-fp32 kernels: fp32 inputs accumulate their
+// Accumulator type of the exact-fp32 forward kernels: fp32 inputs accumulate their
 // reductions in fp64 so that results stay within 1e-6 absolute / 1e-5 relative
-// of an fp64 evaluation; bf16 inputs accumulate in fp32.
+// of an fp64 evaluation; bf16 inputs accumulate in fp32.  (Not in the backward
+// passes, qk_norm.cu and gdn_decode.cu: their sums are fp32.)
 template <typename T> struct AccT { using type = float; };
 template <> struct AccT<float> { using type = double; };
 

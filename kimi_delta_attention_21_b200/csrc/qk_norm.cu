@@ -10,8 +10,11 @@
 //
 // Both are bound by HBM: a row is read once and written once, every intermediate stays in registers.  Measured (bf16,
 // heads of 128): forward, 4096 tokens x 32 heads, 12 us (10 at the copy rate); backward, 16384 tokens x 64 heads with
-// fp32 gradients, 195 us (164): rows in flight do not bound it (a shared-memory ring of any depth: 241 us), but the
-// row's two sums, and the angles of a token, which cost as much as three rows.
+// fp32 gradients, 198 us (164).  What bounds the backward is not one thing: issue and DRAM are half busy, 128 registers leave
+// 16 warps an SM, whose waits for loads lead the stalls; but more rows in flight were no faster (a shared-memory ring of any
+// depth: 241 us), and the angles of a token cost as much as three rows (without rotation 187 us).  Heads of no whole vectors,
+// or rotated halves of none, take the kernel of a warp per row: 4096 tokens x 32 heads of 80 with R = 40, 52 us (6.4), backward
+// of 16384 x 64 such heads 712 us (102).
 // A group of G lanes holds one row, 16 bytes of input per lane and register vector, so that a warp's
 // loads are whole rows; the pairs of a half-split rotation are 16-byte vectors apart and meet by a
 // shuffle.  A group takes `hc` heads of one token in turn: the token's cosines and sines are computed
