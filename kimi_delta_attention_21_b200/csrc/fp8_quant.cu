@@ -3,9 +3,10 @@
 //   scale = max(amax / 448, 2^-126) over the block (1 for a block of zeros),  value = rn_e4m3(x / scale).
 // The scale maps the block's largest magnitude to e4m3's largest, so nothing saturates.
 //
-// All are bound by HBM: each input is read once, the values leave as 1 byte each.  Measured: norm and gate, 8192 rows x
-// 32 heads of 128 in bf16, 40 us (26 at the copy rate; what it issues takes the SMs longer than the bytes); 65536 x 4096
-// values 146 us (123), a 4096 x 4096 weight 13 us.
+// Each input is read once, the values leave as 1 byte each.  The quantisers are bound by HBM: 65536 x 4096 bf16 values
+// 146 us (123 at the copy rate), a 4096 x 4096 weight 13 us (8; its blocks are held in registers, two CTAs an SM).  Norm
+// and gate are bound by what a channel issues (85% of the issue slots): 8192 rows x 32 heads of 128 in bf16 40 us (26),
+// in fp32 66 us (46).
 #include <cuda_fp8.h>
 
 #include "host_check.cuh"
